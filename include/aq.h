@@ -1,6 +1,6 @@
 /*
- * libaq -- group-wise INT4 (W4A16) weight quantization, AWQ calibration and an
- * FP4 decode path for AMD Instinct MI355X (gfx950).  C ABI.
+ * libaq -- group-wise INT4 (W4A16) weight quantization, AWQ calibration, an FP4
+ * decode path and MXFP4 products for AMD Instinct MI355X (gfx950).  C ABI.
  *
  * Conventions shared by every entry point
  *   - Tensor arguments are DEVICE pointers owned by the caller (the library
@@ -319,6 +319,78 @@ size_t aq_fp4_quantize_workspace(int64_t N, int64_t K);
 aq_status aq_fp4_quantize(const void* W, int32_t w_dtype, int64_t N, int64_t K, uint8_t* codes,
                           uint8_t* block_scales, float* tensor_scale, void* workspace, size_t workspace_bytes,
                           void* stream);
+
+/*
+ * MXFP4: blocks of 32 consecutive k of a row share one E8M0 byte s, the factor
+ * 2^(s - 127) (s = 255: NaN); every element is an E2M1 code (the magnitudes and the
+ * code layout of aq_fp4_gemm).  The microscaling formats of the Open Compute Project
+ * define the format; there is no tensor scale, and the matrix cores of gfx950 take codes
+ * and scale bytes as they are.
+ *   codes [M, K/2] uint8 (k even in the low nibble), scales [M, K/32] uint8.
+ *
+ * aq_mxfp4_quantize: for each block with a = max |x|
+ *   e = max(floor(log2 a) - 2, -127) (-127 when a = 0),  s = e + 127,
+ *   code = nearest E2M1 of x 2^-e, ties to the even code, at most 6; the sign bit is set
+ *   for negative x with a non-zero magnitude.  A block that holds a NaN or an infinity
+ *   gets s = 255 and codes 0 (the one entry point group whose inputs need not be finite).
+ * Every step but the rounding to E2M1 is exact.
+ * X [M, K] fp32 or bf16 (x_dtype), rows ldx elements apart (ldx >= K, a multiple of 16
+ * bytes; K for a dense matrix), device; codes and scales dense.
+ * aq_mxfp4_dequantize: Y [M, K] (fp32 or bf16, exact in both) = e2m1(code) 2^(s - 127).
+ * Errors: EINVAL for a bad dtype, M < 0, K <= 0 or K % 32, ldx < K or rows that are not 16
+ *         bytes aligned, M or K >= 2^30, M * K >= 2^36, NULL / misaligned pointers (X, Y,
+ *         codes 16 bytes).
+ */
+aq_status aq_mxfp4_quantize(const void* X, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* codes,
+                            uint8_t* scales, void* stream);
+aq_status aq_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* Y,
+                              int32_t y_dtype, void* stream);
+
+/*
+ * Products with MXFP4 weights, any M >= 0:
+ *   aq_mxfp4_gemm     Y[m, n] = sum_k X[m, k] e2m1(c[n, k]) 2^(s[n, k/32] - 127)
+ *                     (X bf16: the activations keep their 16 bits)
+ *   aq_mxfp4_gemm_a4  the same with X [M, K] given in MXFP4 (x_codes, x_scales, as
+ *                     aq_mxfp4_quantize writes them), on the block-scaled matrix
+ *                     instructions
+ * fp32 sums; Y [M, N] is fp32, or bf16 rounded once to nearest even (y_dtype).
+ * X [M, K] bf16, rows ldx elements apart (ldx >= K, a multiple of 8); codes [N, K/2],
+ * scales [N, K/32].  aq_mxfp4_gemm forms each weight in bf16, so scale bytes of 253 and
+ * above (factors over 2^125, which the quantiser does not write) may overflow.
+ * Sums run in a fixed order: a call gives the same bits every time, and a row's outputs
+ * do not depend on the other rows' values.
+ * Errors: EINVAL for a bad y_dtype, M < 0 or M >= 2^30, N < 0 or N >= 2^22, K <= 0, K >=
+ *         2^22 or K % 32, ldx < K or ldx % 8, NULL / misaligned pointers (X, codes 16
+ *         bytes; Y two elements).
+ */
+aq_status aq_mxfp4_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
+                        const uint8_t* scales, int64_t N, void* Y, int32_t y_dtype, void* stream);
+aq_status aq_mxfp4_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, int64_t K,
+                           const uint8_t* codes, const uint8_t* scales, int64_t N, void* Y, int32_t y_dtype,
+                           void* stream);
+
+/*
+ * The same products grouped by expert (mixture of experts): E weight matrices codes
+ * [E, N, K/2], scales [E, N, K/32]; row r of Y [M, N] with offsets[e] <= r < offsets[e + 1]
+ * is activation row rows[r] (r itself when rows is NULL) times expert e's weights.
+ *
+ * offsets [E + 1] int32, ascending, within 0 .. M; rows [M] int32 within 0 .. T - 1 or
+ * NULL (then T >= M); X [T, K].  Both lists are read on the device at the time the call
+ * runs, so a captured call follows their contents.  An expert may have no rows.  Rows of Y
+ * outside offsets[0] .. offsets[E] - 1 are left as they were.  A list entry outside its
+ * range never leads outside the buffers: offsets are clamped to 0 .. M and to be
+ * ascending, a row of Y whose rows[r] is outside X becomes NaN.
+ * Errors: as the products above; EINVAL also for E <= 0, E * N >= 2^27, M * N >= 2^38,
+ *         T < 0 or T >= 2^30, T < M without rows, T = 0 with M > 0, NULL / misaligned
+ *         offsets or rows (4 bytes).
+ */
+aq_status aq_mxfp4_grouped_gemm(const uint16_t* X, int64_t T, int64_t K, int64_t ldx, const uint8_t* codes,
+                                const uint8_t* scales, int64_t E, int64_t N, const int32_t* offsets,
+                                const int32_t* rows, int64_t M, void* Y, int32_t y_dtype, void* stream);
+aq_status aq_mxfp4_grouped_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t K,
+                                   const uint8_t* codes, const uint8_t* scales, int64_t E, int64_t N,
+                                   const int32_t* offsets, const int32_t* rows, int64_t M, void* Y, int32_t y_dtype,
+                                   void* stream);
 
 /* Thread-local text for the last non-OK status of this thread ("" if none). */
 const char* aq_last_error(void);

@@ -1,0 +1,488 @@
+"""MXFP4 on the GPU against the 64-bit oracle.
+
+Quantising and reading back are exact up to the one rounding, so they are compared bit for bit.  Products:
+inputs whose sums fit 24 bits are compared for equality; for others a sum of K terms in fp32, in any order and
+with each addition rounded or cut (a relative 2^-23 at most), is off by at most K 2^-23 sum |x w|, and the
+rounding to bf16 adds at most 2^-8 of the value.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mxfp4 as O
+from tests.gpu_util import dev, host, step
+from weight_only_bit_group_amd import synth
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu(lib):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def B():
+    from weight_only_bit_group_amd import binding
+    return binding
+
+
+def _np(t):
+    """A tensor's values as fp64 (exact)."""
+    return host(t.double())
+
+
+def _weights(rng, *lead, k, lo=120, hi=134):
+    return (rng.integers(0, 256, (*lead, k // 2), dtype=np.uint8),
+            rng.integers(lo, hi, (*lead, k // 32)).astype(np.uint8))
+
+
+def _close(y, ref, mag, k, what):
+    tol = k * 2.0 ** -23 * mag
+    if y.dtype == BF16:
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    err = np.abs(_np(y) - ref)
+    print(f"[gpu] {what}: worst share of the bound {np.max(err / (tol + 1e-300)):.3f}", flush=True)
+    assert (err <= tol).all(), what
+
+
+# ---- quantising ------------------------------------------------------------------------------------
+
+SPECIAL = [0.0, -0.0, .25, -.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, -7.5, 8.0, 2.0 ** -126, -2.0 ** -128,
+           3.0 * 2.0 ** -133, 1e-38, 3e38, -3.38e38, 1.0, 2.0 ** -100, 6 * 2.0 ** -127]
+
+
+def _quant_input(rng, m, k):
+    x = rng.standard_normal((m, k)) * np.exp(rng.standard_normal((m, k // 32)).repeat(32, 1) * 20)
+    x = np.clip(x, -3e38, 3e38)
+    flat = x.reshape(-1)
+    for i, v in enumerate(SPECIAL):
+        if 32 * i + 32 <= flat.size // 2:
+            flat[32 * i:32 * i + 32] = 0
+            flat[32 * i + (5 * i) % 32] = v
+            if i % 2:
+                flat[32 * i + (5 * i + 7) % 32] = v / 3
+    if m * k >= 4096:
+        flat[-3], flat[-70], flat[-100] = np.nan, np.inf, -np.inf
+    return x
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,k", [(1, 32), (3, 64), (1, 2048), (17, 96), (33, 2080), (129, 4096), (5, 14336)])
+def test_quantize_is_exact(m, k, dtype):
+    x = torch.from_numpy(_quant_input(np.random.default_rng(m * 7 + k), m, k)).to(dtype).cuda()
+    step(f"aq_mxfp4_quantize {m}x{k} {dtype}")
+    c, s = B().aq_mxfp4_quantize(x)
+    c0, s0 = O.quantize(_np(x))
+    assert np.array_equal(host(s), s0)
+    assert np.array_equal(host(c), c0)
+
+
+def test_quantize_every_bf16_value():
+    """Each finite bf16 value alone in its block, and under a maximum that fixes the factor at 1."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF16)
+    alone = torch.zeros(65536, 32, dtype=BF16)
+    alone[:, 9] = bits
+    under = alone.clone()
+    under[:, 30] = 6.0
+    for name, x in (("alone", alone), ("under 6", under)):
+        step(f"aq_mxfp4_quantize every bf16 value {name}")
+        c, s = B().aq_mxfp4_quantize(x.cuda())
+        c0, s0 = O.quantize(x.double().numpy())
+        assert np.array_equal(host(s), s0) and np.array_equal(host(c), c0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_quantize_strided_rows(dtype):
+    wide = torch.randn(37, 512, device="cuda").to(dtype)
+    x = wide[:, 64:64 + 160]
+    step("aq_mxfp4_quantize strided rows")
+    c, s = B().aq_mxfp4_quantize(x)
+    c0, s0 = O.quantize(_np(x.contiguous()))
+    assert np.array_equal(host(c), c0) and np.array_equal(host(s), s0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_dequantize_every_code_and_factor(dtype):
+    c = np.zeros((256, 256 * 16), np.uint8)
+    c[:, ::16] = np.arange(256)          # code byte j in block j of every row
+    c[:, 7::16] = np.arange(256)[::-1]
+    s = np.repeat(np.arange(256, dtype=np.uint8)[:, None], 256, 1)
+    step(f"aq_mxfp4_dequantize {dtype}")
+    y = _np(B().aq_mxfp4_dequantize(dev(c), dev(s), out_dtype=dtype))
+    with np.errstate(over="ignore"):
+        ref = torch.from_numpy(O.dequantize(c, s)).to(dtype).double().numpy()   # 6 * 2^127 is infinite
+    assert np.array_equal(y, ref, equal_nan=True)
+
+
+def test_round_trip_through_outputs_given():
+    x = torch.randn(64, 256, device="cuda")
+    c, s = torch.empty(64, 128, dtype=torch.uint8, device="cuda"), torch.empty(64, 8, dtype=torch.uint8, device="cuda")
+    out = torch.empty(64, 256, dtype=BF16, device="cuda")
+    step("aq_mxfp4 round trip into given outputs")
+    got = B().aq_mxfp4_dequantize(*B().aq_mxfp4_quantize(x, codes=c, scales=s), out=out)
+    assert got is out
+    assert np.array_equal(_np(out), O.dequantize(*O.quantize(_np(x))))
+
+
+# ---- products --------------------------------------------------------------------------------------
+
+def _act(rng, m, k, a4, integers):
+    """(arguments of the call, the activations' fp64 values)."""
+    if a4:
+        c, s = _weights(rng, m, k=k, lo=126, hi=129) if integers else _weights(rng, m, k=k)
+        return (dev(c), dev(s)), O.dequantize(c, s)
+    if integers:
+        x = rng.integers(-8, 9, (m, k)).astype(np.float32)
+        return (torch.from_numpy(x).to(BF16).cuda(),), x.astype(np.float64)
+    x = torch.from_numpy(rng.standard_normal((m, k)) * np.where(rng.random(k) < 0.02, 20, 1)).to(BF16)
+    return (x.cuda(),), x.double().numpy()
+
+
+def _gemm(a4):
+    return B().aq_mxfp4_gemm_a4 if a4 else B().aq_mxfp4_gemm
+
+
+def _grouped(a4):
+    return B().aq_mxfp4_grouped_gemm_a4 if a4 else B().aq_mxfp4_grouped_gemm
+
+
+def _guarded(m, n, dtype):
+    """An output inside a larger buffer of a known pattern, and the buffer."""
+    whole = torch.full((m * n + 512,), 77.0, dtype=dtype, device="cuda")
+    return whole[256:256 + m * n].view(m, n), whole
+
+
+def _untouched(whole, n):
+    return bool((whole[:256] == 77).all()) and bool((whole[256 + n:] == 77).all())
+
+
+SIZES = [(1, 1, 32), (1, 16, 64), (1, 17, 96), (2, 250, 128), (3, 33, 160), (16, 48, 512), (15, 100, 544), (17, 64, 480),
+         (31, 65, 1024), (32, 127, 1056), (33, 200, 2048), (48, 130, 2080), (64, 96, 4128), (65, 128, 256), (64, 129, 288),
+         (100, 255, 992), (128, 257, 544), (129, 256, 64), (256, 384, 512), (257, 300, 1056), (300, 513, 96),
+         (513, 256, 2048), (700, 1003, 736)]
+
+
+@pytest.mark.parametrize("a4", [False, True])
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_product_of_integers_is_exact(m, n, k, a4):
+    """Sums of multiples of 1/16 below 2^20: every order of additions is exact."""
+    rng = np.random.default_rng(m * 31 + n * 7 + k)
+    c, s = _weights(rng, n, k=k, lo=126, hi=129)
+    x, xv = _act(rng, m, k, a4, True)
+    ref = O.forward(xv, c, s)
+    for dtype in (F32, BF16):
+        out, whole = _guarded(m, n, dtype)
+        step(f"mxfp4 gemm a4={a4} {m}x{n}x{k} {dtype}")
+        y = _gemm(a4)(*x, dev(c), dev(s), out=out)
+        want = torch.from_numpy(ref).to(F32).to(dtype).double().numpy()
+        assert np.array_equal(_np(y), want)
+        assert _untouched(whole, m * n)
+
+
+@pytest.mark.parametrize("a4", [False, True])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 2048), (16, 64, 14336), (37, 130, 4096), (64, 100, 2080), (200, 300, 1024),
+                                   (600, 520, 1568)])
+def test_product_of_real_values(m, n, k, a4):
+    rng = np.random.default_rng(k + m)
+    w = synth_weight(rng, n, k)
+    c, s = O.quantize(w)
+    x, xv = _act(rng, m, k, False, False)
+    if a4:
+        x = B().aq_mxfp4_quantize(*x)
+        xv = O.dequantize(*O.quantize(xv))
+    ref = O.forward(xv, c, s)
+    mag = np.abs(xv) @ np.abs(O.dequantize(c, s)).T
+    for dtype in (F32, BF16):
+        step(f"mxfp4 gemm real a4={a4} {m}x{n}x{k} {dtype}")
+        y = _gemm(a4)(*x, dev(c), dev(s), out_dtype=dtype)
+        assert y.dtype == dtype
+        _close(y, ref, mag, k, f"gemm a4={a4} {m}x{n}x{k} {dtype}")
+
+
+def synth_weight(rng, n, k):
+    w = rng.standard_normal((n, k)) * 0.02 * np.where(rng.random((n, k)) < 0.001, 10, 1)
+    return w.astype(np.float32)
+
+
+@pytest.mark.parametrize("a4", [False, True])
+@pytest.mark.parametrize("m", [3, 40, 200, 300])
+def test_far_apart_factors(m, a4):
+    """Factors from 2^-120 to 2^110 in one matrix; a weight or activation factor that is NaN."""
+    n, k = 70, 576
+    rng = np.random.default_rng(m)
+    c, s = _weights(rng, n, k=k, lo=7, hi=60)
+    s[::3] += 150
+    x, xv = _act(rng, m, k, a4, True)
+    step(f"mxfp4 far factors a4={a4} m={m}")
+    y = _gemm(a4)(*x, dev(c), dev(s))
+    ref = O.forward(xv, c, s)
+    mag = np.abs(xv) @ np.abs(O.dequantize(c, s)).T
+    # products below fp32's smallest normal value may be lost: K of them at most
+    assert (np.abs(_np(y) - ref) <= k * 2.0 ** -23 * mag + k * 2.0 ** -126).all()
+    s2 = s.copy()
+    s2[5, 17] = 255
+    s2[9, 0] = 255
+    y2 = _np(_gemm(a4)(*x, dev(c), dev(s2)))
+    bad = np.zeros(n, bool)
+    bad[[5, 9]] = True
+    assert np.isnan(y2[:, bad]).all() and np.array_equal(y2[:, ~bad], _np(y)[:, ~bad])
+    if a4:
+        xs = host(x[1]).copy()
+        xs[m - 1, 17] = 255
+        y3 = _np(_gemm(a4)(x[0], dev(xs), dev(c), dev(s)))
+        assert np.isnan(y3[m - 1]).all() and np.array_equal(y3[:m - 1], _np(y)[:m - 1])
+
+
+@pytest.mark.parametrize("m", [1, 16, 50, 100, 400])
+def test_gemm_strided_rows_and_determinism(m):
+    rng = np.random.default_rng(m)
+    c, s = _weights(rng, 96, k=288)
+    wide = torch.randn(m, 1024, device="cuda").to(BF16)
+    x = wide[:, 8:8 + 288]
+    step(f"mxfp4 gemm strided m={m}")
+    a = B().aq_mxfp4_gemm(x, dev(c), dev(s))
+    b = B().aq_mxfp4_gemm(x.contiguous(), dev(c), dev(s))
+    assert torch.equal(a, b)
+    assert all(torch.equal(a, B().aq_mxfp4_gemm(x, dev(c), dev(s))) for _ in range(3))
+
+
+def test_infinite_activations_reach_their_rows_only():
+    """x = inf in the last k of a row whose K ends inside a tile: that row alone is not finite."""
+    for m in (2, 40, 130, 300):
+        rng = np.random.default_rng(m)
+        c, s = _weights(rng, 40, k=96)
+        c |= 0x11                                # no zero weights
+        x = torch.ones(m, 96, dtype=BF16, device="cuda")
+        x[1, 95] = float("inf")
+        step(f"mxfp4 gemm infinite activation m={m}")
+        y = host(B().aq_mxfp4_gemm(x, dev(c), dev(s)))
+        assert np.isinf(y[1]).all() and np.isfinite(np.delete(y, 1, 0)).all()
+
+
+# ---- grouped by expert -----------------------------------------------------------------------------
+
+COUNTS = {
+    "even": [3, 3, 3, 3],
+    "one token": [0, 1, 0, 0, 1, 0, 1],
+    "ragged": [0, 5, 70, 1, 0, 33, 16, 0],
+    "one expert has all": [0, 0, 150, 0],
+    "many": [(i * 7) % 5 for i in range(150)],
+    "large": [300, 0, 513, 17, 130, 256],
+    "skewed": [700, 1, 0, 2, 1, 0, 3, 0],
+}
+
+
+@pytest.mark.parametrize("a4", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("name", list(COUNTS))
+def test_grouped_of_integers_is_exact(name, gather, a4):
+    counts = COUNTS[name]
+    e, m = len(counts), sum(counts)
+    n, k = (130, 160) if m > 400 else (67, 544)
+    rng = np.random.default_rng(len(name) + 2 * gather + a4)
+    c, s = _weights(rng, e, n, k=k, lo=126, hi=129)
+    t = 23 if gather else m
+    rows = rng.integers(0, t, m).astype(np.int32) if gather else None
+    x, xv = _act(rng, t, k, a4, True)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    ref = O.grouped_forward(xv, c, s, off, rows)
+    for dtype in (F32, BF16):
+        out, whole = _guarded(m, n, dtype)
+        step(f"mxfp4 grouped {name} gather={gather} a4={a4} {dtype}")
+        y = _grouped(a4)(*x, dev(c), dev(s), dev(off), rows=None if rows is None else dev(rows), out=out)
+        want = torch.from_numpy(ref).to(F32).to(dtype).double().numpy()
+        assert np.array_equal(_np(y), want)
+        assert _untouched(whole, m * n)
+
+
+@pytest.mark.parametrize("a4", [False, True])
+@pytest.mark.parametrize("m", [12, 90, 900])
+def test_grouped_rows_outside_and_lists_out_of_range(m, a4):
+    """Rows before the first and behind the last offset stay as they were; a listed row outside X gives NaN in its
+    row only; offsets outside 0 .. M are cut to it."""
+    rng = np.random.default_rng(m)
+    e, n, k, t = 3, 50, 96, 9
+    c, s = _weights(rng, e, n, k=k, lo=126, hi=129)
+    x, xv = _act(rng, t, k, a4, True)
+    rows = rng.integers(0, t, m).astype(np.int32)
+    off = np.array([2, m // 3, m // 3, m - 3], np.int32)
+    ref = O.grouped_forward(xv, c, s, off, rows)
+    out = torch.full((m, n), 7.0, device="cuda")
+    step(f"mxfp4 grouped partial rows m={m} a4={a4}")
+    y = _np(_grouped(a4)(*x, dev(c), dev(s), dev(off), rows=dev(rows), out=out))
+    own = np.zeros(m, bool)
+    own[2:m - 3] = True
+    assert np.array_equal(y[own], ref[own]) and (y[~own] == 7).all()
+    bad = rows.copy()
+    bad[3], bad[m - 5] = -1, t
+    y = _np(_grouped(a4)(*x, dev(c), dev(s), dev(off), rows=dev(bad), out=out.fill_(7.0)))
+    lost = np.zeros(m, bool)
+    lost[[3, m - 5]] = True
+    assert np.isnan(y[lost]).all() and np.array_equal(y[own & ~lost], ref[own & ~lost]) and (y[~own] == 7).all()
+    wild = np.array([-5, m // 3, m // 3, m + 100], np.int32)
+    ref = O.grouped_forward(xv, c, s, np.clip(wild, 0, m), rows)
+    y = _np(_grouped(a4)(*x, dev(c), dev(s), dev(wild), rows=dev(rows)))
+    assert np.array_equal(y, ref)
+
+
+def test_grouped_with_one_expert_is_the_product():
+    rng = np.random.default_rng(5)
+    for m in (7, 50, 200, 400):
+        c, s = _weights(rng, 1, 80, k=320)
+        x, _ = _act(rng, m, 320, False, False)
+        step(f"mxfp4 grouped, one expert, m={m}")
+        off = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+        assert torch.equal(B().aq_mxfp4_grouped_gemm(*x, dev(c), dev(s), off), B().aq_mxfp4_gemm(*x, dev(c[0]), dev(s[0])))
+
+
+# ---- as a program uses them ------------------------------------------------------------------------
+
+def test_graph_replays_follow_the_lists():
+    """A captured quantise + grouped product, replayed with other activations and other routings."""
+    rng = np.random.default_rng(8)
+    e, n, k, m, t = 5, 64, 256, 40, 16
+    c, s = _weights(rng, e, n, k=k, lo=126, hi=129)
+    cd, sd = dev(c), dev(s)
+    x = torch.zeros(t, k, dtype=BF16, device="cuda")
+    off = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
+    rows = torch.zeros(m, dtype=torch.int32, device="cuda")
+    out, out16 = torch.empty(m, n, device="cuda"), torch.empty(m, n, device="cuda")
+    xc = torch.empty(t, k // 2, dtype=torch.uint8, device="cuda")
+    xs = torch.empty(t, k // 32, dtype=torch.uint8, device="cuda")
+
+    def work():
+        B().aq_mxfp4_quantize(x, codes=xc, scales=xs)
+        B().aq_mxfp4_grouped_gemm_a4(xc, xs, cd, sd, off, rows=rows, out=out)
+        B().aq_mxfp4_grouped_gemm(x, cd, sd, off, rows=rows, out=out16)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for i in range(4):
+        step(f"mxfp4 graph replay {i}")
+        x.copy_(torch.from_numpy(rng.integers(-4, 5, (t, k)).astype(np.float32)))
+        cut = np.sort(rng.integers(0, m + 1, e - 1))
+        off.copy_(torch.from_numpy(np.concatenate([[0], cut, [m]]).astype(np.int32)))
+        rows.copy_(torch.from_numpy(rng.integers(0, t, m).astype(np.int32)))
+        torch.cuda.synchronize()
+        graph.replay()
+        got, got16 = out.clone(), out16.clone()
+        work()
+        assert torch.equal(got, out) and torch.equal(got16, out16)
+        xv = _np(x)
+        assert np.array_equal(_np(got16), O.grouped_forward(xv, c, s, host(off), host(rows)))
+        assert np.array_equal(_np(got), O.grouped_forward(O.dequantize(*O.quantize(xv)), c, s, host(off), host(rows)))
+
+
+def test_two_streams_at_once():
+    rng = np.random.default_rng(9)
+    c, s = _weights(rng, 300, k=1024)
+    cd, sd = dev(c), dev(s)
+    xs = [torch.randn(m, 1024, device="cuda").to(BF16) for m in (4, 300)]
+    want = [B().aq_mxfp4_gemm(x, cd, sd) for x in xs]
+    want4 = [B().aq_mxfp4_gemm_a4(*B().aq_mxfp4_quantize(x), cd, sd) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    step("mxfp4 products on two streams")
+    got, got4 = [None, None], [None, None]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = B().aq_mxfp4_gemm(xs[i], cd, sd)
+                got4[i] = B().aq_mxfp4_gemm_a4(*B().aq_mxfp4_quantize(xs[i]), cd, sd)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got + got4, want + want4))
+
+
+def test_empty_inputs():
+    c, s = torch.zeros(2, 8, 32, dtype=torch.uint8, device="cuda"), torch.zeros(2, 8, 2, dtype=torch.uint8, device="cuda")
+    x = torch.zeros(0, 64, dtype=BF16, device="cuda")
+    xc, xs = B().aq_mxfp4_quantize(x)
+    assert xc.shape == (0, 32) and xs.shape == (0, 2)
+    assert B().aq_mxfp4_dequantize(xc, xs).shape == (0, 64)
+    assert B().aq_mxfp4_gemm(x, c[0], s[0]).shape == (0, 8)
+    assert B().aq_mxfp4_gemm_a4(xc, xs, c[0], s[0]).shape == (0, 8)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert B().aq_mxfp4_grouped_gemm(x, c, s, off).shape == (0, 8)
+    # no expert has a row: the output keeps what it held
+    out = torch.full((5, 8), 3.0, device="cuda")
+    step("mxfp4 grouped, no expert has rows")
+    B().aq_mxfp4_grouped_gemm(torch.ones(5, 64, dtype=BF16, device="cuda"), c, s, off, out=out)
+    assert bool((out == 3).all())
+
+
+def test_offsets_beyond_32_bits():
+    """Weights of more than 2^32 bytes (the last expert counts) and outputs of more than 2^31 elements."""
+    e, n, k = 34, 16384, 16384
+    codes = torch.zeros(e, n, k // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.full((e, n, k // 32), 127, dtype=torch.uint8, device="cuda")
+    codes[-1] = 0x22                                   # all ones
+    codes[-1, -1] = 0x44                               # twos in the last row
+    assert codes.numel() > 2 ** 32
+    for m in (2, 40 * e, 300 * e):
+        off = torch.full((e + 1,), 0, dtype=torch.int32, device="cuda")
+        off[-1] = m
+        x = torch.ones(4, k, dtype=BF16, device="cuda")
+        rows = torch.zeros(m, dtype=torch.int32, device="cuda")
+        step(f"mxfp4 grouped, large weights, m={m}")
+        y = B().aq_mxfp4_grouped_gemm(x, codes, scales, off, rows=rows, out_dtype=F32)
+        y4 = B().aq_mxfp4_grouped_gemm_a4(*B().aq_mxfp4_quantize(x), codes, scales, off, rows=rows, out_dtype=F32)
+        for t in (y, y4):
+            assert bool((t[:, :-1] == k).all()) and bool((t[:, -1] == 2 * k).all())
+    del codes, scales
+    m, n, k = 270000, 8192, 32
+    assert m * n > 2 ** 31
+    x = torch.ones(m, k, dtype=BF16, device="cuda")
+    x[-1] = 2
+    c, s = torch.full((n, 16), 0x22, dtype=torch.uint8, device="cuda"), torch.full((n, 1), 127, dtype=torch.uint8, device="cuda")
+    step("mxfp4 gemm, large output")
+    for y in (B().aq_mxfp4_gemm(x, c, s, out_dtype=BF16), B().aq_mxfp4_gemm_a4(*B().aq_mxfp4_quantize(x), c, s, out_dtype=BF16)):
+        assert bool((y[:-1] == 32).all()) and bool((y[-1] == 64).all())
+        del y
+
+
+def test_binding_refusals():
+    b = B()
+    x = torch.zeros(4, 64, dtype=BF16, device="cuda")
+    c, s = torch.zeros(8, 32, dtype=torch.uint8, device="cuda"), torch.zeros(8, 2, dtype=torch.uint8, device="cuda")
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: b.aq_mxfp4_quantize(x[:, ::2]),                       # columns strided
+        lambda: b.aq_mxfp4_quantize(x[:, :48]),                       # K % 32
+        lambda: b.aq_mxfp4_quantize(x.half()),
+        lambda: b.aq_mxfp4_quantize(x[0]),
+        lambda: b.aq_mxfp4_quantize(x.expand(4, 64)[:1].expand(4, 64)),   # rows that overlap
+        lambda: b.aq_mxfp4_quantize(torch.zeros(4, 66, dtype=BF16, device="cuda")[:, :64]),   # rows not 16-byte aligned
+        lambda: b.aq_mxfp4_quantize(torch.zeros(4, 72, dtype=BF16, device="cuda")[:, 4:68]),  # start not aligned
+        lambda: b.aq_mxfp4_quantize(x, codes=c),
+        lambda: b.aq_mxfp4_quantize(x, scales=s),
+        lambda: b.aq_mxfp4_dequantize(c, s[:4]),
+        lambda: b.aq_mxfp4_dequantize(c, s, out_dtype=torch.float16),
+        lambda: b.aq_mxfp4_gemm(x.float(), c, s),
+        lambda: b.aq_mxfp4_gemm(x, c[:, :16], s),
+        lambda: b.aq_mxfp4_gemm(x, c, s[:, :1]),
+        lambda: b.aq_mxfp4_gemm(x, c, s.int()),
+        lambda: b.aq_mxfp4_gemm(x, c.t().contiguous().t(), s),
+        lambda: b.aq_mxfp4_gemm(x, c, s, out=torch.zeros(4, 9, device="cuda")),
+        lambda: b.aq_mxfp4_gemm(x, c, s, out_dtype=BF16, out=torch.zeros(4, 8, device="cuda")),
+        lambda: b.aq_mxfp4_gemm(x, c, s, out=torch.zeros(4, 8, device="cuda").t()),
+        lambda: b.aq_mxfp4_gemm(x, c.cpu(), s),
+        lambda: b.aq_mxfp4_gemm_a4(c, s, c[:, :16].contiguous(), s),
+        lambda: b.aq_mxfp4_grouped_gemm(x, c, s, off),                # weights of one expert, not [E, N, K/2]
+        lambda: b.aq_mxfp4_grouped_gemm(x, c[None], s[None], off.long()),
+        lambda: b.aq_mxfp4_grouped_gemm(x, c[None], s[None], off[:1]),
+        lambda: b.aq_mxfp4_grouped_gemm(x, c[None], s[None], off, rows=torch.zeros(4, device="cuda")),
+        lambda: b.aq_mxfp4_grouped_gemm(x, c[None], s[None], off, rows=torch.zeros(4, 1, dtype=torch.int32, device="cuda")),
+        lambda: b.aq_mxfp4_grouped_gemm(x[:0], c[None], s[None], off, rows=torch.zeros(4, dtype=torch.int32, device="cuda")),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            print("not refused:", i)

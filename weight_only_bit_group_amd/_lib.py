@@ -38,6 +38,12 @@ SIGNATURES = {
     "aq_fp4_gemm": (_I32, [_P, _I64, _I64, _P, _P, ctypes.c_float, _I64, _P, _P, _SZ, _P]),
     "aq_fp4_quantize_workspace": (_SZ, [_I64, _I64]),
     "aq_fp4_quantize": (_I32, [_P, _I32, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "aq_mxfp4_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _P]),
+    "aq_mxfp4_dequantize": (_I32, [_P, _P, _I64, _I64, _P, _I32, _P]),
+    "aq_mxfp4_gemm": (_I32, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P]),
+    "aq_mxfp4_gemm_a4": (_I32, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P]),
+    "aq_mxfp4_grouped_gemm": (_I32, [_P, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P]),
+    "aq_mxfp4_grouped_gemm_a4": (_I32, [_P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P]),
     "aq_last_error": (ctypes.c_char_p, []),
 }
 

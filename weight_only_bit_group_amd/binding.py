@@ -332,3 +332,178 @@ def aq_w8a16_gemv(X, codes, scales, zeros, group: int, out=None):
 def aq_w8a16_gemm(X, codes, scales, zeros, group: int, out=None, workspace=None):
     """Y[M, N] fp32 = X[M, K] (bf16, any M) times the dequantized 8-bit weight (staged bf16 + MFMA)."""
     return _product8("aq_w8a16_gemm", X, codes, scales, zeros, group, out, workspace)
+
+
+# ---- MXFP4 -------------------------------------------------------------------------------
+# These calls also run on a device that is not the current one (every tensor has to be on
+# X's device), and X may have rows further apart than their length.
+
+def _mx_call(name: str, dev: int, *args) -> None:
+    fn = getattr(_lib.load(), name)
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        check(st, name)
+
+
+def _mx_need(t, name: str, dtype, shape, device):
+    """A dense tensor of this type and shape on X's device (one test when it is)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _need(t, name, dtype)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+
+
+def _mx_rows(X, name: str, types):
+    """(rows, columns, row stride in elements) of a GPU matrix whose rows are dense."""
+    if not isinstance(X, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not X.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (got {X.device})")
+    if X.dtype not in types:
+        raise ValueError(f"{name} must be {' or '.join(str(t) for t in types)} (got {X.dtype})")
+    if X.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions")
+    m, k = X.shape
+    ld, step = X.stride()
+    if m <= 1 or ld == k:   # (the stride of a single row says nothing)
+        ld = k
+    if k > 1 and step != 1 or ld < k:
+        raise ValueError(f"{name} must have dense rows (strides {X.stride()})")
+    if k == 0 or k % 32:
+        raise ValueError(f"K must be a positive multiple of 32 (got {k})")
+    return m, k, ld
+
+
+_MX_OUT = {torch.float32: AQ_F32, torch.bfloat16: AQ_BF16}
+
+
+def _mx_out(out, shape, out_dtype, device):
+    """(the output tensor, its dtype code); out gives the type when out_dtype is None."""
+    if out_dtype is None:
+        out_dtype = torch.float32 if out is None else out.dtype
+    code = _MX_OUT.get(out_dtype)
+    if code is None:
+        raise ValueError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
+    if out is None:
+        return torch.empty(shape, dtype=out_dtype, device=device), code
+    _mx_need(out, "Y", out_dtype, shape, device)
+    return out, code
+
+
+def aq_mxfp4_quantize(X, *, codes=None, scales=None):
+    """(codes [M, K/2] u8, scales [M, K/32] u8) of X[M, K] (f32 or bf16; its rows may be strided)."""
+    m, k, ld = _mx_rows(X, "X", (torch.bfloat16, torch.float32))
+    dev = X.device
+    if codes is None:
+        codes = torch.empty((m, k // 2), dtype=torch.uint8, device=dev)
+    else:
+        _mx_need(codes, "codes", torch.uint8, (m, k // 2), dev)
+    if scales is None:
+        scales = torch.empty((m, k // 32), dtype=torch.uint8, device=dev)
+    else:
+        _mx_need(scales, "scales", torch.uint8, (m, k // 32), dev)
+    if m:
+        _mx_call("aq_mxfp4_quantize", dev.index, X.data_ptr(), _MX_OUT[X.dtype], m, k, ld, codes.data_ptr(),
+                 scales.data_ptr())
+    return codes, scales
+
+
+def aq_mxfp4_dequantize(codes, scales, out_dtype=None, out=None):
+    """Y[M, K] (float32, or bfloat16: exact in both) = the values of codes [M, K/2] and scales [M, K/32]."""
+    _need(codes, "codes", torch.uint8, 2)
+    m, k = codes.shape[0], codes.shape[1] * 2
+    if k == 0 or k % 32:
+        raise ValueError(f"K must be a positive multiple of 32 (got {k})")
+    _mx_need(scales, "scales", torch.uint8, (m, k // 32), codes.device)
+    out, code = _mx_out(out, (m, k), out_dtype, codes.device)
+    if m:
+        _mx_call("aq_mxfp4_dequantize", codes.device.index, codes.data_ptr(), scales.data_ptr(), m, k, out.data_ptr(),
+                 code)
+    return out
+
+
+def _mx_weights(codes, scales, k: int, device, ndim: int):
+    """The shape [N] or [E, N] of MXFP4 weights with rows of k."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != ndim:
+        raise ValueError("codes must be [N, K/2]" if ndim == 2 else "codes must be [E, N, K/2]")
+    lead = tuple(codes.shape[:-1])
+    _mx_need(codes, "codes", torch.uint8, lead + (k // 2,), device)
+    _mx_need(scales, "scales", torch.uint8, lead + (k // 32,), device)
+    return lead
+
+
+def _mx_a4(X_codes, X_scales):
+    _need(X_codes, "X_codes", torch.uint8, 2)
+    m, k = X_codes.shape[0], X_codes.shape[1] * 2
+    if k == 0 or k % 32:
+        raise ValueError(f"K must be a positive multiple of 32 (got {k})")
+    _mx_need(X_scales, "X_scales", torch.uint8, (m, k // 32), X_codes.device)
+    return m, k
+
+
+def aq_mxfp4_gemm(X, codes, scales, out_dtype=None, out=None):
+    """Y[M, N] (float32, or bfloat16) = X[M, K] (bf16; its rows may be strided) times the MXFP4 weights, transposed."""
+    m, k, ld = _mx_rows(X, "X", (torch.bfloat16,))
+    n, = _mx_weights(codes, scales, k, X.device, 2)
+    out, code = _mx_out(out, (m, n), out_dtype, X.device)
+    if m and n:
+        _mx_call("aq_mxfp4_gemm", X.device.index, X.data_ptr(), m, k, ld, codes.data_ptr(), scales.data_ptr(), n,
+                 out.data_ptr(), code)
+    return out
+
+
+def aq_mxfp4_gemm_a4(X_codes, X_scales, codes, scales, out_dtype=None, out=None):
+    """Y[M, N] (float32, or bfloat16) of MXFP4 activations (as aq_mxfp4_quantize returns them) and MXFP4 weights."""
+    m, k = _mx_a4(X_codes, X_scales)
+    n, = _mx_weights(codes, scales, k, X_codes.device, 2)
+    out, code = _mx_out(out, (m, n), out_dtype, X_codes.device)
+    if m and n:
+        _mx_call("aq_mxfp4_gemm_a4", X_codes.device.index, X_codes.data_ptr(), X_scales.data_ptr(), m, k,
+                 codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), code)
+    return out
+
+
+def _mx_lists(offsets, rows, e: int, t: int, device) -> int:
+    """Rows of Y: the length of rows, or all t rows of X."""
+    _mx_need(offsets, "offsets", torch.int32, (e + 1,), device)
+    if rows is None:
+        return t
+    _need(rows, "rows", torch.int32, 1)
+    if rows.device != device:
+        raise ValueError(f"rows must be on {device} (got {rows.device})")
+    return rows.shape[0]
+
+
+def aq_mxfp4_grouped_gemm(X, codes, scales, offsets, rows=None, out_dtype=None, out=None):
+    """Y[M, N]: rows offsets[e] .. offsets[e + 1] - 1 are X's rows (or those that ``rows`` [M] lists) times expert
+    e's MXFP4 weights, transposed.
+
+    X [T, K] bf16 (its rows may be strided), codes [E, N, K/2], scales [E, N, K/32], offsets [E + 1] int32 and rows
+    int32 on the device.  Rows of Y outside the offsets are not written.
+    """
+    t, k, ld = _mx_rows(X, "X", (torch.bfloat16,))
+    e, n = _mx_weights(codes, scales, k, X.device, 3)
+    m = _mx_lists(offsets, rows, e, t, X.device)
+    out, code = _mx_out(out, (m, n), out_dtype, X.device)
+    if m and n:
+        _mx_call("aq_mxfp4_grouped_gemm", X.device.index, X.data_ptr(), t, k, ld, codes.data_ptr(), scales.data_ptr(),
+                 e, n, offsets.data_ptr(), _ptr(rows), m, out.data_ptr(), code)
+    return out
+
+
+def aq_mxfp4_grouped_gemm_a4(X_codes, X_scales, codes, scales, offsets, rows=None, out_dtype=None, out=None):
+    """aq_mxfp4_grouped_gemm with the activations in MXFP4 (X_codes [T, K/2], X_scales [T, K/32])."""
+    t, k = _mx_a4(X_codes, X_scales)
+    e, n = _mx_weights(codes, scales, k, X_codes.device, 3)
+    m = _mx_lists(offsets, rows, e, t, X_codes.device)
+    out, code = _mx_out(out, (m, n), out_dtype, X_codes.device)
+    if m and n:
+        _mx_call("aq_mxfp4_grouped_gemm_a4", X_codes.device.index, X_codes.data_ptr(), X_scales.data_ptr(), t, k,
+                 codes.data_ptr(), scales.data_ptr(), e, n, offsets.data_ptr(), _ptr(rows), m, out.data_ptr(), code)
+    return out

@@ -540,4 +540,126 @@ aq_status aq_fp4_gemm(const uint16_t* X, int64_t M, int64_t K, const uint8_t* co
   return runtime_status(e, "aq_fp4_gemm");
 }
 
+// a [M, K] matrix of MXFP4 blocks and the launch's 256 threads per 8192 elements
+static aq_status check_mx_matrix(const char* fn, int64_t M, int64_t K) {
+  AQ_REQUIRE(M >= 0 && M < kDimLimit, "%s: M out of range (%lld)", fn, (long long)M);
+  AQ_REQUIRE(K > 0 && K < kDimLimit && K % 32 == 0, "%s: K must be a positive multiple of 32 (got %lld)", fn,
+             (long long)K);
+  AQ_REQUIRE(M * K < (int64_t(1) << 36), "%s: M * K must be below 2^36", fn);
+  return AQ_OK;
+}
+
+aq_status aq_mxfp4_quantize(const void* X, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* codes,
+                            uint8_t* scales, void* stream) {
+  const char* fn = "aq_mxfp4_quantize";
+  AQ_REQUIRE(x_dtype == AQ_F32 || x_dtype == AQ_BF16, "%s: x_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, x_dtype);
+  const aq_status st = check_mx_matrix(fn, M, K);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(ldx >= K && ldx < kDimLimit * 2 && ldx % (x_dtype == AQ_BF16 ? 8 : 4) == 0,
+             "%s: ldx (%lld) must be at least K and a multiple of 16 bytes", fn, (long long)ldx);
+  AQ_PTR(X, 16, "X");
+  AQ_PTR(codes, 16, "codes");
+  AQ_PTR(scales, 1, "scales");
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (M == 0) return ok();
+  return runtime_status(aq::launch_mxfp4_quantize(X, x_dtype == AQ_BF16, M, K, ldx, codes, scales, (hipStream_t)stream),
+                        fn);
+}
+
+aq_status aq_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* Y,
+                              int32_t y_dtype, void* stream) {
+  const char* fn = "aq_mxfp4_dequantize";
+  AQ_REQUIRE(y_dtype == AQ_F32 || y_dtype == AQ_BF16, "%s: y_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, y_dtype);
+  const aq_status st = check_mx_matrix(fn, M, K);
+  if (st != AQ_OK) return st;
+  AQ_PTR(codes, 16, "codes");
+  AQ_PTR(scales, 1, "scales");
+  AQ_PTR(Y, 16, "Y");
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (M == 0) return ok();
+  return runtime_status(aq::launch_mxfp4_dequantize(codes, scales, M, K, Y, y_dtype == AQ_BF16, (hipStream_t)stream),
+                        fn);
+}
+
+// X: bf16 rows ldx elements apart (x_scales NULL), or MXFP4 codes with x_scales
+static aq_status check_mx_product(const char* fn, const void* X, const uint8_t* x_scales, bool a4, int64_t M,
+                                  int64_t K, int64_t ldx, const uint8_t* codes, const uint8_t* scales, int64_t N,
+                                  const void* Y, int32_t y_dtype) {
+  AQ_REQUIRE(y_dtype == AQ_F32 || y_dtype == AQ_BF16, "%s: y_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, y_dtype);
+  AQ_REQUIRE(M >= 0 && M < kDimLimit, "%s: M out of range (%lld)", fn, (long long)M);
+  AQ_REQUIRE(K > 0 && K < kGemmDimLimit && K % 32 == 0, "%s: K must be a positive multiple of 32 below 2^22 (got %lld)",
+             fn, (long long)K);
+  AQ_REQUIRE(N >= 0 && N < kGemmDimLimit, "%s: N out of range (%lld)", fn, (long long)N);
+  if (!a4)
+    AQ_REQUIRE(ldx >= K && ldx < kDimLimit && ldx % 8 == 0, "%s: ldx (%lld) must be at least K and a multiple of 8", fn,
+               (long long)ldx);
+  AQ_PTR(X, 16, a4 ? "x_codes" : "X");
+  if (a4) AQ_PTR(x_scales, 1, "x_scales");
+  AQ_PTR(codes, 16, "codes");
+  AQ_PTR(scales, 1, "scales");
+  AQ_PTR(Y, y_dtype == AQ_BF16 ? 4 : 8, "Y");
+  return AQ_OK;
+}
+
+static aq_status mx_gemm(const char* fn, const void* X, const uint8_t* x_scales, bool a4, int64_t M, int64_t K,
+                         int64_t ldx, const uint8_t* codes, const uint8_t* scales, int64_t N, void* Y, int32_t y_dtype,
+                         void* stream) {
+  const aq_status st = check_mx_product(fn, X, x_scales, a4, M, K, ldx, codes, scales, N, Y, y_dtype);
+  if (st != AQ_OK) return st;
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (M == 0 || N == 0) return ok();
+  return runtime_status(aq::launch_mxfp4_gemm(X, x_scales, a4 ? K / 2 : ldx * 2, (int)M, (int)K, codes, scales, (int)N,
+                                              Y, y_dtype == AQ_BF16, (hipStream_t)stream),
+                        fn);
+}
+
+aq_status aq_mxfp4_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
+                        const uint8_t* scales, int64_t N, void* Y, int32_t y_dtype, void* stream) {
+  return mx_gemm("aq_mxfp4_gemm", X, nullptr, false, M, K, ldx, codes, scales, N, Y, y_dtype, stream);
+}
+
+aq_status aq_mxfp4_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, int64_t K,
+                           const uint8_t* codes, const uint8_t* scales, int64_t N, void* Y, int32_t y_dtype,
+                           void* stream) {
+  return mx_gemm("aq_mxfp4_gemm_a4", x_codes, x_scales, true, M, K, K, codes, scales, N, Y, y_dtype, stream);
+}
+
+static aq_status mx_grouped(const char* fn, const void* X, const uint8_t* x_scales, bool a4, int64_t T, int64_t K,
+                            int64_t ldx, const uint8_t* codes, const uint8_t* scales, int64_t E, int64_t N,
+                            const int32_t* offsets, const int32_t* rows, int64_t M, void* Y, int32_t y_dtype,
+                            void* stream) {
+  const aq_status st = check_mx_product(fn, X, x_scales, a4, M, K, ldx, codes, scales, N, Y, y_dtype);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(E > 0 && E < kDimLimit, "%s: E out of range (%lld)", fn, (long long)E);
+  AQ_REQUIRE(E * N < (int64_t(1) << 27) && M * N < (int64_t(1) << 38),
+             "%s: E * N must be below 2^27 and M * N below 2^38 (E %lld, M %lld, N %lld)", fn, (long long)E, (long long)M,
+             (long long)N);
+  AQ_REQUIRE(T >= 0 && T < kDimLimit, "%s: T out of range (%lld)", fn, (long long)T);
+  AQ_REQUIRE(M == 0 || (T > 0 && (rows != nullptr || T >= M)), "%s: X has %lld rows for %lld rows of Y", fn, (long long)T,
+             (long long)M);
+  AQ_PTR(offsets, 4, "offsets");
+  AQ_REQUIRE(aligned(rows, 4), "%s: rows must be 4-byte aligned", fn);
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (M == 0 || N == 0) return ok();
+  return runtime_status(aq::launch_mxfp4_grouped_gemm(X, x_scales, a4 ? K / 2 : ldx * 2, (int)T, (int)K, codes, scales,
+                                                      (int)E, (int)N, offsets, rows, (int)M, Y, y_dtype == AQ_BF16,
+                                                      (hipStream_t)stream),
+                        fn);
+}
+
+aq_status aq_mxfp4_grouped_gemm(const uint16_t* X, int64_t T, int64_t K, int64_t ldx, const uint8_t* codes,
+                                const uint8_t* scales, int64_t E, int64_t N, const int32_t* offsets,
+                                const int32_t* rows, int64_t M, void* Y, int32_t y_dtype, void* stream) {
+  return mx_grouped("aq_mxfp4_grouped_gemm", X, nullptr, false, T, K, ldx, codes, scales, E, N, offsets, rows, M, Y,
+                    y_dtype, stream);
+}
+
+aq_status aq_mxfp4_grouped_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T, int64_t K,
+                                   const uint8_t* codes, const uint8_t* scales, int64_t E, int64_t N,
+                                   const int32_t* offsets, const int32_t* rows, int64_t M, void* Y, int32_t y_dtype,
+                                   void* stream) {
+  return mx_grouped("aq_mxfp4_grouped_gemm_a4", x_codes, x_scales, true, T, K, K, codes, scales, E, N, offsets, rows, M,
+                    Y, y_dtype, stream);
+}
+
 }  // extern "C"

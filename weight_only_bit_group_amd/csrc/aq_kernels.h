@@ -58,6 +58,18 @@ size_t fp4_quantize_workspace_bytes(int64_t N, int64_t K);
 // ts: one fp32 on the device (written); partial: fp4_quantize_workspace_bytes of device memory
 hipError_t launch_fp4_quantize(const void* W, bool w_bf16, int64_t N, int64_t K, uint8_t* codes, uint8_t* bscale,
                                float* ts, float* partial, hipStream_t stream);
+// MXFP4: x_bf16 / y_bf16 false means fp32; ldx in elements
+hipError_t launch_mxfp4_quantize(const void* X, bool x_bf16, int64_t M, int64_t K, int64_t ldx, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* Y,
+                                   bool y_bf16, hipStream_t stream);
+// XS == NULL: X is bf16, else X holds MXFP4 codes and XS their scale bytes; xrow = bytes
+// between rows of X.  Grouped: M rows of Y, T rows of X, rows NULL or [M]
+hipError_t launch_mxfp4_gemm(const void* X, const uint8_t* XS, int64_t xrow, int M, int K, const uint8_t* codes,
+                             const uint8_t* scales, int N, void* Y, bool y_bf16, hipStream_t stream);
+hipError_t launch_mxfp4_grouped_gemm(const void* X, const uint8_t* XS, int64_t xrow, int T, int K,
+                                     const uint8_t* codes, const uint8_t* scales, int E, int N, const int32_t* offsets,
+                                     const int32_t* rows, int M, void* Y, bool y_bf16, hipStream_t stream);
 // compute units of the current device (cached per device)
 int device_cu_count();
 int64_t sumsq_gemm_blocks(int64_t M, int64_t N);

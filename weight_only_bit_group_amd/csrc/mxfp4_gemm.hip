@@ -67,9 +67,46 @@ __device__ __forceinline__ void dma16_at(const uint8_t* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory");
 }
 
+// The same from a wave-uniform base and the lane's 32-bit offset.  s_nop: the compiler does not
+// see into the block, and a base that it read out of a vector register just before needs five
+// wait states until a load may use it.
+__device__ __forceinline__ void dma16_from(const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
+}
+
 // every load and LDS write of this wave done, then the workgroup's barrier
 __device__ __forceinline__ void drain_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The tile kernel's matrix instructions, accumulating in place in AGPRs.  Written out because
+// the compiler gives a 16 x 16 instruction another destination than its addend and then moves
+// accumulators about (60 moves for 64 instructions in the loop).  It does not see the hazards
+// either: s_nop 1 covers an operand that a VALU instruction wrote just before (free, the matrix
+// core is busy with the instruction before), settle() the results' first reads after the loop.
+template <int Q>   // the scale byte of both dwords that applies
+__device__ __forceinline__ void mfma_a4(f32x4& c, u32x4 x, u32x4 w, uint32_t sx, uint32_t sw) {
+  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] "
+               "op_sel_hi:[%6,%6,0] cbsz:4 blgp:4"
+               : "+a"(c) : "v"(x), "v"(w), "v"(sx), "v"(sw), "n"(Q & 1), "n"(Q >> 1));
+}
+__device__ __forceinline__ void mfma_a16(f32x4& c, u32x4 x, bf16x8 w) {
+  asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(x), "v"(w));
+}
+template <int FM, int FN>
+__device__ __forceinline__ void settle(f32x4 (&acc)[FM][FN]) {
+  asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+
+// a wave-uniform address, in scalar registers
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
 }
 
 struct MxTile {
@@ -310,42 +347,61 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_rows_kernel(MxArgs a) {
 }
 
 // ---- many rows ----------------------------------------------------------------------------
-// WM x WN waves, each a (32 FM) x (32 FN) tile of 32 x 32 outputs.  K advances in stages of
-// 128 bytes of an activation row (A4: 256 k, A16: 64 k) through two LDS buffers filled by
-// LDS-DMA: while one stage is multiplied the next one is in flight, one barrier a stage.
-// Tile rows of 128 bytes keep unit u (16 bytes) of row r at u ^ ((r >> 1) & 7): two rows
-// span the 64 banks, so the 16 rows that a phase of a ds_read_b128 takes (the same unit of
-// each) fall into all of them.  The 32-byte weight rows of A16 use u ^ ((r >> 3) & 1).
+// WM x WN waves, each a (16 FM) x (16 FN) tile of 16 x 16 outputs.  (Against 32 x 32 x 64 and
+// 32 x 32 x 16 the instructions 16 x 16 x 128 and 16 x 16 x 32 touch each accumulator half as
+// often: on random operands, where the card's power sets the clock, 7.3 against 6.3 PFLOP/s
+// and 2.06 against 1.82 in a loop of nothing else.)  K advances in stages of 128 bytes of an
+// activation row (A4: 256 k, A16: 64 k) through two LDS buffers filled by LDS-DMA, one
+// barrier a stage.  The scale bytes of two stages are loaded at once, through registers.
+// A tile row keeps its 16-byte units permuted so that the 16 rows which a phase of a
+// ds_read takes fall into all 64 banks: unit u of row r is at u ^ ((r >> 1) & 7) in rows of
+// 128 bytes, at u ^ ((r >> 3) & 1) in rows of 32.
 // The weight rows of a wave are stored so that lane c of its FN operands holds rows
-// FN c .. FN c + FN - 1: its outputs of one row are neighbours and leave in one store, 32
-// lanes 128 or 256 contiguous bytes.
+// FN c .. FN c + FN - 1: its outputs of one row are neighbours and leave in one store, 16
+// lanes 64 to 256 contiguous bytes.
 template <bool A4_, int WM_, int WN_, int FM_, int FN_>
 struct MxCfg {
   static constexpr bool A4 = A4_;
   static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_;
   static constexpr int NW = WM * WN, NT = 64 * NW;
-  static constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
-  static constexpr int KS = A4 ? 256 : 64;           // k per stage
+  static constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
+  static constexpr int KS = A4 ? 256 : 64;           // k per stage, two instructions
+  static constexpr int XB = 128;                     // activation bytes per row and stage
   static constexpr int WB = A4 ? 128 : 32;           // weight bytes per row and stage
-  static constexpr int SPC = 512 / KS;               // stages per chunk of scale bytes
-  static constexpr int A_DMA = BM / 8 / NW;          // loads per wave and stage, 1 KiB each
+  static constexpr int A_DMA = BM * XB / 1024 / NW;  // loads per wave and stage, 1 KiB each
   static constexpr int B_DMA = BN * WB / 1024 / NW;
+  static constexpr int DMA = A_DMA + B_DMA;
+  static constexpr int SB = KS / 32;                 // scale bytes per row and stage
+  static constexpr int CB = 2 * SB;                  // and per row and chunk of two stages
   static constexpr int SROWS = A4 ? BM + BN : BN;    // rows of scale bytes
   static constexpr int SPT = (SROWS + NT - 1) / NT;  // of them per thread
-  static_assert(BM % (8 * NW) == 0 && (BN * WB) % (1024 * NW) == 0, "whole loads per wave");
+  static_assert(BM * XB % (1024 * NW) == 0 && BN * WB % (1024 * NW) == 0, "whole loads per wave");
 };
+
+template <int ROWB>
+__device__ __forceinline__ int lds_unit(int r, int u) {
+  return ROWB == 128 ? u ^ ((r >> 1) & 7) : u ^ ((r >> 3) & 1);
+}
+
+// the 4 x 4 bytes of v transposed: byte j of word i becomes byte i of word j
+__device__ __forceinline__ u32x4 transpose4(u32x4 v) {
+  const uint32_t a = __builtin_amdgcn_perm(v[1], v[0], 0x05010400u), b = __builtin_amdgcn_perm(v[1], v[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(v[3], v[2], 0x05010400u), d = __builtin_amdgcn_perm(v[3], v[2], 0x07030602u);
+  return u32x4{__builtin_amdgcn_perm(c, a, 0x05040100u), __builtin_amdgcn_perm(c, a, 0x07060302u),
+               __builtin_amdgcn_perm(d, b, 0x05040100u), __builtin_amdgcn_perm(d, b, 0x07060302u)};
+}
 
 template <class C, bool GROUPED, bool BF16>
 __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t As[2][C::BM * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t As[2][C::BM * C::XB];
   __shared__ __attribute__((aligned(1024))) uint8_t Bs[2][C::BN * C::WB];
-  __shared__ __attribute__((aligned(16))) uint8_t Ss[2][C::SROWS * 16];
+  __shared__ __attribute__((aligned(16))) uint8_t Ss[2][C::SROWS * C::CB];
   __shared__ uint8_t lost[GROUPED ? C::BM : 1];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wid / C::WN, wn = wid % C::WN;
-  const int l32 = lane & 31, lh = lane >> 5;
+  const int l16 = lane & 15, g = lane >> 4;
   const int tiles_n = (a.N + C::BN - 1) / C::BN;
   MxTile t;
   if constexpr (GROUPED) {
@@ -365,209 +421,291 @@ __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
     t.n0 = __builtin_amdgcn_readfirstlane((within / gm) * C::BN);
   }
   const int nblk = a.K >> 5;
-  const int nstage = (a.K + C::KS - 1) / C::KS;
-  const int krow = a.K >> 1;   // bytes of a code row
+  const int last = (a.K + C::KS - 1) / C::KS - 1;   // the last stage, perhaps part-filled
+  const int krow = a.K >> 1;                        // bytes of a code row
 
   // ---- sources of the LDS-DMA loads ----
-  // weight row of LDS row i: wave region i / (32 FN), operand (i / 32) % FN, lane i % 32
+  // weight row of LDS row i, from the tile's first: wave region i / (16 FN), operand
+  // (i / 16) % FN, lane i % 16
   auto brow = [&](int i) {
-    const int n = t.n0 + (i / (32 * C::FN)) * (32 * C::FN) + C::FN * (i & 31) + (i / 32) % C::FN;
-    return (int64_t)t.e * a.N + min(n, a.N - 1);
+    const int n = (i / (16 * C::FN)) * (16 * C::FN) + C::FN * (i & 15) + (i / 16) % C::FN;
+    return min(n, a.N - 1 - t.n0);
   };
-  const uint8_t* asrc[C::A_DMA];
-  const uint8_t* bsrc[C::B_DMA];
-  int aunit[C::A_DMA], bunit[C::B_DMA];
+  auto xrow = [&](int i) -> int64_t {
+    const int r = min(t.r0 + i, t.r1 - 1);
+    return GROUPED ? max(source_row(a, r), 0) : r;
+  };
+  const int64_t wfirst = (int64_t)t.e * a.N + t.n0;
+  const uint8_t* wtile = a.W + wfirst * krow;
+  // load j of wave w covers 8 activation rows (A4: or weight rows) or 32 weight rows from 8
+  // (32) (j NW + w) on; the unit that a lane fetches is the same in all of them, since
+  // their rows differ by whole periods of the permutation, 16 rows
+  constexpr int WU = C::WB / 16;
+  const int aunit = lds_unit<128>(8 * wid + (lane >> 3), lane & 7);
+  const int bunit = lds_unit<C::WB>((64 / WU) * wid + lane / WU, lane % WU);
+  static_assert(C::NW % 2 == 0, "the permutation's period");
+  uint32_t asrc[C::A_DMA];   // units from X (X is below 2^36 bytes)
+  uint32_t bsrc[C::B_DMA];   // bytes from wtile; below 2^31 for K < 2^22
 #pragma unroll
-  for (int j = 0; j < C::A_DMA; ++j) {
-    const int i = 8 * (j * C::NW + wid) + (lane >> 3);
-    aunit[j] = (lane & 7) ^ ((i >> 1) & 7);
-    const int src = max(GROUPED ? source_row(a, min(t.r0 + i, t.r1 - 1)) : min(t.r0 + i, t.r1 - 1), 0);
-    asrc[j] = a.X + (int64_t)src * a.xrow + 16 * aunit[j];
-  }
+  for (int j = 0; j < C::A_DMA; ++j)
+    asrc[j] = (uint32_t)((xrow(8 * (j * C::NW + wid) + (lane >> 3)) * a.xrow) >> 4) + aunit;
 #pragma unroll
-  for (int j = 0; j < C::B_DMA; ++j) {
-    if constexpr (C::A4) {
-      const int i = 8 * (j * C::NW + wid) + (lane >> 3);
-      bunit[j] = (lane & 7) ^ ((i >> 1) & 7);
-      bsrc[j] = a.W + brow(i) * krow + 16 * bunit[j];
-    } else {
-      const int i = 32 * (j * C::NW + wid) + (lane >> 1);
-      bunit[j] = (lane & 1) ^ ((i >> 3) & 1);
-      bsrc[j] = a.W + brow(i) * krow + 16 * bunit[j];
-    }
-  }
-  // In the last stage the units past the row's end read its last unit instead.  A unit is
-  // 32 k of an A4 row and of a weight row, 8 k of a bf16 row.
+  for (int j = 0; j < C::B_DMA; ++j)
+    bsrc[j] = (uint32_t)brow((64 / WU) * (j * C::NW + wid) + lane / WU) * (uint32_t)krow + 16u * bunit;
+  // In a part-filled last stage the units past the row's end read its last unit instead.  A
+  // unit is 32 k of an A4 row and of a weight row, 8 k of a bf16 row.
+  const int left = a.K - last * C::KS;
+  const uint32_t aback = max(aunit - (C::A4 ? left >> 5 : left >> 3) + 1, 0);
+  const uint32_t bback = 16 * max(bunit - (left >> 5) + 1, 0);
+  struct Source { const uint8_t *x, *w; uint32_t aback, bback; };
+  auto source = [&](int s) {
+    return Source{a.X + (int64_t)s * C::XB, uniform(wtile + (int64_t)s * C::WB), s == last ? aback : 0u, s == last ? bback : 0u};
+  };
+  auto issue_one = [&](const Source& f, int buf, int j) {
+    if (j < C::A_DMA)
+      dma16_at(f.x + 16 * (uint64_t)(asrc[j] - f.aback), lds_addr(&As[buf][1024 * (C::NW * j + wid)]));
+    else
+      dma16_from(f.w, bsrc[j - C::A_DMA] - f.bback, lds_addr(&Bs[buf][1024 * (C::NW * (j - C::A_DMA) + wid)]));
+  };
   auto issue = [&](int s, int buf) {
-    const int left = a.K - s * C::KS;
-    const bool tail = left < C::KS;
-    const int au = C::A4 ? left >> 5 : left >> 3, bu = left >> 5;
+    const Source f = source(s);
 #pragma unroll
-    for (int j = 0; j < C::A_DMA; ++j) {
-      const uint8_t* p = asrc[j] + (int64_t)s * 128;
-      if (tail && aunit[j] >= au) p -= 16 * (aunit[j] - au + 1);
-      dma16_at(p, __builtin_amdgcn_readfirstlane(lds_addr(&As[buf][1024 * (j * C::NW + wid)])));
-    }
-#pragma unroll
-    for (int j = 0; j < C::B_DMA; ++j) {
-      const uint8_t* p = bsrc[j] + (int64_t)s * C::WB;
-      if (tail && bunit[j] >= bu) p -= 16 * (bunit[j] - bu + 1);
-      dma16_at(p, __builtin_amdgcn_readfirstlane(lds_addr(&Bs[buf][1024 * (j * C::NW + wid)])));
-    }
+    for (int j = 0; j < C::DMA; ++j) issue_one(f, buf, j);
   };
 
-  // ---- scale bytes: 16 per row and chunk of 512 k, through registers ----
+  // ---- scale bytes: CB per row and chunk of two stages, through registers ----
+  using Sword = std::conditional_t<C::A4, unsigned __int128, uint32_t>;
   const uint8_t* ssrc[C::SPT];
-  u32x4 sreg[C::SPT];
+  Sword sreg[C::SPT];
 #pragma unroll
   for (int j = 0; j < C::SPT; ++j) {
     const int i = min(j * C::NT + tid, C::SROWS - 1);
-    if (C::A4 && i < C::BM) {
-      const int src = GROUPED ? source_row(a, min(t.r0 + i, t.r1 - 1)) : min(t.r0 + i, t.r1 - 1);
-      ssrc[j] = a.XS + (int64_t)max(src, 0) * nblk;
-    } else {
-      ssrc[j] = a.WS + brow(C::A4 ? i - C::BM : i) * nblk;
-    }
+    ssrc[j] = C::A4 && i < C::BM ? a.XS + xrow(i) * nblk : a.WS + (wfirst + brow(C::A4 ? i - C::BM : i)) * nblk;
   }
+  // of a chunk that the row ends in: its last CB bytes; those of the chunk before are
+  // shifted out when the word is written, so the bytes past the row's end are zero
+  int sshift = 0;
   auto load_scales = [&](int c) {
-    const int left = nblk - 16 * c;
+    const int at = min(c * C::CB, nblk - C::CB);
+    sshift = 8 * (c * C::CB - at);
+#pragma unroll
+    for (int j = 0; j < C::SPT; ++j) sreg[j] = load_any<Sword>(ssrc[j] + at);
+  };
+  auto load_short = [&]() {   // rows of fewer than CB bytes
 #pragma unroll
     for (int j = 0; j < C::SPT; ++j) {
-      if (left >= 16) {
-        sreg[j] = load_any<u32x4>(ssrc[j] + 16 * c);
-      } else if (nblk >= 16) {
-        // the row's last 16 bytes, those of earlier chunks shifted out and zeros in
-        const u32x4 v = load_any<u32x4>(ssrc[j] + nblk - 16);
-        uint64_t lo = ((uint64_t)v[1] << 32) | v[0], hi = ((uint64_t)v[3] << 32) | v[2];
-        int sh = 16 - left;   // 1 .. 15 bytes
-        if (sh >= 8) {
-          lo = hi;
-          hi = 0;
-          sh -= 8;
-        }
-        if (sh > 0) {
-          lo = (lo >> (8 * sh)) | (hi << (64 - 8 * sh));
-          hi >>= 8 * sh;
-        }
-        sreg[j] = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-      } else {
-        u32x4 v = {0, 0, 0, 0};
+      sreg[j] = 0;
+      for (int i = 0; i < nblk; ++i) sreg[j] |= (Sword)ssrc[j][i] << (8 * i);
+    }
+  };
+  // A4: byte 4 q + g, block g of instruction q of the chunk, goes to byte q of dword g,
+  // which is what lane group g reads
+  auto write_scales = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < 15; ++i)
-          if (i < left) v[i >> 2] |= (uint32_t)ssrc[j][i] << (8 * (i & 3));
-        sreg[j] = v;
+    for (int j = 0; j < C::SPT; ++j) {
+      const Sword v = sshift < 8 * C::CB ? sreg[j] >> sshift : 0;
+      if ((j + 1) * C::NT <= C::SROWS || j * C::NT + tid < C::SROWS) {
+        uint8_t* to = &Ss[buf][C::CB * (j * C::NT + tid)];
+        if constexpr (C::A4) *reinterpret_cast<u32x4*>(to) = transpose4(__builtin_bit_cast(u32x4, v));
+        else *reinterpret_cast<Sword*>(to) = v;
       }
     }
   };
-  auto write_scales = [&](int c) {
-#pragma unroll
-    for (int j = 0; j < C::SPT; ++j)
-      if ((j + 1) * C::NT <= C::SROWS || j * C::NT + tid < C::SROWS)
-        *reinterpret_cast<u32x4*>(&Ss[c & 1][16 * (j * C::NT + tid)]) = sreg[j];
-  };
 
-  f32x16 acc[C::FM][C::FN];
+  f32x4 acc[C::FM][C::FN];
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto row128 = [&](const uint8_t* base, int r, int u) {
-    return *reinterpret_cast<const u32x4*>(base + 128 * r + 16 * (u ^ ((r >> 1) & 7)));
+  const int am = wm * 16 * C::FM + l16, bn = wn * 16 * C::FN + l16;   // this lane's first LDS rows
+  // A stage is two steps of FM x FN instructions.  A4: lane group g takes block 4 q + g of
+  // the stage in step q.  A16: it takes 16 k, units 2 g and 2 g + 1 of its activation row
+  // and half of block g / 2 of its weight row, 8 k a step.  Operands are read a step ahead:
+  // the activations of row block i into the registers that its products have just used,
+  // A4's weights into a second set.
+  u32x4 xr[C::FM];
+  u32x4 wr[2][C::FN];              // A4: the two steps' codes
+  uint64_t wc[C::FN], wcnext[C::FN];   // A16: the stage's codes
+  uint32_t sa[C::FM], sb[C::FN], sbnext[C::FN];   // A4: the chunk's scale bytes; A16: sb, the stage's
+  auto load_x = [&](int buf, int q, int i) {
+    const int r = am + 16 * i;
+    xr[i] = *reinterpret_cast<const u32x4*>(&As[buf][128 * r + 16 * lds_unit<128>(r, C::A4 ? 4 * q + g : 2 * g + q)]);
   };
-  // the products of stage s; valid: its blocks of 32 k
-  auto multiply = [&](int s, int buf, auto tail_, int valid) {
-    constexpr bool TAIL = decltype(tail_)::value;
-    const uint8_t* sc = Ss[(s / C::SPC) & 1];
-    const int am = wm * 32 * C::FM, bn = wn * 32 * C::FN;
-    if constexpr (C::A4) {
-      // half h of the lanes takes blocks 4 h .. 4 h + 3 of the stage, one per instruction
-      uint32_t sa[C::FM], sb[C::FN];
+  auto load_w = [&](int buf, int q) {
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i)
-        sa[i] = *reinterpret_cast<const uint32_t*>(sc + 16 * (am + 32 * i + l32) + 8 * (s & 1) + 4 * lh);
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j)
-        sb[j] = *reinterpret_cast<const uint32_t*>(sc + 16 * (C::BM + bn + 32 * j + l32) + 8 * (s & 1) + 4 * lh);
-      auto step = [&](auto q_) {
-        constexpr int Q = decltype(q_)::value;
-        if (TAIL && Q >= valid) return;
-        i32x8 x[C::FM], w[C::FN];
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i) x[i] = codes8(row128(As[buf], am + 32 * i + l32, 4 * lh + Q));
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) w[j] = codes8(row128(Bs[buf], bn + 32 * j + l32, 4 * lh + Q));
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-          for (int j = 0; j < C::FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x[i], w[j], acc[i][j], 4, 4, Q, (int)sa[i], Q, (int)sb[j]);
-      };
-      step(std::integral_constant<int, 0>{});
-      step(std::integral_constant<int, 1>{});
-      step(std::integral_constant<int, 2>{});
-      step(std::integral_constant<int, 3>{});
-    } else {
-      // half h of the lanes takes block h of the stage, 8 k per instruction
-      u32x4 w[C::FN];
-      float f[C::FN];
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        const int r = bn + 32 * j + l32;
-        w[j] = *reinterpret_cast<const u32x4*>(Bs[buf] + 32 * r + 16 * (lh ^ ((r >> 3) & 1)));
-        f[j] = __uint_as_float((uint32_t)sc[16 * r + 2 * (s % C::SPC) + lh] << 23);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        bf16x8 x[C::FM], b[C::FN];
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-          u32x4 v = row128(As[buf], am + 32 * i + l32, 4 * lh + q);
-          if (TAIL && lh >= valid) v = u32x4{0, 0, 0, 0};
-          x[i] = __builtin_bit_cast(bf16x8, v);
-        }
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) b[j] = mx_bf16x8(w[j][q], f[j]);
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-          for (int j = 0; j < C::FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], b[j], acc[i][j], 0, 0, 0);
-      }
+    for (int j = 0; j < C::FN; ++j) {
+      const int r = bn + 16 * j;
+      wr[q][j] = *reinterpret_cast<const u32x4*>(&Bs[buf][128 * r + 16 * lds_unit<128>(r, 4 * q + g)]);
     }
   };
+  auto load_wc = [&](int buf, int st, int chunk) {
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const int r = bn + 16 * j;
+      wcnext[j] = *reinterpret_cast<const uint64_t*>(&Bs[buf][32 * r + 16 * lds_unit<32>(r, g >> 1) + 8 * (g & 1)]);
+      sbnext[j] = Ss[chunk & 1][4 * r + 2 * st + (g >> 1)];
+    }
+  };
+  auto load_sa = [&](int chunk, int i) {
+    sa[i] = *reinterpret_cast<const uint32_t*>(&Ss[chunk & 1][16 * (am + 16 * i) + 4 * g]);
+  };
+  auto load_sb = [&](int chunk) {
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+      sbnext[j] = *reinterpret_cast<const uint32_t*>(&Ss[chunk & 1][16 * (C::BM + bn + 16 * j) + 4 * g]);
+  };
+  auto take = [&](bool fresh) {   // the scale bytes (and A16's codes) requested last
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      if (C::A4 ? fresh : true) sb[j] = sbnext[j];
+      if constexpr (!C::A4) wc[j] = wcnext[j];
+    }
+  };
+  // A16: the bf16 weights of step q from the stage's codes
+  bf16x8 b[C::FN];
+  auto convert = [&](int q) {
+    if constexpr (!C::A4) {
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) b[j] = mx_bf16x8((uint32_t)(wc[j] >> (32 * q)), __uint_as_float(sb[j] << 23));
+    }
+  };
+  // the products of row blocks from .. to - 1 in step q of stage st of a chunk; after those
+  // of row block i, next(i) requests what comes next
+  auto products = [&](auto st_, auto q_, int from, int to, auto next) {
+    constexpr int ST = decltype(st_)::value, Q = decltype(q_)::value;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+      if (i < from || i >= to) continue;
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        if constexpr (C::A4) mfma_a4<2 * ST + Q>(acc[i][j], xr[i], wr[Q][j], sa[i], sb[j]);
+        else mfma_a16(acc[i][j], xr[i], b[j]);
+      }
+      next(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  constexpr std::integral_constant<int, 0> c0{};
+  constexpr std::integral_constant<int, 1> c1{};
 
   if constexpr (GROUPED) {
     for (int i = tid; i < C::BM; i += C::NT) lost[i] = source_row(a, min(t.r0 + i, t.r1 - 1)) < 0;
   }
-  load_scales(0);
+  // stage 0 and its scale bytes first, stage 1 behind them (with a single stage that one
+  // again, into the buffer that is not read)
   issue(0, 0);
-  const int nfull = a.K / C::KS;
-  for (int s = 0; s < nfull; ++s) {
-    if (s % C::SPC == 0) write_scales(s / C::SPC);
-    drain_barrier();
-    if (s + 1 < nstage) {
-      issue(s + 1, (s + 1) & 1);
-      if ((s + 1) % C::SPC == 0) load_scales((s + 1) / C::SPC);
-    }
-    multiply(s, s & 1, std::false_type{}, 0);
+  if (nblk >= C::CB) load_scales(0);
+  else load_short();
+  write_scales(0);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  issue(min(1, last), 1);
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    load_x(0, 0, i);
+    if constexpr (C::A4) load_sa(0, i);
   }
-  if (nfull < nstage) {
-    if (nfull % C::SPC == 0) write_scales(nfull / C::SPC);
-    drain_barrier();
-    multiply(nfull, nfull & 1, std::true_type{}, nblk - nfull * (C::KS / 32));
+  if constexpr (C::A4) {
+    load_w(0, 0);
+    load_sb(0);
+  } else {
+    load_wc(0, 0, 0);
   }
 
-  // ---- outputs: lane c of operand pair j holds columns FN c .. of its wave's columns ----
-  const int col = t.n0 + wn * 32 * C::FN + C::FN * l32;
-  const bool pairs = (a.N & 1) == 0;   // both columns of a pair are inside, and its store aligned
+  // One stage that is not the last, whole by that.  The hand-over to the next stage comes
+  // among the second step's products: by then every wave has had time to receive its last
+  // operands, so the buffer is free for the stage after next, whose loads go out between the
+  // products, and the rest of the products covers the first reads of the next stage.  There
+  // is no branch, which would let the compiler move the products past it: at the end the
+  // last stage is requested again, into the buffer that is not read.  (s is 2 chunk + ST,
+  // its buffer ST.)
+  constexpr int HEAD = C::FM / 4;   // row blocks before the hand-over
+  auto stage = [&](int s, auto st_) {
+    constexpr int ST = decltype(st_)::value, buf = ST, nbuf = ST ^ 1;
+    const int chunk = s >> 1;
+    take(ST == 0);
+    if constexpr (C::A4) load_w(buf, 1);
+    convert(0);
+    products(st_, c0, 0, C::FM, [&](int i) { load_x(buf, 1, i); });
+    convert(1);
+    products(st_, c1, 0, HEAD, [](int) {});
+    if constexpr (ST == 1) write_scales((chunk + 1) & 1);
+    drain_barrier();
+    if constexpr (ST == 0) load_scales(min((chunk + 1) * 2, last) >> 1);
+    const Source f = source(min(s + 2, last));
+    if constexpr (C::A4) {
+      load_w(nbuf, 0);
+      if constexpr (ST == 1) load_sb(chunk + 1);
+    } else {
+      load_wc(nbuf, ST ^ 1, ST == 1 ? chunk + 1 : chunk);
+    }
+    auto next = [&](int i) {
+      load_x(nbuf, 0, i);
+      if constexpr (C::A4 && ST == 1) load_sa(chunk + 1, i);
+    };
+#pragma unroll
+    for (int i = 0; i < HEAD; ++i) next(i);
+    products(st_, c1, HEAD, C::FM, [&](int i) {
+      next(i);
+      constexpr int L = C::FM - HEAD;
+#pragma unroll
+      for (int j = (i - HEAD) * C::DMA / L; j < (i - HEAD + 1) * C::DMA / L; ++j) issue_one(f, buf, j);
+    });
+  };
+  int s = 0;
+  for (; s + 2 <= last; s += 2) {
+    stage(s, c0);
+    stage(s + 1, c1);
+  }
+  // the last chunk: one or two stages, the last perhaps part-filled: its blocks past K have
+  // activations (A16) or both scale bytes (A4) zero, and an A4 step without any block is
+  // left out
+  auto rest = [&](auto st_, int valid) {
+    constexpr int ST = decltype(st_)::value, buf = ST;
+    if constexpr (ST == 1) {
+      drain_barrier();
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) load_x(buf, 0, i);
+      if constexpr (C::A4) load_w(buf, 0);
+      else load_wc(buf, 1, s >> 1);
+    }
+    take(ST == 0);
+    auto cut = [&]() {
+      if constexpr (!C::A4) {
+        if ((g >> 1) >= valid) {
+#pragma unroll
+          for (int i = 0; i < C::FM; ++i) xr[i] = u32x4{0, 0, 0, 0};
+        }
+      }
+    };
+    cut();
+    convert(0);
+    products(st_, c0, 0, C::FM, [](int) {});
+    if (C::A4 && valid <= 4) return;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) load_x(buf, 1, i);
+    if constexpr (C::A4) load_w(buf, 1);
+    cut();
+    convert(1);
+    products(st_, c1, 0, C::FM, [](int) {});
+  };
+  rest(c0, nblk - s * C::SB);
+  if (s < last) rest(c1, nblk - (s + 1) * C::SB);
+  settle(acc);
+  // no load may land in LDS that the next block owns by then
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  // ---- outputs: lane c of operand j holds column FN c + j of its wave's columns ----
+  const int col = t.n0 + wn * 16 * C::FN + C::FN * l16;
+  constexpr int ES = BF16 ? 2 : 4;
+  // all FN columns are inside or none, and their store aligned
+  const bool whole = a.N % C::FN == 0 && (reinterpret_cast<uintptr_t>(a.Y) & (C::FN * ES - 1)) == 0;
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int rl = wm * 32 * C::FM + 32 * i + 8 * (v >> 2) + 4 * lh + (v & 3);
+    for (int v = 0; v < 4; ++v) {
+      const int rl = wm * 16 * C::FM + 16 * i + 4 * g + v;
       const int r = t.r0 + rl;
       if (r >= t.r1) continue;
       const int64_t at = (int64_t)r * a.N + col;
@@ -577,15 +715,21 @@ __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
         o[j] = acc[i][j][v];
         if (GROUPED && lost[rl]) o[j] = __builtin_nanf("");
       }
-      static_assert(C::FN == 2, "outputs leave in pairs");
-      if (pairs) {
+      if (whole) {
         if (col < a.N) {
-          if constexpr (BF16) *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.Y) + at) = bf16_pair(o[0], o[1]);
-          else *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.Y) + at) = float2{o[0], o[1]};
+          if constexpr (BF16) {
+            uint32_t w[C::FN / 2];
+#pragma unroll
+            for (int j = 0; j < C::FN / 2; ++j) w[j] = bf16_pair(o[2 * j], o[2 * j + 1]);
+            __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<uint16_t*>(a.Y) + at, 2 * C::FN), w, 2 * C::FN);
+          } else {
+            __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<float*>(a.Y) + at, 4 * C::FN), o, 4 * C::FN);
+          }
         }
       } else {
-        if (col < a.N) store_one<BF16>(a.Y, at, o[0]);
-        if (col + 1 < a.N) store_one<BF16>(a.Y, at + 1, o[1]);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+          if (col + j < a.N) store_one<BF16>(a.Y, at + j, o[j]);
       }
     }
 }
@@ -617,8 +761,8 @@ hipError_t launch_any(const MxArgs& a, bool y_bf16, hipStream_t stream) {
   if (per <= 16) return launch_rows<A4, 1, 4, GROUPED>(a, y_bf16, stream);
   if (per <= 32) return launch_rows<A4, 2, 4, GROUPED>(a, y_bf16, stream);
   if (per <= 64) return launch_rows<A4, 4, 4, GROUPED>(a, y_bf16, stream);
-  if (per <= 256) return launch_tile<MxCfg<A4, 2, 2, 2, 2>, GROUPED>(a, y_bf16, stream);
-  return launch_tile<MxCfg<A4, 2, 4, 4, 2>, GROUPED>(a, y_bf16, stream);
+  if (per <= 256) return launch_tile<MxCfg<A4, 2, 2, 4, 4>, GROUPED>(a, y_bf16, stream);
+  return launch_tile<MxCfg<A4, 2, 4, 8, 4>, GROUPED>(a, y_bf16, stream);
 }
 
 }  // namespace

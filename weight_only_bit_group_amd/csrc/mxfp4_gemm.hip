@@ -189,6 +189,29 @@ __device__ __forceinline__ void store_one(void* Y, int64_t i, float v) {
   else reinterpret_cast<float*>(Y)[i] = v;
 }
 
+// FN neighbouring outputs from column `col` on; whole: all are inside or none, and aligned
+template <bool BF16, int FN>
+__device__ __forceinline__ void store_row(const MxArgs& a, int64_t at, int col, bool whole, const float (&o)[FN]) {
+  if (whole) {
+    if (col < a.N) {
+      if constexpr (BF16 && FN > 1) {
+        uint32_t w[FN / 2];
+#pragma unroll
+        for (int j = 0; j < FN / 2; ++j) w[j] = bf16_pair(o[2 * j], o[2 * j + 1]);
+        __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<uint16_t*>(a.Y) + at, 2 * FN), w, 2 * FN);
+      } else if constexpr (BF16) {
+        store_one<true>(a.Y, at, o[0]);
+      } else {
+        __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<float*>(a.Y) + at, 4 * FN), o, 4 * FN);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      if (col + j < a.N) store_one<BF16>(a.Y, at + j, o[j]);
+  }
+}
+
 // the four bf16 pairs of code dword w times the block factor f
 __device__ __forceinline__ bf16x8 mx_bf16x8(uint32_t w, float f) {
   const u32x4 v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 0)),
@@ -203,145 +226,234 @@ __device__ __forceinline__ i32x8 codes8(u32x4 v) {
 }
 
 // ---- few rows -----------------------------------------------------------------------------
-// Bound by the weight bytes: a block takes 16 weight rows and up to 16 MT activation rows,
-// its waves share K in chunks of 512 (lane group g of 16 lanes: blocks 4 g .. 4 g + 3 of the
-// chunk, 64 contiguous bytes of its row), codes straight from memory into the operands, the
-// next chunk's codes requested before the current one is multiplied.  The waves' sums are
-// added in LDS in wave order.
-template <bool A4, int MT, int NW, bool GROUPED, bool BF16>
-__global__ __launch_bounds__(64 * NW) void mxfp4_rows_kernel(MxArgs a) {
-  __shared__ float part[NW][MT][4][64];
+// Bound by the weight bytes (and from some ten rows on by the activation bytes that every
+// block reads from its L2).  A block's NW waves share K: each takes a contiguous run of
+// stages (A4: 256 k, A16: 64 k) of the (16 FM) x (16 FN) tile through LDS buffers of its own,
+// filled by its own LDS-DMA loads, so there is no barrier before the sums are joined: a wave
+// only waits for its own oldest loads, with R stages in flight.  The LDS layout and the
+// order of the weight rows are those of the larger tiles below; the scale bytes come straight
+// to the lanes that use them, 16 bytes of a row at a time.
+template <int ROWB>
+__device__ __forceinline__ int lds_unit(int r, int u) {
+  return ROWB == 128 ? u ^ ((r >> 1) & 7) : u ^ ((r >> 3) & 1);
+}
+
+// 16 scale bytes from byte `at` of a row of nblk, zeros past its end
+__device__ __forceinline__ u32x4 scales16(const uint8_t* row, int at, int nblk) {
+  if (nblk >= 16) {
+    const int from = min(at, nblk - 16);
+    const unsigned __int128 v = load_any<unsigned __int128>(row + from);
+    const int sh = 8 * (at - from);
+    return __builtin_bit_cast(u32x4, sh < 128 ? v >> sh : (unsigned __int128)0);
+  }
+  unsigned __int128 v = 0;
+  for (int i = at; i < nblk; ++i) v |= (unsigned __int128)row[i] << (8 * (i - at));
+  return __builtin_bit_cast(u32x4, v);
+}
+
+template <bool A4_, int FM_, int FN_, int NW_, int R_>
+struct MxSplit {
+  static constexpr bool A4 = A4_;
+  static constexpr int FM = FM_, FN = FN_, NW = NW_, R = R_;
+  static constexpr int BM = 16 * FM, BN = 16 * FN, NT = 64 * NW;
+  static constexpr int KS = A4 ? 256 : 64;
+  static constexpr int WB = A4 ? 128 : 32;
+  static constexpr int A_DMA = 2 * FM;
+  static constexpr int B_DMA = A4 ? 2 * FN : (FN + 1) / 2;
+  static constexpr int DMA = A_DMA + B_DMA;
+  static constexpr int STAGE = 1024 * DMA;                  // LDS bytes of a wave's stage
+  static constexpr int SB = KS / 32;
+  static constexpr int SC = 16 / SB;                        // stages whose scale bytes are loaded at once
+  static constexpr int PART = 4 * FM * FN * 64 * 4;         // bytes of a wave's sums
+  static constexpr int LDS = NW * (R * STAGE > PART ? R * STAGE : PART);
+  static_assert((R - 1) * DMA < 64, "the loads in flight are counted in six bits");
+};
+
+template <class C, bool GROUPED, bool BF16>
+__global__ __launch_bounds__(C::NT) void mxfp4_split_kernel(MxArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles_n = (a.N + 15) >> 4;
+  const int l16 = lane & 15, g = lane >> 4;
+  const int tiles_n = (a.N + C::BN - 1) / C::BN;
   MxTile t;
   if constexpr (GROUPED) {
-    if (!grouped_tile<16 * MT>(a, tiles_n, 16, blockIdx.x, t)) return;   // the whole block
+    if (!grouped_tile<C::BM>(a, tiles_n, C::BN, blockIdx.x, t)) return;   // the whole block
   } else {
-    t = MxTile{0, 0, a.M, 16 * tile_of_block(blockIdx.x, tiles_n)};
+    // the row tiles of a column run side by side: they share its weights in the L2
+    const int tiles_m = (a.M + C::BM - 1) / C::BM;
+    const int i = tile_of_block(blockIdx.x, tiles_m * tiles_n);
+    t.e = 0;
+    t.r0 = (i % tiles_m) * C::BM;
+    t.r1 = min(t.r0 + C::BM, a.M);
+    t.n0 = (i / tiles_m) * C::BN;
   }
-  const int l16 = lane & 15, g = lane >> 4;
-  const int nblk = a.K >> 5;
-  const int64_t wr = (int64_t)t.e * a.N + min(t.n0 + l16, a.N - 1);
-  const uint8_t* wc = a.W + wr * (a.K >> 1);
-  const uint8_t* ws = a.WS + wr * nblk;
-  const uint8_t* xc[MT];
-  const uint8_t* xs[MT];
-  bool live[MT], lost[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int r = t.r0 + 16 * i + l16;
-    live[i] = r < t.r1;
-    const int src = live[i] ? source_row(a, r) : 0;
-    lost[i] = src < 0;
-    xc[i] = a.X + (int64_t)max(src, 0) * a.xrow;
-    xs[i] = A4 ? a.XS + (int64_t)max(src, 0) * nblk : nullptr;
-  }
-  // the dword of scale bytes of blocks b .. b + 3 (zero past the row's end)
-  auto scales4 = [&](const uint8_t* row, int b) -> uint32_t {
-    if (nblk >= 4) {
-      const int at = min(b, nblk - 4);
-      const int sh = 8 * (b - at);
-      const uint32_t v = load_any<uint32_t>(row + at);
-      return sh < 32 ? v >> sh : 0u;
-    }
-    uint32_t v = 0;
-    for (int i = 0; i < 4; ++i)
-      if (b + i < nblk) v |= (uint32_t)row[b + i] << (8 * i);
-    return v;
-  };
-  f32x4 acc[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int nblk = a.K >> 5, krow = a.K >> 1;
+  const int stages = (a.K + C::KS - 1) / C::KS;
+  const int first = (int)((int64_t)wid * stages / C::NW), end = (int)((int64_t)(wid + 1) * stages / C::NW);
+  uint8_t* mine = lds + wid * C::R * C::STAGE;
 
-  const int nchunk = (nblk + 15) >> 4;
-  u32x4 wq[4];
-  uint32_t wsc = 0;
-  auto fetch = [&](int c) {
-    const int b = 16 * c + 4 * g;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) wq[u] = *reinterpret_cast<const u32x4*>(wc + 16 * min(b + u, nblk - 1));
-    wsc = scales4(ws, b);
+  auto brow = [&](int i) { return min(C::FN * (i & 15) + (i >> 4), a.N - 1 - t.n0); };
+  auto xrow = [&](int i) -> int64_t {
+    const int r = min(t.r0 + i, t.r1 - 1);
+    return GROUPED ? max(source_row(a, r), 0) : r;
   };
-  if (wid < nchunk) fetch(wid);
-  for (int c = wid; c < nchunk; c += NW) {
-    const int b = 16 * c + 4 * g;
-    u32x4 w[4];
+  constexpr int WU = C::WB / 16;
+  const int aunit = lds_unit<128>(lane >> 3, lane & 7);
+  const int bunit = lds_unit<C::WB>(lane / WU, lane % WU);
+  const int64_t wfirst = (int64_t)t.e * a.N + t.n0;
+  const uint8_t* wtile = a.W + wfirst * krow;
+  uint32_t asrc[C::A_DMA], bsrc[C::B_DMA];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) w[u] = wq[u];
-    const uint32_t sw = wsc;
-    if constexpr (A4) {
-      u32x4 x[MT][4];
-      uint32_t sx[MT];
+  for (int j = 0; j < C::A_DMA; ++j) asrc[j] = (uint32_t)((xrow(8 * j + (lane >> 3)) * a.xrow) >> 4) + (aunit ^ (4 * (j & 1)));
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        sx[i] = scales4(xs[i], b);
+  for (int j = 0; j < C::B_DMA; ++j) {
+    // (rows past the tile, when it has fewer than a load covers: the last row again)
+    const int i = min((64 / WU) * j + lane / WU, C::BN - 1);
+    bsrc[j] = (uint32_t)brow(i) * (uint32_t)krow + 16u * (C::A4 ? bunit ^ (4 * (j & 1)) : bunit);
+  }
+  // units past the row's end in a part-filled last stage: its last unit instead
+  const int left = a.K - (stages - 1) * C::KS;
+  auto issue = [&](int s, int slot) {
+    const uint8_t* x = a.X + (int64_t)s * 128;
+    const uint8_t* w = uniform(wtile + (int64_t)s * C::WB);
+    const bool tail = s == stages - 1;
+    const uint32_t base = lds_addr(mine + slot * C::STAGE);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          x[i][u] = *reinterpret_cast<const u32x4*>(xc[i] + 16 * min(b + u, nblk - 1));
-          if (b + u >= nblk) x[i][u] = u32x4{0, 0, 0, 0};
-        }
+    for (int j = 0; j < C::A_DMA; ++j) {
+      const int back = max((aunit ^ (4 * (j & 1))) - (C::A4 ? left >> 5 : left >> 3) + 1, 0);
+      dma16_at(x + 16 * (uint64_t)(asrc[j] - (tail ? back : 0)), __builtin_amdgcn_readfirstlane(base + 1024 * j));
+    }
+#pragma unroll
+    for (int j = 0; j < C::B_DMA; ++j) {
+      const int back = max((C::A4 ? bunit ^ (4 * (j & 1)) : bunit) - (left >> 5) + 1, 0);
+      dma16_from(w, bsrc[j] - (tail ? 16 * back : 0), __builtin_amdgcn_readfirstlane(base + 1024 * (C::A_DMA + j)));
+    }
+  };
+
+  const uint8_t* wscale[C::FN];
+  const uint8_t* xscale[C::A4 ? C::FM : 1];
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) wscale[j] = a.WS + (wfirst + brow(16 * j + l16)) * nblk;
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+    if constexpr (C::A4) xscale[i] = a.XS + xrow(16 * i + l16) * nblk;
+
+  f32x4 acc[C::FM][C::FN];
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+#pragma unroll
+  for (int s = 0; s < C::R; ++s)
+    if (first + s < end) issue(first + s, s);
+  u32x4 sw[C::FN], sx[C::FM];
+  auto fetch_scales = [&](int s) {
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) sw[j] = scales16(wscale[j], s * C::SB, nblk);
+    if constexpr (C::A4) {
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) sx[i] = scales16(xscale[i], s * C::SB, nblk);
+    }
+  };
+  auto row = [&](const uint8_t* tile, int r, int u) { return *reinterpret_cast<const u32x4*>(tile + 128 * r + 16 * lds_unit<128>(r, u)); };
+  // stage s, the ST-th of those whose scale bytes are at hand
+  auto stage = [&](int s, auto st_) {
+    constexpr int ST = decltype(st_)::value;
+    if (s >= end) return;
+    const int slot = (s - first) % C::R;
+    if (s + C::R < end) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((C::R - 1) * C::DMA) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const uint8_t* xt = mine + slot * C::STAGE;
+    const uint8_t* wt = xt + 1024 * C::A_DMA;
+    const int valid = nblk - s * C::SB;
+    u32x4 x[2][C::FM];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        x[q][i] = row(xt, 16 * i + l16, C::A4 ? 4 * q + g : 2 * g + q);
+        if (!C::A4 && (g >> 1) >= valid) x[q][i] = u32x4{0, 0, 0, 0};
       }
-      if (c + NW < nchunk) fetch(c + NW);
+    if constexpr (C::A4) {
+      u32x4 w[2][C::FN];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes8(x[i][0]), codes8(w[0]), acc[i], 4, 4, 0, (int)sx[i], 0, (int)sw);
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes8(x[i][1]), codes8(w[1]), acc[i], 4, 4, 1, (int)sx[i], 1, (int)sw);
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes8(x[i][2]), codes8(w[2]), acc[i], 4, 4, 2, (int)sx[i], 2, (int)sw);
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes8(x[i][3]), codes8(w[3]), acc[i], 4, 4, 3, (int)sx[i], 3, (int)sw);
-      }
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) w[q][j] = row(wt, 16 * j + l16, 4 * q + g);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (s + C::R < end) issue(s + C::R, slot);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j)
+            mfma_a4<0>(acc[i][j], x[q][i], w[q][j], sx[i][2 * ST + q] >> (8 * g), sw[j][2 * ST + q] >> (8 * g));
     } else {
-      if (c + NW < nchunk) fetch(c + NW);
+      uint64_t wc[C::FN];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float f = __uint_as_float(((sw >> (8 * u)) & 255u) << 23);
-        u32x4 x[MT][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            x[i][q] = u32x4{0, 0, 0, 0};
-            if (live[i] && b + u < nblk) x[i][q] = *reinterpret_cast<const u32x4*>(xc[i] + 64 * (b + u) + 16 * q);
-          }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const bf16x8 bw = mx_bf16x8(w[u][q], f);
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[i][q]), bw, acc[i], 0, 0, 0);
-        }
+      for (int j = 0; j < C::FN; ++j) {
+        const int r = 16 * j + l16;
+        wc[j] = *reinterpret_cast<const uint64_t*>(wt + 32 * r + 16 * lds_unit<32>(r, g >> 1) + 8 * (g & 1));
       }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (s + C::R < end) issue(s + C::R, slot);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+          const uint32_t byte = (sw[j][ST >> 1] >> (16 * (ST & 1) + 8 * (g >> 1))) & 255u;
+          const bf16x8 b = mx_bf16x8((uint32_t)(wc[j] >> (32 * q)), __uint_as_float(byte << 23));
+#pragma unroll
+          for (int i = 0; i < C::FM; ++i) mfma_a16(acc[i][j], x[q][i], b);
+        }
+    }
+  };
+  for (int s = first; s < end; s += C::SC) {
+    fetch_scales(s);
+    stage(s, std::integral_constant<int, 0>{});
+    stage(s + 1, std::integral_constant<int, 1>{});
+    if constexpr (C::SC == 8) {
+      stage(s + 2, std::integral_constant<int, 2>{});
+      stage(s + 3, std::integral_constant<int, 3>{});
+      stage(s + 4, std::integral_constant<int, 4>{});
+      stage(s + 5, std::integral_constant<int, 5>{});
+      stage(s + 6, std::integral_constant<int, 6>{});
+      stage(s + 7, std::integral_constant<int, 7>{});
     }
   }
-  // rows of Y whose listed activation row is outside X become NaN: the lane that holds
-  // operand row r tells the lanes that hold it as outputs
-  uint64_t lostm[MT];
+  settle(acc);
+
+  // ---- the waves' sums, added in wave order; lane c of operand j: column FN c + j ----
+  float* part = reinterpret_cast<float*>(lds);
+  __syncthreads();   // (every wave has read its last stage)
 #pragma unroll
-  for (int i = 0; i < MT; ++i) lostm[i] = __ballot(lost[i]);
+  for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+    for (int v = 0; v < 4; ++v)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) part[wid][i][j][lane] = acc[i][j];
+      for (int j = 0; j < C::FN; ++j) part[(((wid * C::FM + i) * 4 + v) * C::FN + j) * 64 + lane] = acc[i][j][v];
   __syncthreads();
-  const int n = t.n0 + l16;
+  const int col = t.n0 + C::FN * l16;
+  constexpr int ES = BF16 ? 2 : 4;
+  const bool whole = a.N % C::FN == 0 && (reinterpret_cast<uintptr_t>(a.Y) & (C::FN * ES - 1)) == 0;
+  for (int o = wid; o < 4 * C::FM; o += C::NW) {
+    float sum[C::FN];
 #pragma unroll
-  for (int o = 0; o < MT * 4; o += NW) {
-    const int idx = o + wid;   // (i, j) of the outputs this wave adds and stores
-    if (idx < MT * 4) {
-      const int i = idx >> 2, j = idx & 3;
-      float v = part[0][i][j][lane];
+    for (int j = 0; j < C::FN; ++j) sum[j] = part[(o * C::FN + j) * 64 + lane];
 #pragma unroll
-      for (int w = 1; w < NW; ++w) v += part[w][i][j][lane];
-      const int rl = 4 * g + j;
-      const int r = t.r0 + 16 * i + rl;
-      if (GROUPED) {
-        uint64_t m = 0;
+    for (int w = 1; w < C::NW; ++w)
 #pragma unroll
-        for (int q = 0; q < MT; ++q)
-          if (q == i) m = lostm[q];
-        if ((m >> rl) & 1) v = __builtin_nanf("");
+      for (int j = 0; j < C::FN; ++j) sum[j] += part[((w * 4 * C::FM + o) * C::FN + j) * 64 + lane];
+    const int r = t.r0 + 16 * (o >> 2) + 4 * g + (o & 3);
+    if (r < t.r1) {
+      if (GROUPED && source_row(a, r) < 0) {
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) sum[j] = __builtin_nanf("");
       }
-      if (r < t.r1 && n < a.N) store_one<BF16>(a.Y, (int64_t)r * a.N + n, v);
+      store_row<BF16, C::FN>(a, (int64_t)r * a.N + col, col, whole, sum);
     }
   }
 }
@@ -377,11 +489,6 @@ struct MxCfg {
   static constexpr int SPT = (SROWS + NT - 1) / NT;  // of them per thread
   static_assert(BM * XB % (1024 * NW) == 0 && BN * WB % (1024 * NW) == 0, "whole loads per wave");
 };
-
-template <int ROWB>
-__device__ __forceinline__ int lds_unit(int r, int u) {
-  return ROWB == 128 ? u ^ ((r >> 1) & 7) : u ^ ((r >> 3) & 1);
-}
 
 // the 4 x 4 bytes of v transposed: byte j of word i becomes byte i of word j
 __device__ __forceinline__ u32x4 transpose4(u32x4 v) {
@@ -715,22 +822,7 @@ __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
         o[j] = acc[i][j][v];
         if (GROUPED && lost[rl]) o[j] = __builtin_nanf("");
       }
-      if (whole) {
-        if (col < a.N) {
-          if constexpr (BF16) {
-            uint32_t w[C::FN / 2];
-#pragma unroll
-            for (int j = 0; j < C::FN / 2; ++j) w[j] = bf16_pair(o[2 * j], o[2 * j + 1]);
-            __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<uint16_t*>(a.Y) + at, 2 * C::FN), w, 2 * C::FN);
-          } else {
-            __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<float*>(a.Y) + at, 4 * C::FN), o, 4 * C::FN);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-          if (col + j < a.N) store_one<BF16>(a.Y, at + j, o[j]);
-      }
+      store_row<BF16, C::FN>(a, at, col, whole, o);
     }
 }
 
@@ -745,22 +837,23 @@ hipError_t launch_tile(const MxArgs& a, bool y_bf16, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool A4, int MT, int NW, bool GROUPED>
-hipError_t launch_rows(const MxArgs& a, bool y_bf16, hipStream_t stream) {
-  const int64_t tiles_n = (a.N + 15) / 16;
-  const int64_t tiles_m = GROUPED ? std::min<int64_t>(a.M, a.M / (16 * MT) + a.E) : 1;
-  const dim3 grid((unsigned)(tiles_m * tiles_n)), block(64 * NW);
-  if (y_bf16) hipLaunchKernelGGL((mxfp4_rows_kernel<A4, MT, NW, GROUPED, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((mxfp4_rows_kernel<A4, MT, NW, GROUPED, false>), grid, block, 0, stream, a);
+template <class C, bool GROUPED>
+hipError_t launch_split(const MxArgs& a, bool y_bf16, hipStream_t stream) {
+  const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
+  const int64_t tiles_m = GROUPED ? std::min<int64_t>(a.M, a.M / C::BM + a.E) : (a.M + C::BM - 1) / C::BM;
+  const dim3 grid((unsigned)(tiles_m * tiles_n)), block(C::NT);
+  static_assert(C::LDS <= 64 * 1024, "within the limit of dynamic LDS that needs no attribute");
+  if (y_bf16) hipLaunchKernelGGL((mxfp4_split_kernel<C, GROUPED, true>), grid, block, C::LDS, stream, a);
+  else hipLaunchKernelGGL((mxfp4_split_kernel<C, GROUPED, false>), grid, block, C::LDS, stream, a);
   return hipGetLastError();
 }
 
 template <bool A4, bool GROUPED>
 hipError_t launch_any(const MxArgs& a, bool y_bf16, hipStream_t stream) {
   const int per = GROUPED ? (a.M + a.E - 1) / a.E : a.M;   // rows of a product (grouped: their mean)
-  if (per <= 16) return launch_rows<A4, 1, 4, GROUPED>(a, y_bf16, stream);
-  if (per <= 32) return launch_rows<A4, 2, 4, GROUPED>(a, y_bf16, stream);
-  if (per <= 64) return launch_rows<A4, 4, 4, GROUPED>(a, y_bf16, stream);
+  if (per <= 16) return launch_split<MxSplit<A4, 1, 1, 8, 2>, GROUPED>(a, y_bf16, stream);
+  if (per <= 32) return launch_split<MxSplit<A4, 2, 2, 4, 2>, GROUPED>(a, y_bf16, stream);
+  if (per <= 64) return launch_split<MxSplit<A4, 4, 4, 4, 1>, GROUPED>(a, y_bf16, stream);
   if (per <= 256) return launch_tile<MxCfg<A4, 2, 2, 4, 4>, GROUPED>(a, y_bf16, stream);
   return launch_tile<MxCfg<A4, 2, 4, 8, 4>, GROUPED>(a, y_bf16, stream);
 }

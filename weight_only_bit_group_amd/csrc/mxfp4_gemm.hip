@@ -26,6 +26,7 @@
 // the last row; the activations (or both scale bytes) of a block past K are zero, rows
 // past the end are not stored.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "aq_device.h"
@@ -189,22 +190,26 @@ __device__ __forceinline__ void store_one(void* Y, int64_t i, float v) {
   else reinterpret_cast<float*>(Y)[i] = v;
 }
 
+// FN neighbouring outputs in one aligned store
+template <bool BF16, int FN>
+__device__ __forceinline__ void store_vector(void* Y, int64_t at, const float (&o)[FN]) {
+  if constexpr (BF16 && FN > 1) {
+    uint32_t w[FN / 2];
+#pragma unroll
+    for (int j = 0; j < FN / 2; ++j) w[j] = bf16_pair(o[2 * j], o[2 * j + 1]);
+    __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<uint16_t*>(Y) + at, 2 * FN), w, 2 * FN);
+  } else if constexpr (BF16) {
+    store_one<true>(Y, at, o[0]);
+  } else {
+    __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<float*>(Y) + at, 4 * FN), o, 4 * FN);
+  }
+}
+
 // FN neighbouring outputs from column `col` on; whole: all are inside or none, and aligned
 template <bool BF16, int FN>
 __device__ __forceinline__ void store_row(const MxArgs& a, int64_t at, int col, bool whole, const float (&o)[FN]) {
   if (whole) {
-    if (col < a.N) {
-      if constexpr (BF16 && FN > 1) {
-        uint32_t w[FN / 2];
-#pragma unroll
-        for (int j = 0; j < FN / 2; ++j) w[j] = bf16_pair(o[2 * j], o[2 * j + 1]);
-        __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<uint16_t*>(a.Y) + at, 2 * FN), w, 2 * FN);
-      } else if constexpr (BF16) {
-        store_one<true>(a.Y, at, o[0]);
-      } else {
-        __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<float*>(a.Y) + at, 4 * FN), o, 4 * FN);
-      }
-    }
+    if (col < a.N) store_vector<BF16, FN>(a.Y, at, o);
   } else {
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -580,6 +585,14 @@ __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
     for (int j = 0; j < C::DMA; ++j) issue_one(f, buf, j);
   };
 
+  // the loads of stage s that go out after the products of the i-th of n row blocks
+  auto issue_slice = [&](int s, int buf, int i, int n) {
+    const Source f = source(s);
+#pragma unroll
+    for (int j = 0; j < C::DMA; ++j)
+      if (j >= i * C::DMA / n && j < (i + 1) * C::DMA / n) issue_one(f, buf, j);
+  };
+
   // ---- scale bytes: CB per row and chunk of two stages, through registers ----
   using Sword = std::conditional_t<C::A4, unsigned __int128, uint32_t>;
   const uint8_t* ssrc[C::SPT];
@@ -699,15 +712,12 @@ __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
   if constexpr (GROUPED) {
     for (int i = tid; i < C::BM; i += C::NT) lost[i] = source_row(a, min(t.r0 + i, t.r1 - 1)) < 0;
   }
-  // stage 0 and its scale bytes first, stage 1 behind them (with a single stage that one
-  // again, into the buffer that is not read)
+  // stage 0 and its scale bytes first; stage 1 goes out between the first products
   issue(0, 0);
   if (nblk >= C::CB) load_scales(0);
   else load_short();
   write_scales(0);
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  issue(min(1, last), 1);
-  asm volatile("s_barrier" ::: "memory");
+  drain_barrier();
 #pragma unroll
   for (int i = 0; i < C::FM; ++i) {
     load_x(0, 0, i);
@@ -734,7 +744,10 @@ __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
     take(ST == 0);
     if constexpr (C::A4) load_w(buf, 1);
     convert(0);
-    products(st_, c0, 0, C::FM, [&](int i) { load_x(buf, 1, i); });
+    products(st_, c0, 0, C::FM, [&](int i) {
+      load_x(buf, 1, i);
+      if (ST == 0 && s == 0) issue_slice(1, 1, i, C::FM);
+    });
     convert(1);
     products(st_, c1, 0, HEAD, [](int) {});
     if constexpr (ST == 1) write_scales((chunk + 1) & 1);
@@ -797,6 +810,7 @@ __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
     convert(1);
     products(st_, c1, 0, C::FM, [](int) {});
   };
+  if (s == 0 && last == 1) issue(1, 1);
   rest(c0, nblk - s * C::SB);
   if (s < last) rest(c1, nblk - (s + 1) * C::SB);
   settle(acc);
@@ -842,20 +856,70 @@ hipError_t launch_split(const MxArgs& a, bool y_bf16, hipStream_t stream) {
   const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
   const int64_t tiles_m = GROUPED ? std::min<int64_t>(a.M, a.M / C::BM + a.E) : (a.M + C::BM - 1) / C::BM;
   const dim3 grid((unsigned)(tiles_m * tiles_n)), block(C::NT);
-  static_assert(C::LDS <= 64 * 1024, "within the limit of dynamic LDS that needs no attribute");
-  if (y_bf16) hipLaunchKernelGGL((mxfp4_split_kernel<C, GROUPED, true>), grid, block, C::LDS, stream, a);
-  else hipLaunchKernelGGL((mxfp4_split_kernel<C, GROUPED, false>), grid, block, C::LDS, stream, a);
-  return hipGetLastError();
+  auto launch = [&](auto kernel, std::atomic<uint64_t>& done) -> hipError_t {
+    if (C::LDS > 64 * 1024) {
+      // the kernel's limit of dynamic LDS, raised once per device (bit d of done)
+      int dev = 0;
+      hipError_t e = hipGetDevice(&dev);
+      if (e != hipSuccess) return e;
+      const uint64_t bit = uint64_t(1) << (dev & 63);
+      if (!(done.load(std::memory_order_acquire) & bit)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+        if (e != hipSuccess) return e;
+        done.fetch_or(bit, std::memory_order_acq_rel);
+      }
+    }
+    hipLaunchKernelGGL(kernel, grid, block, C::LDS, stream, a);
+    return hipGetLastError();
+  };
+  static std::atomic<uint64_t> done_bf16{0}, done_f32{0};
+  return y_bf16 ? launch(mxfp4_split_kernel<C, GROUPED, true>, done_bf16) : launch(mxfp4_split_kernel<C, GROUPED, false>, done_f32);
 }
 
+// The form of a product by its sizes: from the largest tile to the smallest, the first one
+// that is not twice as high as the rows of a product (grouped: their mean over the experts
+// that can have any; 64 x 128 may be) and gives enough blocks for the device.
+//   Two thirds of the compute units are enough for A4, whose larger tiles gain more than the
+// idle units lose (M = 1024 on [11008, 2048]: 172 tiles of 256 x 256 22.2 us, 688 of 128 x
+// 128 25.6; M = 128: 172 of 64 x 128 9.7, 344 of 64 x 32 12.4); A16's tiles above 64 x 64
+// want 4/3 (M = 1024: 50.7 against 46.6 us; M = 128: 17.2 against 15.2 with 344 of 64 x 64).
+//   Of the forms that share K, tall ones for few tiles (M = 64 on [2048, 2048]: 16 x 32 4.3
+// us, 64 x 32 over 5.1), wide ones where 16 rows already give thousands of tiles (512 rows
+// over 128 experts of [2048, 1024]: 16 x 64 34, 16 x 16 86 us).
+//   Their waves: four; eight, and sixteen for 16 x 16, over rows of more than 4096 k (M = 16
+// on [4096, 14336]: 8.7 against 11.3 us for A4, 14.3 against 20.0 for A16); one where the
+// tiles alone fill the device many times over (the 128 experts above: 34 against 42 us).
 template <bool A4, bool GROUPED>
 hipError_t launch_any(const MxArgs& a, bool y_bf16, hipStream_t stream) {
-  const int per = GROUPED ? (a.M + a.E - 1) / a.E : a.M;   // rows of a product (grouped: their mean)
-  if (per <= 16) return launch_split<MxSplit<A4, 1, 1, 8, 2>, GROUPED>(a, y_bf16, stream);
-  if (per <= 32) return launch_split<MxSplit<A4, 2, 2, 4, 2>, GROUPED>(a, y_bf16, stream);
-  if (per <= 64) return launch_split<MxSplit<A4, 4, 4, 4, 1>, GROUPED>(a, y_bf16, stream);
-  if (per <= 256) return launch_tile<MxCfg<A4, 2, 2, 4, 4>, GROUPED>(a, y_bf16, stream);
-  return launch_tile<MxCfg<A4, 2, 4, 8, 4>, GROUPED>(a, y_bf16, stream);
+  const int64_t cus = device_cu_count();
+  const int64_t products = GROUPED ? std::min(a.M, a.E) : 1;
+  const int64_t per = (a.M + products - 1) / products;
+  auto fits = [&](int64_t bm, int64_t bn, int64_t thirds) {
+    return bm < 2 * per + (bm == 64 && bn == 128) && 3 * products * ((per + bm - 1) / bm) * ((a.N + bn - 1) / bn) >= thirds * cus;
+  };
+  const bool longk = a.K > 4096;
+  if (per > 16) {
+    if (fits(256, 256, A4 ? 2 : 4)) return launch_tile<MxCfg<A4, 2, 4, 8, 4>, GROUPED>(a, y_bf16, stream);
+    if (fits(128, 128, A4 ? 2 : 4)) return launch_tile<MxCfg<A4, 2, 2, 4, 4>, GROUPED>(a, y_bf16, stream);
+    if (fits(64, 128, A4 ? 2 : 4))
+      return launch_tile<std::conditional_t<A4, MxCfg<A4, 2, 2, 2, 4>, MxCfg<A4, 1, 4, 4, 2>>, GROUPED>(a, y_bf16, stream);
+    if constexpr (!A4) {
+      if (!longk && fits(64, 64, 2)) return launch_split<MxSplit<A4, 4, 4, 4, 1>, GROUPED>(a, y_bf16, stream);
+    }
+    if (fits(64, 32, 2))
+      return longk ? launch_split<MxSplit<A4, 4, 2, 8, 1>, GROUPED>(a, y_bf16, stream)
+                   : launch_split<MxSplit<A4, 4, 2, 4, 1>, GROUPED>(a, y_bf16, stream);
+    if (fits(32, 32, 2) || per > 256)
+      return longk ? launch_split<MxSplit<A4, 2, 2, 8, 1>, GROUPED>(a, y_bf16, stream)
+                   : launch_split<MxSplit<A4, 2, 2, 4, 2>, GROUPED>(a, y_bf16, stream);
+    return longk ? launch_split<MxSplit<A4, 1, 2, 8, 2>, GROUPED>(a, y_bf16, stream)
+                 : launch_split<MxSplit<A4, 1, 2, 4, 2>, GROUPED>(a, y_bf16, stream);
+  }
+  const int64_t wide = products * ((a.N + 63) / 64);   // tiles of 16 x 64
+  if (wide >= 16 * cus) return launch_split<MxSplit<A4, 1, 4, 1, 2>, GROUPED>(a, y_bf16, stream);
+  if (wide >= 4 * cus) return launch_split<MxSplit<A4, 1, 4, 4, 1>, GROUPED>(a, y_bf16, stream);
+  return longk ? launch_split<MxSplit<A4, 1, 1, 16, 2>, GROUPED>(a, y_bf16, stream)
+               : launch_split<MxSplit<A4, 1, 1, 4, 2>, GROUPED>(a, y_bf16, stream);
 }
 
 }  // namespace

@@ -336,10 +336,17 @@ def aq_w8a16_gemm(X, codes, scales, zeros, group: int, out=None, workspace=None)
 
 # ---- MXFP4 -------------------------------------------------------------------------------
 # These calls also run on a device that is not the current one (every tensor has to be on
-# X's device), and X may have rows further apart than their length.
+# X's device), and X may have rows further apart than their length.  A call on a few rows is
+# a matter of microseconds on the host, so arguments are looked over in one expression each;
+# what fails it is named by the slower _mx_need.
+
+_MX_FN = {}   # name -> the library's function
+
 
 def _mx_call(name: str, dev: int, *args) -> None:
-    fn = getattr(_lib.load(), name)
+    fn = _MX_FN.get(name)
+    if fn is None:
+        fn = _MX_FN[name] = getattr(_lib.load(), name)
     if torch._C._cuda_getDevice() == dev:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
@@ -349,18 +356,17 @@ def _mx_call(name: str, dev: int, *args) -> None:
         check(st, name)
 
 
-def _mx_need(t, name: str, dtype, shape, device):
-    """A dense tensor of this type and shape on X's device (one test when it is)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
-        _need(t, name, dtype)
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
+def _mx_need(t, name: str, dtype, shape, dev: int):
+    """Raises unless t is a dense GPU tensor of this type and shape on device dev."""
+    _need(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev} (got {t.device})")
 
 
 def _mx_rows(X, name: str, types):
-    """(rows, columns, row stride in elements) of a GPU matrix whose rows are dense."""
+    """(rows, columns, row stride in elements, device) of a GPU matrix whose rows are dense."""
     if not isinstance(X, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not X.is_cuda:
@@ -370,20 +376,53 @@ def _mx_rows(X, name: str, types):
     if X.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions")
     m, k = X.shape
-    ld, step = X.stride()
-    if m <= 1 or ld == k:   # (the stride of a single row says nothing)
-        ld = k
-    if k > 1 and step != 1 or ld < k:
-        raise ValueError(f"{name} must have dense rows (strides {X.stride()})")
-    if k == 0 or k % 32:
+    if k == 0 or k & 31:
         raise ValueError(f"K must be a positive multiple of 32 (got {k})")
-    return m, k, ld
+    ld = k
+    if not X.is_contiguous():
+        ld, step = X.stride()
+        if m <= 1:   # (the stride of a single row says nothing)
+            ld = k
+        if step != 1 or ld < k:
+            raise ValueError(f"{name} must have dense rows (strides {X.stride()})")
+    return m, k, ld, X.get_device()
+
+
+_U8 = torch.uint8
+
+
+def _mx_codes(codes, scales, name: str, scales_name: str):
+    """(rows, columns, device) of an MXFP4 matrix: codes [M, K/2], scales [M, K/32]."""
+    if not (isinstance(codes, torch.Tensor) and codes.is_cuda and codes.dtype is _U8 and codes.dim() == 2
+            and codes.is_contiguous()):
+        _need(codes, name, _U8, 2)
+    m, half = codes.shape
+    if half == 0 or half & 15:
+        raise ValueError(f"K must be a positive multiple of 32 (got {2 * half})")
+    dev = codes.get_device()
+    if not (isinstance(scales, torch.Tensor) and scales.dtype is _U8 and scales.shape == (m, half >> 4)
+            and scales.get_device() == dev and scales.is_contiguous()):
+        _mx_need(scales, scales_name, _U8, (m, half >> 4), dev)
+    return m, 2 * half, dev
+
+
+def _mx_weights(codes, scales, k: int, dev: int, ndim: int):
+    """The shape (N,) or (E, N) of MXFP4 weights with rows of k."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != ndim:
+        raise ValueError("codes must be [N, K/2]" if ndim == 2 else "codes must be [E, N, K/2]")
+    *lead, half = codes.shape
+    if not (half * 2 == k and codes.dtype is _U8 and codes.get_device() == dev and codes.is_contiguous()):
+        _mx_need(codes, "codes", _U8, (*lead, k // 2), dev)
+    if not (isinstance(scales, torch.Tensor) and scales.shape == (*lead, k >> 5) and scales.dtype is _U8
+            and scales.get_device() == dev and scales.is_contiguous()):
+        _mx_need(scales, "scales", _U8, (*lead, k >> 5), dev)
+    return lead
 
 
 _MX_OUT = {torch.float32: AQ_F32, torch.bfloat16: AQ_BF16}
 
 
-def _mx_out(out, shape, out_dtype, device):
+def _mx_out(out, m: int, n: int, out_dtype, like, dev: int):
     """(the output tensor, its dtype code); out gives the type when out_dtype is None."""
     if out_dtype is None:
         out_dtype = torch.float32 if out is None else out.dtype
@@ -391,92 +430,67 @@ def _mx_out(out, shape, out_dtype, device):
     if code is None:
         raise ValueError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
     if out is None:
-        return torch.empty(shape, dtype=out_dtype, device=device), code
-    _mx_need(out, "Y", out_dtype, shape, device)
+        return like.new_empty((m, n), dtype=out_dtype), code
+    _mx_need(out, "Y", out_dtype, (m, n), dev)
     return out, code
 
 
 def aq_mxfp4_quantize(X, *, codes=None, scales=None):
     """(codes [M, K/2] u8, scales [M, K/32] u8) of X[M, K] (f32 or bf16; its rows may be strided)."""
-    m, k, ld = _mx_rows(X, "X", (torch.bfloat16, torch.float32))
-    dev = X.device
+    m, k, ld, dev = _mx_rows(X, "X", _MX_OUT)
     if codes is None:
-        codes = torch.empty((m, k // 2), dtype=torch.uint8, device=dev)
+        codes = X.new_empty((m, k >> 1), dtype=torch.uint8)
     else:
-        _mx_need(codes, "codes", torch.uint8, (m, k // 2), dev)
+        _mx_need(codes, "codes", torch.uint8, (m, k >> 1), dev)
     if scales is None:
-        scales = torch.empty((m, k // 32), dtype=torch.uint8, device=dev)
+        scales = X.new_empty((m, k >> 5), dtype=torch.uint8)
     else:
-        _mx_need(scales, "scales", torch.uint8, (m, k // 32), dev)
+        _mx_need(scales, "scales", torch.uint8, (m, k >> 5), dev)
     if m:
-        _mx_call("aq_mxfp4_quantize", dev.index, X.data_ptr(), _MX_OUT[X.dtype], m, k, ld, codes.data_ptr(),
-                 scales.data_ptr())
+        _mx_call("aq_mxfp4_quantize", dev, X.data_ptr(), _MX_OUT[X.dtype], m, k, ld, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def aq_mxfp4_dequantize(codes, scales, out_dtype=None, out=None):
     """Y[M, K] (float32, or bfloat16: exact in both) = the values of codes [M, K/2] and scales [M, K/32]."""
-    _need(codes, "codes", torch.uint8, 2)
-    m, k = codes.shape[0], codes.shape[1] * 2
-    if k == 0 or k % 32:
-        raise ValueError(f"K must be a positive multiple of 32 (got {k})")
-    _mx_need(scales, "scales", torch.uint8, (m, k // 32), codes.device)
-    out, code = _mx_out(out, (m, k), out_dtype, codes.device)
+    m, k, dev = _mx_codes(codes, scales, "codes", "scales")
+    out, code = _mx_out(out, m, k, out_dtype, codes, dev)
     if m:
-        _mx_call("aq_mxfp4_dequantize", codes.device.index, codes.data_ptr(), scales.data_ptr(), m, k, out.data_ptr(),
-                 code)
+        _mx_call("aq_mxfp4_dequantize", dev, codes.data_ptr(), scales.data_ptr(), m, k, out.data_ptr(), code)
     return out
-
-
-def _mx_weights(codes, scales, k: int, device, ndim: int):
-    """The shape [N] or [E, N] of MXFP4 weights with rows of k."""
-    if not isinstance(codes, torch.Tensor) or codes.dim() != ndim:
-        raise ValueError("codes must be [N, K/2]" if ndim == 2 else "codes must be [E, N, K/2]")
-    lead = tuple(codes.shape[:-1])
-    _mx_need(codes, "codes", torch.uint8, lead + (k // 2,), device)
-    _mx_need(scales, "scales", torch.uint8, lead + (k // 32,), device)
-    return lead
-
-
-def _mx_a4(X_codes, X_scales):
-    _need(X_codes, "X_codes", torch.uint8, 2)
-    m, k = X_codes.shape[0], X_codes.shape[1] * 2
-    if k == 0 or k % 32:
-        raise ValueError(f"K must be a positive multiple of 32 (got {k})")
-    _mx_need(X_scales, "X_scales", torch.uint8, (m, k // 32), X_codes.device)
-    return m, k
 
 
 def aq_mxfp4_gemm(X, codes, scales, out_dtype=None, out=None):
     """Y[M, N] (float32, or bfloat16) = X[M, K] (bf16; its rows may be strided) times the MXFP4 weights, transposed."""
-    m, k, ld = _mx_rows(X, "X", (torch.bfloat16,))
-    n, = _mx_weights(codes, scales, k, X.device, 2)
-    out, code = _mx_out(out, (m, n), out_dtype, X.device)
+    m, k, ld, dev = _mx_rows(X, "X", (torch.bfloat16,))
+    n, = _mx_weights(codes, scales, k, dev, 2)
+    out, code = _mx_out(out, m, n, out_dtype, X, dev)
     if m and n:
-        _mx_call("aq_mxfp4_gemm", X.device.index, X.data_ptr(), m, k, ld, codes.data_ptr(), scales.data_ptr(), n,
-                 out.data_ptr(), code)
+        _mx_call("aq_mxfp4_gemm", dev, X.data_ptr(), m, k, ld, codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), code)
     return out
 
 
 def aq_mxfp4_gemm_a4(X_codes, X_scales, codes, scales, out_dtype=None, out=None):
     """Y[M, N] (float32, or bfloat16) of MXFP4 activations (as aq_mxfp4_quantize returns them) and MXFP4 weights."""
-    m, k = _mx_a4(X_codes, X_scales)
-    n, = _mx_weights(codes, scales, k, X_codes.device, 2)
-    out, code = _mx_out(out, (m, n), out_dtype, X_codes.device)
+    m, k, dev = _mx_codes(X_codes, X_scales, "X_codes", "X_scales")
+    n, = _mx_weights(codes, scales, k, dev, 2)
+    out, code = _mx_out(out, m, n, out_dtype, X_codes, dev)
     if m and n:
-        _mx_call("aq_mxfp4_gemm_a4", X_codes.device.index, X_codes.data_ptr(), X_scales.data_ptr(), m, k,
-                 codes.data_ptr(), scales.data_ptr(), n, out.data_ptr(), code)
+        _mx_call("aq_mxfp4_gemm_a4", dev, X_codes.data_ptr(), X_scales.data_ptr(), m, k, codes.data_ptr(),
+                 scales.data_ptr(), n, out.data_ptr(), code)
     return out
 
 
-def _mx_lists(offsets, rows, e: int, t: int, device) -> int:
+def _mx_lists(offsets, rows, e: int, t: int, dev: int) -> int:
     """Rows of Y: the length of rows, or all t rows of X."""
-    _mx_need(offsets, "offsets", torch.int32, (e + 1,), device)
+    if not (isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32 and offsets.shape == (e + 1,)
+            and offsets.get_device() == dev and offsets.is_contiguous()):
+        _mx_need(offsets, "offsets", torch.int32, (e + 1,), dev)
     if rows is None:
         return t
     _need(rows, "rows", torch.int32, 1)
-    if rows.device != device:
-        raise ValueError(f"rows must be on {device} (got {rows.device})")
+    if rows.get_device() != dev:
+        raise ValueError(f"rows must be on cuda:{dev} (got {rows.device})")
     return rows.shape[0]
 
 
@@ -487,23 +501,24 @@ def aq_mxfp4_grouped_gemm(X, codes, scales, offsets, rows=None, out_dtype=None, 
     X [T, K] bf16 (its rows may be strided), codes [E, N, K/2], scales [E, N, K/32], offsets [E + 1] int32 and rows
     int32 on the device.  Rows of Y outside the offsets are not written.
     """
-    t, k, ld = _mx_rows(X, "X", (torch.bfloat16,))
-    e, n = _mx_weights(codes, scales, k, X.device, 3)
-    m = _mx_lists(offsets, rows, e, t, X.device)
-    out, code = _mx_out(out, (m, n), out_dtype, X.device)
+    t, k, ld, dev = _mx_rows(X, "X", (torch.bfloat16,))
+    e, n = _mx_weights(codes, scales, k, dev, 3)
+    m = _mx_lists(offsets, rows, e, t, dev)
+    out, code = _mx_out(out, m, n, out_dtype, X, dev)
     if m and n:
-        _mx_call("aq_mxfp4_grouped_gemm", X.device.index, X.data_ptr(), t, k, ld, codes.data_ptr(), scales.data_ptr(),
-                 e, n, offsets.data_ptr(), _ptr(rows), m, out.data_ptr(), code)
+        _mx_call("aq_mxfp4_grouped_gemm", dev, X.data_ptr(), t, k, ld, codes.data_ptr(), scales.data_ptr(), e, n,
+                 offsets.data_ptr(), None if rows is None else rows.data_ptr(), m, out.data_ptr(), code)
     return out
 
 
 def aq_mxfp4_grouped_gemm_a4(X_codes, X_scales, codes, scales, offsets, rows=None, out_dtype=None, out=None):
     """aq_mxfp4_grouped_gemm with the activations in MXFP4 (X_codes [T, K/2], X_scales [T, K/32])."""
-    t, k = _mx_a4(X_codes, X_scales)
-    e, n = _mx_weights(codes, scales, k, X_codes.device, 3)
-    m = _mx_lists(offsets, rows, e, t, X_codes.device)
-    out, code = _mx_out(out, (m, n), out_dtype, X_codes.device)
+    t, k, dev = _mx_codes(X_codes, X_scales, "X_codes", "X_scales")
+    e, n = _mx_weights(codes, scales, k, dev, 3)
+    m = _mx_lists(offsets, rows, e, t, dev)
+    out, code = _mx_out(out, m, n, out_dtype, X_codes, dev)
     if m and n:
-        _mx_call("aq_mxfp4_grouped_gemm_a4", X_codes.device.index, X_codes.data_ptr(), X_scales.data_ptr(), t, k,
-                 codes.data_ptr(), scales.data_ptr(), e, n, offsets.data_ptr(), _ptr(rows), m, out.data_ptr(), code)
+        _mx_call("aq_mxfp4_grouped_gemm_a4", dev, X_codes.data_ptr(), X_scales.data_ptr(), t, k, codes.data_ptr(),
+                 scales.data_ptr(), e, n, offsets.data_ptr(), None if rows is None else rows.data_ptr(), m,
+                 out.data_ptr(), code)
     return out

@@ -190,26 +190,26 @@ __device__ __forceinline__ void store_one(void* Y, int64_t i, float v) {
   else reinterpret_cast<float*>(Y)[i] = v;
 }
 
-// FN neighbouring outputs in one aligned store
+// FN neighbouring outputs of one row from column `col` on, in one store where all are inside
+// (rows of Y start at any element: an unaligned store, which the hardware takes)
 template <bool BF16, int FN>
-__device__ __forceinline__ void store_vector(void* Y, int64_t at, const float (&o)[FN]) {
-  if constexpr (BF16 && FN > 1) {
-    uint32_t w[FN / 2];
+__device__ __forceinline__ void store_row(const MxArgs& a, int64_t at, int col, const float (&o)[FN]) {
+  if (col + FN <= a.N) {
+    if constexpr (FN == 1) {
+      store_one<BF16>(a.Y, at, o[0]);
+    } else if constexpr (BF16) {
+      typedef uint32_t vec __attribute__((ext_vector_type(FN / 2), aligned(2)));
+      vec v;
 #pragma unroll
-    for (int j = 0; j < FN / 2; ++j) w[j] = bf16_pair(o[2 * j], o[2 * j + 1]);
-    __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<uint16_t*>(Y) + at, 2 * FN), w, 2 * FN);
-  } else if constexpr (BF16) {
-    store_one<true>(Y, at, o[0]);
-  } else {
-    __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<float*>(Y) + at, 4 * FN), o, 4 * FN);
-  }
-}
-
-// FN neighbouring outputs from column `col` on; whole: all are inside or none, and aligned
-template <bool BF16, int FN>
-__device__ __forceinline__ void store_row(const MxArgs& a, int64_t at, int col, bool whole, const float (&o)[FN]) {
-  if (whole) {
-    if (col < a.N) store_vector<BF16, FN>(a.Y, at, o);
+      for (int j = 0; j < FN / 2; ++j) v[j] = bf16_pair(o[2 * j], o[2 * j + 1]);
+      *reinterpret_cast<vec*>(reinterpret_cast<uint16_t*>(a.Y) + at) = v;
+    } else {
+      typedef float vec __attribute__((ext_vector_type(FN), aligned(4)));
+      vec v;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) v[j] = o[j];
+      *reinterpret_cast<vec*>(reinterpret_cast<float*>(a.Y) + at) = v;
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -442,8 +442,6 @@ __global__ __launch_bounds__(C::NT) void mxfp4_split_kernel(MxArgs a) {
       for (int j = 0; j < C::FN; ++j) part[(((wid * C::FM + i) * 4 + v) * C::FN + j) * 64 + lane] = acc[i][j][v];
   __syncthreads();
   const int col = t.n0 + C::FN * l16;
-  constexpr int ES = BF16 ? 2 : 4;
-  const bool whole = a.N % C::FN == 0 && (reinterpret_cast<uintptr_t>(a.Y) & (C::FN * ES - 1)) == 0;
   for (int o = wid; o < 4 * C::FM; o += C::NW) {
     float sum[C::FN];
 #pragma unroll
@@ -458,7 +456,7 @@ __global__ __launch_bounds__(C::NT) void mxfp4_split_kernel(MxArgs a) {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) sum[j] = __builtin_nanf("");
       }
-      store_row<BF16, C::FN>(a, (int64_t)r * a.N + col, col, whole, sum);
+      store_row<BF16, C::FN>(a, (int64_t)r * a.N + col, col, sum);
     }
   }
 }
@@ -819,9 +817,6 @@ __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
 
   // ---- outputs: lane c of operand j holds column FN c + j of its wave's columns ----
   const int col = t.n0 + wn * 16 * C::FN + C::FN * l16;
-  constexpr int ES = BF16 ? 2 : 4;
-  // all FN columns are inside or none, and their store aligned
-  const bool whole = a.N % C::FN == 0 && (reinterpret_cast<uintptr_t>(a.Y) & (C::FN * ES - 1)) == 0;
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
@@ -836,7 +831,7 @@ __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
         o[j] = acc[i][j][v];
         if (GROUPED && lost[rl]) o[j] = __builtin_nanf("");
       }
-      store_row<BF16, C::FN>(a, at, col, whole, o);
+      store_row<BF16, C::FN>(a, at, col, o);
     }
 }
 

@@ -360,8 +360,8 @@ aq_status aq_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64
  * Sums run in a fixed order: a call gives the same bits every time, and a row's outputs
  * do not depend on the other rows' values.
  * Errors: EINVAL for a bad y_dtype, M < 0 or M >= 2^30, N < 0 or N >= 2^22, K <= 0, K >=
- *         2^22 or K % 32, ldx < K or ldx % 8, NULL / misaligned pointers (X, codes 16
- *         bytes; Y two elements).
+ *         2^22 or K % 32, ldx < K or ldx % 8, M * N >= 2^37, X of 2^36 bytes or more, NULL /
+ *         misaligned pointers (X, codes 16 bytes; Y two elements).
  */
 aq_status aq_mxfp4_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
                         const uint8_t* scales, int64_t N, void* Y, int32_t y_dtype, void* stream);
@@ -380,7 +380,7 @@ aq_status aq_mxfp4_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scales, int6
  * outside offsets[0] .. offsets[E] - 1 are left as they were.  A list entry outside its
  * range never leads outside the buffers: offsets are clamped to 0 .. M and to be
  * ascending, a row of Y whose rows[r] is outside X becomes NaN.
- * Errors: as the products above; EINVAL also for E <= 0, E * N >= 2^27, M * N >= 2^38,
+ * Errors: as the products above; EINVAL also for E <= 0 or E >= 2^20, E * N >= 2^27,
  *         T < 0 or T >= 2^30, T < M without rows, T = 0 with M > 0, NULL / misaligned
  *         offsets or rows (4 bytes).
  */

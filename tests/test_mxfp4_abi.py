@@ -58,6 +58,18 @@ def test_products_einval(lib, kw):
             assert call(lib, a4, **kw) == _lib.AQ_EINVAL, (call, a4)
 
 
+def test_products_einval_of_sizes_past_the_offsets(lib):
+    """X's 16-byte units and the launch's threads are counted in 32 bits."""
+    for a4, K in ((False, 1 << 11), (True, 1 << 13)):   # rows of 4 KiB
+        for call, kw in ((_g, {}), (_e, dict(T=1 << 24))):
+            assert call(lib, a4, M=1 << 24, K=K, **kw) == _lib.AQ_EINVAL and "2^36" in _lib.last_error()
+        assert _e(lib, a4, T=1 << 24, K=K, M=4, rows=FAKE) == _lib.AQ_EINVAL and "2^36" in _lib.last_error()
+        for call, kw in ((_g, {}), (_e, dict(T=1 << 20))):
+            assert call(lib, a4, M=1 << 20, N=1 << 17, **kw) == _lib.AQ_EINVAL and "2^37" in _lib.last_error()
+    assert _g(lib, False, M=1 << 18, K=64, ldx=1 << 17) == _lib.AQ_EINVAL and "2^36" in _lib.last_error()
+    assert _e(lib, E=1 << 20, N=8) == _lib.AQ_EINVAL and "E out" in _lib.last_error()
+
+
 def test_products_einval_of_one_kind(lib):
     for call in (_g, _e):
         assert call(lib, True, XS=None) == _lib.AQ_EINVAL and "x_scales" in _lib.last_error()

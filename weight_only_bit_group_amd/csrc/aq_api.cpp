@@ -581,9 +581,11 @@ aq_status aq_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64
                         fn);
 }
 
-// X: bf16 rows ldx elements apart (x_scales NULL), or MXFP4 codes with x_scales
-static aq_status check_mx_product(const char* fn, const void* X, const uint8_t* x_scales, bool a4, int64_t M,
-                                  int64_t K, int64_t ldx, const uint8_t* codes, const uint8_t* scales, int64_t N,
+// X: T bf16 rows ldx elements apart (x_scales NULL), or MXFP4 codes with x_scales.  The kernels
+// count X in 16-byte units of 32 bits, and a launch of the largest tiles, a thread for 128
+// outputs, has fewer than 2^32 threads.
+static aq_status check_mx_product(const char* fn, const void* X, const uint8_t* x_scales, bool a4, int64_t T,
+                                  int64_t M, int64_t K, int64_t ldx, const uint8_t* codes, const uint8_t* scales, int64_t N,
                                   const void* Y, int32_t y_dtype) {
   AQ_REQUIRE(y_dtype == AQ_F32 || y_dtype == AQ_BF16, "%s: y_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, y_dtype);
   AQ_REQUIRE(M >= 0 && M < kDimLimit, "%s: M out of range (%lld)", fn, (long long)M);
@@ -593,6 +595,9 @@ static aq_status check_mx_product(const char* fn, const void* X, const uint8_t* 
   if (!a4)
     AQ_REQUIRE(ldx >= K && ldx < kDimLimit && ldx % 8 == 0, "%s: ldx (%lld) must be at least K and a multiple of 8", fn,
                (long long)ldx);
+  AQ_REQUIRE(T * (a4 ? K / 2 : ldx * 2) < (int64_t(1) << 36), "%s: X must be below 2^36 bytes (%lld rows)", fn,
+             (long long)T);
+  AQ_REQUIRE(M * N < (int64_t(1) << 37), "%s: M * N must be below 2^37 (M %lld, N %lld)", fn, (long long)M, (long long)N);
   AQ_PTR(X, 16, a4 ? "x_codes" : "X");
   if (a4) AQ_PTR(x_scales, 1, "x_scales");
   AQ_PTR(codes, 16, "codes");
@@ -604,7 +609,7 @@ static aq_status check_mx_product(const char* fn, const void* X, const uint8_t* 
 static aq_status mx_gemm(const char* fn, const void* X, const uint8_t* x_scales, bool a4, int64_t M, int64_t K,
                          int64_t ldx, const uint8_t* codes, const uint8_t* scales, int64_t N, void* Y, int32_t y_dtype,
                          void* stream) {
-  const aq_status st = check_mx_product(fn, X, x_scales, a4, M, K, ldx, codes, scales, N, Y, y_dtype);
+  const aq_status st = check_mx_product(fn, X, x_scales, a4, M, M, K, ldx, codes, scales, N, Y, y_dtype);
   if (st != AQ_OK) return st;
   if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
   if (M == 0 || N == 0) return ok();
@@ -628,13 +633,11 @@ static aq_status mx_grouped(const char* fn, const void* X, const uint8_t* x_scal
                             int64_t ldx, const uint8_t* codes, const uint8_t* scales, int64_t E, int64_t N,
                             const int32_t* offsets, const int32_t* rows, int64_t M, void* Y, int32_t y_dtype,
                             void* stream) {
-  const aq_status st = check_mx_product(fn, X, x_scales, a4, M, K, ldx, codes, scales, N, Y, y_dtype);
-  if (st != AQ_OK) return st;
-  AQ_REQUIRE(E > 0 && E < kDimLimit, "%s: E out of range (%lld)", fn, (long long)E);
-  AQ_REQUIRE(E * N < (int64_t(1) << 27) && M * N < (int64_t(1) << 38),
-             "%s: E * N must be below 2^27 and M * N below 2^38 (E %lld, M %lld, N %lld)", fn, (long long)E, (long long)M,
-             (long long)N);
   AQ_REQUIRE(T >= 0 && T < kDimLimit, "%s: T out of range (%lld)", fn, (long long)T);
+  const aq_status st = check_mx_product(fn, X, x_scales, a4, T, M, K, ldx, codes, scales, N, Y, y_dtype);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(E > 0 && E < (int64_t(1) << 20), "%s: E out of range (%lld)", fn, (long long)E);
+  AQ_REQUIRE(E * N < (int64_t(1) << 27), "%s: E * N must be below 2^27 (E %lld, N %lld)", fn, (long long)E, (long long)N);
   AQ_REQUIRE(M == 0 || (T > 0 && (rows != nullptr || T >= M)), "%s: X has %lld rows for %lld rows of Y", fn, (long long)T,
              (long long)M);
   AQ_PTR(offsets, 4, "offsets");

@@ -27,6 +27,8 @@
 // past the end are not stored.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
+#include <iterator>
 #include <type_traits>
 
 #include "aq_device.h"
@@ -145,9 +147,10 @@ __device__ __forceinline__ bool grouped_tile(const MxArgs& a, int tiles_n, int b
     incl = scan((hi - lo + BM - 1) / BM);
     total += __shfl(incl, 63, 64);
   }
-  const int64_t ntiles = (int64_t)total * tiles_n;
+  // (no more than the launch has blocks, unless overlapping offsets count rows twice)
+  const int ntiles = (int)min((int64_t)total * tiles_n, (int64_t)gridDim.x);
   if (block >= ntiles) return false;
-  const int t = tile_of_block(block, (int)ntiles);
+  const int t = tile_of_block(block, ntiles);
   const int mt = t / tiles_n;
   int base = 0;
   for (int e0 = 0; e0 < a.E; e0 += 64) {
@@ -271,6 +274,8 @@ struct MxSplit {
   static constexpr int SC = 16 / SB;                        // stages whose scale bytes are loaded at once
   static constexpr int PART = 4 * FM * FN * 64 * 4;         // bytes of a wave's sums
   static constexpr int LDS = NW * (R * STAGE > PART ? R * STAGE : PART);
+  static constexpr bool SPLIT = true;
+  static constexpr int PER_CU = std::max(1, std::min(160 * 1024 / LDS, 32 / NW));   // blocks that a compute unit holds
   static_assert((R - 1) * DMA < 64, "the loads in flight are counted in six bits");
 };
 
@@ -490,6 +495,9 @@ struct MxCfg {
   static constexpr int CB = 2 * SB;                  // and per row and chunk of two stages
   static constexpr int SROWS = A4 ? BM + BN : BN;    // rows of scale bytes
   static constexpr int SPT = (SROWS + NT - 1) / NT;  // of them per thread
+  static constexpr bool SPLIT = false;
+  // blocks that a compute unit holds; their registers leave room for 8 waves, or 12
+  static constexpr int PER_CU = std::max(1, std::min(160 * 1024 / (2 * (BM * XB + BN * WB)), (FM * FN >= 16 ? 8 : 12) / NW));
   static_assert(BM * XB % (1024 * NW) == 0 && BN * WB % (1024 * NW) == 0, "whole loads per wave");
 };
 
@@ -835,86 +843,113 @@ __global__ __launch_bounds__(C::NT, 1) void mxfp4_tile_kernel(MxArgs a) {
     }
 }
 
+// the most row tiles that a launch can have; grouped: at most one part-filled one per expert
+// with rows
 template <class C, bool GROUPED>
-hipError_t launch_tile(const MxArgs& a, bool y_bf16, hipStream_t stream) {
-  const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
-  // a grouped launch has at most one part-filled row tile per expert with rows
-  const int64_t tiles_m = GROUPED ? std::min<int64_t>(a.M, a.M / C::BM + a.E) : (a.M + C::BM - 1) / C::BM;
-  const dim3 grid((unsigned)(tiles_m * tiles_n)), block(C::NT);
-  if (y_bf16) hipLaunchKernelGGL((mxfp4_tile_kernel<C, GROUPED, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((mxfp4_tile_kernel<C, GROUPED, false>), grid, block, 0, stream, a);
-  return hipGetLastError();
+int64_t row_tiles(const MxArgs& a) {
+  return GROUPED ? std::min<int64_t>(a.M, a.M / C::BM + a.E) : (a.M + C::BM - 1) / C::BM;
 }
 
 template <class C, bool GROUPED>
-hipError_t launch_split(const MxArgs& a, bool y_bf16, hipStream_t stream) {
+hipError_t launch(const MxArgs& a, bool y_bf16, hipStream_t stream) {
   const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
-  const int64_t tiles_m = GROUPED ? std::min<int64_t>(a.M, a.M / C::BM + a.E) : (a.M + C::BM - 1) / C::BM;
-  const dim3 grid((unsigned)(tiles_m * tiles_n)), block(C::NT);
-  auto launch = [&](auto kernel, std::atomic<uint64_t>& done) -> hipError_t {
-    if (C::LDS > 64 * 1024) {
-      // the kernel's limit of dynamic LDS, raised once per device (bit d of done)
-      int dev = 0;
-      hipError_t e = hipGetDevice(&dev);
-      if (e != hipSuccess) return e;
-      const uint64_t bit = uint64_t(1) << (dev & 63);
-      if (!(done.load(std::memory_order_acquire) & bit)) {
-        e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+  const dim3 grid((unsigned)(row_tiles<C, GROUPED>(a) * tiles_n)), block(C::NT);
+  if constexpr (C::SPLIT) {
+    auto run = [&](auto kernel, std::atomic<uint64_t>& done) -> hipError_t {
+      if (C::LDS > 64 * 1024) {
+        // the kernel's limit of dynamic LDS, raised once per device (bit d of done)
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
         if (e != hipSuccess) return e;
-        done.fetch_or(bit, std::memory_order_acq_rel);
+        const uint64_t bit = uint64_t(1) << (dev & 63);
+        if (!(done.load(std::memory_order_acquire) & bit)) {
+          e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+          if (e != hipSuccess) return e;
+          done.fetch_or(bit, std::memory_order_acq_rel);
+        }
       }
-    }
-    hipLaunchKernelGGL(kernel, grid, block, C::LDS, stream, a);
+      hipLaunchKernelGGL(kernel, grid, block, C::LDS, stream, a);
+      return hipGetLastError();
+    };
+    static std::atomic<uint64_t> done_bf16{0}, done_f32{0};
+    return y_bf16 ? run(mxfp4_split_kernel<C, GROUPED, true>, done_bf16) : run(mxfp4_split_kernel<C, GROUPED, false>, done_f32);
+  } else {
+    if (y_bf16) hipLaunchKernelGGL((mxfp4_tile_kernel<C, GROUPED, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((mxfp4_tile_kernel<C, GROUPED, false>), grid, block, 0, stream, a);
     return hipGetLastError();
-  };
-  static std::atomic<uint64_t> done_bf16{0}, done_f32{0};
-  return y_bf16 ? launch(mxfp4_split_kernel<C, GROUPED, true>, done_bf16) : launch(mxfp4_split_kernel<C, GROUPED, false>, done_f32);
+  }
 }
 
-// The form of a product by its sizes: from the largest tile to the smallest, the first one
-// that is not twice as high as the rows of a product (grouped: their mean over the experts
-// that can have any; 64 x 128 may be) and gives enough blocks for the device.
-//   Two thirds of the compute units are enough for A4, whose larger tiles gain more than the
-// idle units lose (M = 1024 on [11008, 2048]: 172 tiles of 256 x 256 22.2 us, 688 of 128 x
-// 128 25.6; M = 128: 172 of 64 x 128 9.7, 344 of 64 x 32 12.4); A16's tiles above 64 x 64
-// want 4/3 (M = 1024: 50.7 against 46.6 us; M = 128: 17.2 against 15.2 with 344 of 64 x 64).
-//   Of the forms that share K, tall ones for few tiles (M = 64 on [2048, 2048]: 16 x 32 4.3
-// us, 64 x 32 over 5.1), wide ones where 16 rows already give thousands of tiles (512 rows
-// over 128 experts of [2048, 1024]: 16 x 64 34, 16 x 16 86 us).
-//   Their waves: four; eight, and sixteen for 16 x 16, over rows of more than 4096 k (M = 16
-// on [4096, 14336]: 8.7 against 11.3 us for A4, 14.3 against 20.0 for A16); one where the
-// tiles alone fill the device many times over (the 128 experts above: 34 against 42 us).
+// The form of a product: the one whose estimated time is the least,
+//   fixed + r (round + stage * stages of a wave) + mb * (MB through LDS-DMA)     [us]
+// with r = the tiles over those that the device holds at once, at least 1: a block takes its
+// run of stages whether or not others run beside it, and every tile adds its traffic.
+//   The four figures of a form are least-squares fits of the relative error to graph-replayed
+// times of 520 products (drawn ones, M to 4100, N and K to 14400, to 100 experts; and M = 1 to
+// 4096 on weights of 1024 to 14336 rows and columns, 8 to 128 experts with 1 to 256 rows each),
+// of 27 forms.  The forms kept lose 4% (A4) and 5% (A16) of geometric-mean time against the best of
+// the 27; a rule on tile counts alone lost 12 and 14% on the drawn ones.  Both sides, us:
+//   M = 64 on [2048, 2048], A4: 16 x 16 over 4 waves 6.1, 32 x 64 6.5, tiles of 64 x 128 7.6
+//   M = 128 on [11008, 2048], A4: tiles of 64 x 128 9.0, of 128 x 128 9.9, 32 x 64 11.4;
+//     A16: 64 x 64 over 4 waves 14.8, tiles of 64 x 128 16.1, 32 x 32 over 8 waves 18.8
+//   M = 1024 there, A4: tiles of 256 x 256 21.9, of 128 x 128 25.0; A16: 49.5 against 46.4
+//   M = 16 on [4096, 14336]: 16 x 16 over 16 waves 7.7 (A4) and 14.7 (A16), over 4 10.9 and 20.3
+//   4 rows for each of 128 experts of [4096, 2048], A4: 16 x 64 by one wave 101, 16 x 16 over
+//     4 waves 182
+struct MxCost {
+  float fixed, round, stage, mb;
+};
+
+template <class C, bool GROUPED>
+float estimate(const MxArgs& a, MxCost c) {
+  const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
+  if (row_tiles<C, GROUPED>(a) * tiles_n >= (int64_t(1) << 32) / C::NT) return INFINITY;   // threads of a launch
+  // grouped: every expert's last tile half filled, the lists being on the device
+  const float products = (float)std::min(a.M, a.E);
+  const float tiles = (float)tiles_n * (GROUPED ? std::max(products, (float)a.M / C::BM + 0.5f * products)
+                                                : (float)row_tiles<C, GROUPED>(a));
+  const int64_t stages = (a.K + C::KS - 1) / C::KS, mine = C::SPLIT ? (stages + C::NW - 1) / C::NW : stages;
+  const float r = std::max(1.0f, tiles / (float)(device_cu_count() * C::PER_CU));
+  const float mb = 1e-6f * tiles * (float)(mine * (C::SPLIT ? C::NW : 1)) * (float)(C::BM * 128 + C::BN * C::WB);
+  return c.fixed + r * (c.round + c.stage * (float)mine) + c.mb * mb;
+}
+
+template <class C>   // MxSplit or MxCfg
+struct MxForm {
+  MxCost cost;
+};
+
+template <bool GROUPED, class... C>
+hipError_t launch_least(const MxArgs& a, bool y_bf16, hipStream_t stream, MxForm<C>... form) {
+  using Fn = hipError_t (*)(const MxArgs&, bool, hipStream_t);
+  const float t[] = {estimate<C, GROUPED>(a, form.cost)...};
+  const Fn fn[] = {launch<C, GROUPED>...};
+  return fn[std::min_element(std::begin(t), std::end(t)) - std::begin(t)](a, y_bf16, stream);
+}
+
 template <bool A4, bool GROUPED>
 hipError_t launch_any(const MxArgs& a, bool y_bf16, hipStream_t stream) {
-  const int64_t cus = device_cu_count();
-  const int64_t products = GROUPED ? std::min(a.M, a.E) : 1;
-  const int64_t per = (a.M + products - 1) / products;
-  auto fits = [&](int64_t bm, int64_t bn, int64_t thirds) {
-    return bm < 2 * per + (bm == 64 && bn == 128) && 3 * products * ((per + bm - 1) / bm) * ((a.N + bn - 1) / bn) >= thirds * cus;
-  };
-  const bool longk = a.K > 4096;
-  if (per > 16) {
-    if (fits(256, 256, A4 ? 2 : 4)) return launch_tile<MxCfg<A4, 2, 4, 8, 4>, GROUPED>(a, y_bf16, stream);
-    if (fits(128, 128, A4 ? 2 : 4)) return launch_tile<MxCfg<A4, 2, 2, 4, 4>, GROUPED>(a, y_bf16, stream);
-    if (fits(64, 128, A4 ? 2 : 4))
-      return launch_tile<std::conditional_t<A4, MxCfg<A4, 2, 2, 2, 4>, MxCfg<A4, 1, 4, 4, 2>>, GROUPED>(a, y_bf16, stream);
-    if constexpr (!A4) {
-      if (!longk && fits(64, 64, 2)) return launch_split<MxSplit<A4, 4, 4, 4, 1>, GROUPED>(a, y_bf16, stream);
-    }
-    if (fits(64, 32, 2))
-      return longk ? launch_split<MxSplit<A4, 4, 2, 8, 1>, GROUPED>(a, y_bf16, stream)
-                   : launch_split<MxSplit<A4, 4, 2, 4, 1>, GROUPED>(a, y_bf16, stream);
-    if (fits(32, 32, 2) || per > 256)
-      return longk ? launch_split<MxSplit<A4, 2, 2, 8, 1>, GROUPED>(a, y_bf16, stream)
-                   : launch_split<MxSplit<A4, 2, 2, 4, 2>, GROUPED>(a, y_bf16, stream);
-    return longk ? launch_split<MxSplit<A4, 1, 2, 8, 2>, GROUPED>(a, y_bf16, stream)
-                 : launch_split<MxSplit<A4, 1, 2, 4, 2>, GROUPED>(a, y_bf16, stream);
-  }
-  const int64_t wide = products * ((a.N + 63) / 64);   // tiles of 16 x 64
-  if (wide >= 16 * cus) return launch_split<MxSplit<A4, 1, 4, 1, 2>, GROUPED>(a, y_bf16, stream);
-  if (wide >= 4 * cus) return launch_split<MxSplit<A4, 1, 4, 4, 1>, GROUPED>(a, y_bf16, stream);
-  return longk ? launch_split<MxSplit<A4, 1, 1, 16, 2>, GROUPED>(a, y_bf16, stream)
-               : launch_split<MxSplit<A4, 1, 1, 4, 2>, GROUPED>(a, y_bf16, stream);
+  if constexpr (A4)
+    return launch_least<GROUPED>(a, y_bf16, stream,
+                                 MxForm<MxSplit<A4, 1, 1, 16, 2>>{2.97f, 2.02f, 0.363f, 0.023f},
+                                 MxForm<MxSplit<A4, 1, 1, 4, 2>>{2.47f, 2.38f, 0.189f, 0.042f},
+                                 MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.56f, 4.86f, 0.620f, 0.044f},
+                                 MxForm<MxSplit<A4, 2, 4, 4, 1>>{0.00f, 5.89f, 0.690f, 0.053f},
+                                 MxForm<MxSplit<A4, 4, 2, 8, 1>>{2.28f, 3.88f, 0.994f, 0.022f},
+                                 MxForm<MxCfg<A4, 2, 2, 2, 4>>{0.00f, 5.07f, 0.349f, 0.077f},
+                                 MxForm<MxCfg<A4, 2, 2, 4, 4>>{0.00f, 6.04f, 0.523f, 0.057f},
+                                 MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 9.06f, 1.114f, 0.063f});
+  else
+    return launch_least<GROUPED>(a, y_bf16, stream,
+                                 MxForm<MxSplit<A4, 1, 1, 16, 2>>{2.83f, 2.05f, 0.429f, 0.022f},
+                                 MxForm<MxSplit<A4, 1, 1, 4, 2>>{3.27f, 1.59f, 0.188f, 0.034f},
+                                 MxForm<MxSplit<A4, 1, 2, 4, 2>>{2.77f, 2.12f, 0.236f, 0.043f},
+                                 MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.00f, 5.65f, 0.321f, 0.060f},
+                                 MxForm<MxSplit<A4, 2, 2, 8, 1>>{1.66f, 3.36f, 0.304f, 0.049f},
+                                 MxForm<MxSplit<A4, 4, 4, 4, 1>>{1.40f, 4.94f, 0.580f, 0.035f},
+                                 MxForm<MxCfg<A4, 1, 4, 4, 2>>{1.63f, 3.32f, 0.322f, 0.061f},
+                                 MxForm<MxCfg<A4, 2, 2, 4, 4>>{0.84f, 5.20f, 0.483f, 0.039f},
+                                 MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 8.97f, 1.022f, 0.057f});
 }
 
 }  // namespace

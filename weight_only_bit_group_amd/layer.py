@@ -25,6 +25,9 @@ this module only arranges tensors and swaps modules.
     configuration, and a policy target outside the layers selected by
     target_modules is an error at parse time; "共同约定": explicit errors for a
     model without linears, targets that match nothing, and re-quantization).
+  * ``MXFP4Linear`` and ``MXFP4Experts``: weights in MXFP4 blocks of 32, the
+    activations kept in bf16 or quantized to MXFP4 on the way in; the experts of
+    a mixture run as two products grouped by expert.
 """
 from __future__ import annotations
 
@@ -110,7 +113,7 @@ class W4A16Linear(torch.nn.Module):
 
 
 def _weight_of(linear) -> torch.Tensor:
-    if isinstance(linear, W4A16Linear):
+    if isinstance(linear, (W4A16Linear, MXFP4Linear)):
         raise ValueError("layer is already quantized")
     if not isinstance(linear, torch.nn.Linear):
         raise TypeError(f"expected torch.nn.Linear, got {type(linear).__name__}")
@@ -199,6 +202,154 @@ class W8A16Linear(torch.nn.Module):
         return f"in_features={self.in_features}, out_features={self.out_features}, group={self.group}, bits=8"
 
 
+def _mx_act(act: str) -> str:
+    if act not in ("bf16", "mxfp4"):
+        raise ValueError(f"act must be 'bf16' or 'mxfp4' (got {act!r})")
+    return act
+
+
+def _mx_pair(codes: torch.Tensor, scales: torch.Tensor, name: str, ndim: int) -> None:
+    """Checks codes [.., N, K/2] and scales [.., N, K/32], both uint8."""
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError(f"{name}: codes and scales must be uint8")
+    if codes.dim() != ndim or codes.shape[-1] == 0 or codes.shape[-1] % 16 \
+            or scales.shape != (*codes.shape[:-1], codes.shape[-1] // 16):
+        raise ValueError(f"{name}: codes [.., N, K/2] and scales [.., N, K/32] expected "
+                         f"(got {list(codes.shape)} and {list(scales.shape)})")
+
+
+def _mx_rounded(x2: torch.Tensor, act: str):
+    """The product's activation arguments: bf16 rows, or the codes and scales of rows in their own type."""
+    if act == "bf16":
+        return (x2.to(torch.bfloat16),)
+    return B.aq_mxfp4_quantize(x2 if x2.dtype in (torch.bfloat16, torch.float32) else x2.float())
+
+
+def _mx_rows(x: torch.Tensor, k: int) -> torch.Tensor:
+    """x [.., K] as a matrix whose rows start at 16-byte addresses, copied only if they do not."""
+    if x.shape[-1] != k:
+        raise ValueError(f"expected {k} input features, got {x.shape[-1]}")
+    x2 = x.reshape(-1, k)
+    size = x2.element_size()
+    if x2.stride(1) != 1 or x2.stride(0) < k or x2.stride(0) * size % 16 or x2.data_ptr() % 16:
+        x2 = x2.contiguous()
+        if x2.data_ptr() % 16:   # a dense slice that starts off the alignment
+            x2 = x2.clone()
+    return x2
+
+
+class MXFP4Linear(torch.nn.Module):
+    """y = x W^T (+ bias) with W in MXFP4 (codes [N, K/2], scales [N, K/32]).
+
+    act="bf16" casts the input to bf16; act="mxfp4" quantizes it row by row to MXFP4, which
+    runs on the block-scaled matrix instructions (four times the bf16 rate, coarser inputs).
+    The output is fp32.
+    """
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None,
+                 act: str = "bf16"):
+        super().__init__()
+        _mx_pair(codes, scales, "MXFP4Linear", 2)
+        self.act = _mx_act(act)
+        self.in_features = codes.shape[1] * 2
+        self.out_features = codes.shape[0]
+        self.register_buffer("codes", codes.contiguous())
+        self.register_buffer("scales", scales.contiguous())
+        self.register_buffer("bias", None if bias is None else bias.detach().float().contiguous())
+
+    @classmethod
+    def from_weight(cls, weight: torch.Tensor, bias: torch.Tensor | None = None, act: str = "bf16") -> "MXFP4Linear":
+        """Quantize W [N, K] (fp32 or bf16, on the GPU; K a multiple of 32)."""
+        _mx_act(act)
+        return cls(*B.aq_mxfp4_quantize(weight.detach().contiguous()), bias, act)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        x2 = _mx_rounded(_mx_rows(x, self.in_features), self.act)
+        product = B.aq_mxfp4_gemm if self.act == "bf16" else B.aq_mxfp4_gemm_a4
+        y = product(*x2, self.codes, self.scales)
+        if self.bias is not None:
+            y += self.bias
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+    def extra_repr(self) -> str:
+        return f"in_features={self.in_features}, out_features={self.out_features}, weights=mxfp4, act={self.act}"
+
+
+class MXFP4Experts(torch.nn.Module):
+    """The experts of a mixture, gated MLPs with MXFP4 weights:
+
+        y[t] = sum_j w[t, j] D_e (silu(G_e x[t]) * (U_e x[t])),   e = ids[t, j]
+
+    gate_up holds [G_e; U_e] as codes [E, 2I, K/2] and scales [E, 2I, K/32], down D_e as codes
+    [E, K, I/2] and scales [E, K, I/32].  ``forward(x, ids, weights)`` takes x [.., K] with the
+    router's choices ids [.., top] (any integer type) and weights [.., top]; a choice outside
+    0 .. E - 1 (the filling of a padded batch, an expert of another rank) adds nothing.
+    Both layers run as one product grouped by expert each, for all tokens, without reading a
+    count back to the host.  A token's products are added in the order of its choices, in
+    fp32: the result does not depend on how its choices were grouped.  The output is fp32.
+    """
+
+    def __init__(self, gate_up_codes: torch.Tensor, gate_up_scales: torch.Tensor, down_codes: torch.Tensor,
+                 down_scales: torch.Tensor, act: str = "bf16"):
+        super().__init__()
+        _mx_pair(gate_up_codes, gate_up_scales, "gate_up", 3)
+        _mx_pair(down_codes, down_scales, "down", 3)
+        self.act = _mx_act(act)
+        self.num_experts, rows, half = gate_up_codes.shape
+        self.features, self.inner = 2 * half, 2 * down_codes.shape[2]
+        if rows != 2 * self.inner or tuple(down_codes.shape[:2]) != (self.num_experts, self.features):
+            raise ValueError(f"gate_up [E, 2I, K] and down [E, K, I] expected, codes are {list(gate_up_codes.shape)} "
+                             f"and {list(down_codes.shape)}")
+        self.register_buffer("gate_up_codes", gate_up_codes.contiguous())
+        self.register_buffer("gate_up_scales", gate_up_scales.contiguous())
+        self.register_buffer("down_codes", down_codes.contiguous())
+        self.register_buffer("down_scales", down_scales.contiguous())
+
+    @classmethod
+    def from_weights(cls, gate_up: torch.Tensor, down: torch.Tensor, act: str = "bf16") -> "MXFP4Experts":
+        """Quantize gate_up [E, 2I, K] and down [E, K, I] (fp32 or bf16, on the GPU)."""
+        _mx_act(act)
+        pairs = []
+        for w, name in ((gate_up, "gate_up"), (down, "down")):
+            if w.dim() != 3:
+                raise ValueError(f"{name} must have 3 dimensions")
+            codes, scales = B.aq_mxfp4_quantize(w.detach().reshape(-1, w.shape[2]).contiguous())
+            pairs += [codes.view(*w.shape[:2], -1), scales.view(*w.shape[:2], -1)]
+        return cls(*pairs, act)
+
+    def forward(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor) -> torch.Tensor:
+        x2 = _mx_rows(x, self.features)
+        t = x2.shape[0]
+        if ids.shape != weights.shape or ids.shape[:-1] != x.shape[:-1] or ids.dim() < 1 or ids.shape[-1] == 0:
+            raise ValueError(f"ids and weights must be {[*x.shape[:-1], 'top']} (got {list(ids.shape)} and "
+                             f"{list(weights.shape)})")
+        if ids.is_floating_point() or ids.dtype == torch.bool:
+            raise ValueError(f"ids must be integers (got {ids.dtype})")
+        top = ids.shape[-1]
+        flat = ids.reshape(-1).long()
+        valid = (flat >= 0) & (flat < self.num_experts)
+        # choices sorted by expert, those outside the range behind the last one
+        key, order = torch.where(valid, flat, self.num_experts).sort(stable=True)
+        edges = torch.arange(self.num_experts + 1, device=key.device, dtype=key.dtype)
+        offsets = torch.searchsorted(key, edges, out_int32=True)
+        rows = (order // top).int()
+        product = B.aq_mxfp4_grouped_gemm if self.act == "bf16" else B.aq_mxfp4_grouped_gemm_a4
+        h = product(*_mx_rounded(x2, self.act), self.gate_up_codes, self.gate_up_scales, offsets, rows)
+        h = torch.nn.functional.silu(h[:, :self.inner]) * h[:, self.inner:]
+        y = product(*_mx_rounded(h, self.act), self.down_codes, self.down_scales, offsets)
+        back = torch.empty_like(order)
+        back[order] = torch.arange(order.shape[0], device=order.device)
+        # (the rows behind the last expert were never written)
+        y = torch.where(valid[:, None], y[back], 0.0).view(t, top, self.features)
+        out = y[:, 0] * weights.reshape(t, top)[:, :1].float()
+        for j in range(1, top):
+            out += y[:, j] * weights.reshape(t, top)[:, j:j + 1].float()
+        return out.reshape(*x.shape[:-1], self.features)
+
+    def extra_repr(self) -> str:
+        return f"experts={self.num_experts}, features={self.features}, inner={self.inner}, weights=mxfp4, act={self.act}"
+
+
 @dataclass(frozen=True)
 class LayerQuantPolicy:
     """Per-layer override of the base configuration; None fields inherit it."""
@@ -223,7 +374,7 @@ def plan_quantization(model: torch.nn.Module, target_modules, bits: int = 4, gro
     symmetric, 8-bit asymmetric).
     """
     named = dict(model.named_modules())
-    quantized = [n for n, m in named.items() if isinstance(m, (W4A16Linear, W8A16Linear))]
+    quantized = [n for n, m in named.items() if isinstance(m, (W4A16Linear, W8A16Linear, MXFP4Linear))]
     linears = [n for n, m in named.items() if isinstance(m, torch.nn.Linear)]
     if not linears and not quantized:
         raise ValueError("the model contains no torch.nn.Linear")

@@ -158,7 +158,7 @@ def _untouched(whole, n):
     return bool((whole[:256] == 77).all()) and bool((whole[256 + n:] == 77).all())
 
 
-SIZES = [(1, 1, 32), (1, 16, 64), (1, 17, 96), (2, 250, 128), (3, 33, 160), (16, 48, 512), (15, 100, 544), (17, 64, 480),
+SIZES = [(1, 1, 32), (1, 16, 64), (1, 17, 96), (1, 250, 2080), (1, 33, 8192), (1, 7, 14336), (1, 4099, 544), (2, 250, 128), (3, 33, 160), (16, 48, 512), (15, 100, 544), (17, 64, 480),
          (31, 65, 1024), (32, 127, 1056), (33, 200, 2048), (48, 130, 2080), (64, 96, 4128), (65, 128, 256), (64, 129, 288),
          (100, 255, 992), (128, 257, 544), (129, 256, 64), (256, 384, 512), (257, 300, 1056), (300, 513, 96),
          (513, 256, 2048), (700, 1003, 736)]
@@ -207,7 +207,7 @@ def synth_weight(rng, n, k):
 
 
 @pytest.mark.parametrize("a4", [False, True])
-@pytest.mark.parametrize("m", [3, 40, 200, 300])
+@pytest.mark.parametrize("m", [1, 3, 40, 200, 300])
 def test_far_apart_factors(m, a4):
     """Factors from 2^-120 to 2^110 in one matrix; a weight or activation factor that is NaN."""
     n, k = 70, 576
@@ -325,6 +325,45 @@ def test_grouped_rows_outside_and_lists_out_of_range(m, a4):
     ref = O.grouped_forward(xv, c, s, np.clip(wild, 0, m), rows)
     y = _np(_grouped(a4)(*x, dev(c), dev(s), dev(wild), rows=dev(rows)))
     assert np.array_equal(y, ref)
+
+
+@pytest.mark.parametrize("a4", [False, True])
+@pytest.mark.parametrize("n,k", [(37, 96), (50, 2080), (9, 9248)])
+def test_grouped_of_single_rows(n, k, a4):
+    """A token's experts: a row each, the same activation row for all, experts without one, one lost, short and long k."""
+    rng = np.random.default_rng(n)
+    e, t, m = 70, 3, 9
+    c, s = _weights(rng, e, n, k=k, lo=126, hi=129)
+    x, xv = _act(rng, t, k, a4, True)
+    chosen = np.sort(rng.permutation(e)[:m - 2])
+    off = np.searchsorted(chosen, np.arange(e + 1)).astype(np.int32) + 1   # row 0 and the last belong to none
+    rows = np.full(m, 2, np.int32)
+    ref = O.grouped_forward(xv, c, s, off, rows)
+    rows[4] = 3   # outside X
+    for dtype in (F32, BF16):
+        out, whole = _guarded(m, n, dtype)
+        step(f"mxfp4 grouped single rows {n}x{k} a4={a4} {dtype}")
+        y = _np(_grouped(a4)(*x, dev(c), dev(s), dev(off), rows=dev(rows), out=out))
+        want = torch.from_numpy(ref).to(F32).to(dtype).double().numpy()
+        want[[0, m - 1]], want[4] = 77, np.nan
+        assert np.array_equal(y, want, equal_nan=True)
+        assert _untouched(whole, m * n)
+
+
+@pytest.mark.parametrize("a4", [False, True])
+@pytest.mark.parametrize("m", [7, 200])
+def test_grouped_with_offsets_out_of_order(m, a4):
+    """Offsets that descend or overlap: whatever the rows hold, nothing outside Y is written."""
+    rng = np.random.default_rng(m)
+    e, n, k = 5, 40, 64
+    c, s = _weights(rng, e, n, k=k, lo=126, hi=129)
+    x, _ = _act(rng, m, k, a4, True)
+    for off in ([m, 0, m, 0, m, 0], [0, m, 0, m, 0, m], [-2 ** 31, 2 ** 31 - 1, -1, m + 1, 2, 1]):
+        out, whole = _guarded(m, n, F32)
+        step(f"mxfp4 grouped offsets {off} a4={a4}")
+        _grouped(a4)(*x, dev(c), dev(s), dev(np.array(off, np.int32)), out=out)
+        torch.cuda.synchronize()
+        assert _untouched(whole, m * n)
 
 
 def test_grouped_with_one_expert_is_the_product():

@@ -233,6 +233,132 @@ __device__ __forceinline__ i32x8 codes8(u32x4 v) {
   return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
 }
 
+// ---- one row, A16 --------------------------------------------------------------------------
+// Bound by the weight bytes, so every wave has all it can in flight: NR weight rows, a 16-byte
+// unit (a block of 32 k) of each per lane and 2048 k, straight to registers, the next 2048 k
+// requested before these are used.  The products are fp32 fused multiply-adds of the weights'
+// exact fp32 values (1.5 VALU operations a weight; the matrix instructions of the form below
+// would leave 15 of 16 rows empty, and its LDS ring holds fewer bytes in flight: one row on
+// [11008, 2048] 6.9 against 5.8 us, on [2048, 11008] 9.8 against 6.3, 8 experts' rows of
+// [1536, 2048] 8.6 against 6.5, graph-replayed; two rows 6.9 against 7.1).  NW waves of a block
+// share long rows ([2048, 11008] by one wave each 9.8), their sums are added in wave order.
+template <int NR_, int NW_>
+struct MxVec {
+  static constexpr bool SPLIT = true, VEC = true;
+  static constexpr int NR = NR_, NW = NW_;
+  static constexpr int NT = 256;
+  static constexpr int BM = 1, BN = 4 / NW * NR;
+  static constexpr int KS = 2048;
+  static constexpr int TILE_BYTES = 4096 + 1088 * BN;   // a stage's activations, codes and scale bytes
+  static constexpr int PER_CU = 8;                      // blocks that a compute unit holds
+  static_assert(4 % NW == 0, "whole groups of waves");
+};
+
+template <class C, bool GROUPED, bool BF16>
+__global__ __launch_bounds__(C::NT) void mxfp4_gemv_kernel(MxArgs a) {
+  __shared__ float part[C::NW > 1 ? 4 * C::NR : 1];
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles_n = (a.N + C::BN - 1) / C::BN;
+  MxTile t;
+  if constexpr (GROUPED) {
+    if (!grouped_tile<C::BM>(a, tiles_n, C::BN, blockIdx.x, t)) return;   // the whole block
+  } else {
+    const int i = tile_of_block(blockIdx.x, a.M * tiles_n);
+    t.e = 0;
+    t.r0 = i % a.M;
+    t.n0 = (i / a.M) * C::BN;
+  }
+  const int nblk = a.K >> 5;
+  const int n0 = t.n0 + wid / C::NW * C::NR;
+  const uint8_t *wrow[C::NR], *srow[C::NR];
+#pragma unroll
+  for (int r = 0; r < C::NR; ++r) {
+    const int64_t n = (int64_t)t.e * a.N + min(n0 + r, a.N - 1);
+    wrow[r] = a.W + n * (a.K >> 1);
+    srow[r] = a.WS + n * nblk;
+  }
+  const int src = GROUPED ? source_row(a, t.r0) : t.r0;
+  const uint8_t* xrow = a.X + (int64_t)max(src, 0) * a.xrow;
+
+  float acc[C::NR];
+#pragma unroll
+  for (int r = 0; r < C::NR; ++r) acc[r] = 0.0f;
+  u32x4 w[C::NR];
+  uint32_t sc[C::NR];
+  auto fetch = [&](int b0) {
+    const int b = min(b0 + lane, nblk - 1);
+#pragma unroll
+    for (int r = 0; r < C::NR; ++r) {
+      w[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow[r] + 16 * b));
+      sc[r] = srow[r][b];
+    }
+  };
+  int b0 = 64 * (wid % C::NW);
+  if (b0 < nblk) fetch(b0);
+  for (; b0 < nblk; b0 += 64 * C::NW) {
+    const int b = min(b0 + lane, nblk - 1);
+    u32x4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = *reinterpret_cast<const u32x4*>(xrow + 64 * b + 16 * i);
+      if (b0 + lane >= nblk) x[i] = u32x4{0, 0, 0, 0};   // past the row
+    }
+    u32x4 wnow[C::NR];
+    float f[C::NR];
+#pragma unroll
+    for (int r = 0; r < C::NR; ++r) {
+      wnow[r] = w[r];
+      f[r] = __uint_as_float(sc[r] << 23);
+    }
+    if (b0 + 64 * C::NW < nblk) fetch(b0 + 64 * C::NW);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float xf[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        xf[2 * j] = __uint_as_float(x[i][j] << 16);
+        xf[2 * j + 1] = __uint_as_float(x[i][j] & 0xffff0000u);
+      }
+#pragma unroll
+      for (int r = 0; r < C::NR; ++r) {
+        const uint32_t c = wnow[r][i];
+        const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, f[r], 0);
+        const auto v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, f[r], 1);
+        const auto v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, f[r], 2);
+        const auto v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, f[r], 3);
+        const float v[8] = {v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[r] = __builtin_fmaf(xf[j], v[j], acc[r]);
+      }
+    }
+  }
+
+  wave_sums<C::NR>(acc);
+  auto store = [&](int r, float v) {
+    if (n0 + r < a.N) store_one<BF16>(a.Y, (int64_t)t.r0 * a.N + n0 + r, src < 0 ? __builtin_nanf("") : v);
+  };
+  const bool owner = wave_sums_owner<C::NR>(lane);
+  if constexpr (C::NW == 1) {
+    if (owner) {
+#pragma unroll
+      for (int j = 0; j < wave_sums_out<C::NR>; ++j) store(wave_sums_index<C::NR>(j, lane >> 4), acc[j]);
+    }
+  } else {
+    if (owner) {
+#pragma unroll
+      for (int j = 0; j < wave_sums_out<C::NR>; ++j) part[wid * C::NR + wave_sums_index<C::NR>(j, lane >> 4)] = acc[j];
+    }
+    __syncthreads();
+    if (wid % C::NW == 0 && lane < C::NR) {
+      float v = part[wid * C::NR + lane];
+#pragma unroll
+      for (int w = 1; w < C::NW; ++w) v += part[(wid + w) * C::NR + lane];
+      store(lane, v);
+    }
+  }
+}
+
 // ---- few rows -----------------------------------------------------------------------------
 // Bound by the weight bytes (and from some ten rows on by the activation bytes that every
 // block reads from its L2).  A block's NW waves share K: each takes a contiguous run of
@@ -274,7 +400,8 @@ struct MxSplit {
   static constexpr int SC = 16 / SB;                        // stages whose scale bytes are loaded at once
   static constexpr int PART = 4 * FM * FN * 64 * 4;         // bytes of a wave's sums
   static constexpr int LDS = NW * (R * STAGE > PART ? R * STAGE : PART);
-  static constexpr bool SPLIT = true;
+  static constexpr bool SPLIT = true, VEC = false;
+  static constexpr int TILE_BYTES = BM * 128 + BN * WB;
   static constexpr int PER_CU = std::max(1, std::min(160 * 1024 / LDS, 32 / NW));   // blocks that a compute unit holds
   static_assert((R - 1) * DMA < 64, "the loads in flight are counted in six bits");
 };
@@ -495,7 +622,8 @@ struct MxCfg {
   static constexpr int CB = 2 * SB;                  // and per row and chunk of two stages
   static constexpr int SROWS = A4 ? BM + BN : BN;    // rows of scale bytes
   static constexpr int SPT = (SROWS + NT - 1) / NT;  // of them per thread
-  static constexpr bool SPLIT = false;
+  static constexpr bool SPLIT = false, VEC = false;
+  static constexpr int TILE_BYTES = BM * XB + BN * WB;
   // blocks that a compute unit holds; their registers leave room for 8 waves, or 12
   static constexpr int PER_CU = std::max(1, std::min(160 * 1024 / (2 * (BM * XB + BN * WB)), (FM * FN >= 16 ? 8 : 12) / NW));
   static_assert(BM * XB % (1024 * NW) == 0 && BN * WB % (1024 * NW) == 0, "whole loads per wave");
@@ -854,7 +982,11 @@ template <class C, bool GROUPED>
 hipError_t launch(const MxArgs& a, bool y_bf16, hipStream_t stream) {
   const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
   const dim3 grid((unsigned)(row_tiles<C, GROUPED>(a) * tiles_n)), block(C::NT);
-  if constexpr (C::SPLIT) {
+  if constexpr (C::VEC) {
+    if (y_bf16) hipLaunchKernelGGL((mxfp4_gemv_kernel<C, GROUPED, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((mxfp4_gemv_kernel<C, GROUPED, false>), grid, block, 0, stream, a);
+    return hipGetLastError();
+  } else if constexpr (C::SPLIT) {
     auto run = [&](auto kernel, std::atomic<uint64_t>& done) -> hipError_t {
       if (C::LDS > 64 * 1024) {
         // the kernel's limit of dynamic LDS, raised once per device (bit d of done)
@@ -887,8 +1019,10 @@ hipError_t launch(const MxArgs& a, bool y_bf16, hipStream_t stream) {
 //   The four figures of a form are least-squares fits of the relative error to graph-replayed
 // times of 520 products (drawn ones, M to 4100, N and K to 14400, to 100 experts; and M = 1 to
 // 4096 on weights of 1024 to 14336 rows and columns, 8 to 128 experts with 1 to 256 rows each),
-// of 27 forms.  The forms kept lose 4% (A4) and 5% (A16) of geometric-mean time against the best of
-// the 27; a rule on tile counts alone lost 12 and 14% on the drawn ones.  Both sides, us:
+// of 27 forms; the one-row forms' to 135 products of one row or a few experts' rows.  The forms
+// kept lose 4% (A4), 5% (A16) and 3% (one row) of geometric-mean time against the best of all;
+// a rule on tile counts alone lost 12 and 14% on the drawn ones, one row without the one-row
+// forms 29%.  Both sides, us:
 //   M = 64 on [2048, 2048], A4: 16 x 16 over 4 waves 6.1, 32 x 64 6.5, tiles of 64 x 128 7.6
 //   M = 128 on [11008, 2048], A4: tiles of 64 x 128 9.0, of 128 x 128 9.9, 32 x 64 11.4;
 //     A16: 64 x 64 over 4 waves 14.8, tiles of 64 x 128 16.1, 32 x 32 over 8 waves 18.8
@@ -904,17 +1038,17 @@ template <class C, bool GROUPED>
 float estimate(const MxArgs& a, MxCost c) {
   const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
   if (row_tiles<C, GROUPED>(a) * tiles_n >= (int64_t(1) << 32) / C::NT) return INFINITY;   // threads of a launch
-  // grouped: every expert's last tile half filled, the lists being on the device
+  // grouped: an expert's last tile with half its rows, the lists being on the device
   const float products = (float)std::min(a.M, a.E);
-  const float tiles = (float)tiles_n * (GROUPED ? std::max(products, (float)a.M / C::BM + 0.5f * products)
+  const float tiles = (float)tiles_n * (GROUPED ? std::max(products, (float)a.M / C::BM + 0.5f * products * (C::BM > 1))
                                                 : (float)row_tiles<C, GROUPED>(a));
   const int64_t stages = (a.K + C::KS - 1) / C::KS, mine = C::SPLIT ? (stages + C::NW - 1) / C::NW : stages;
   const float r = std::max(1.0f, tiles / (float)(device_cu_count() * C::PER_CU));
-  const float mb = 1e-6f * tiles * (float)(mine * (C::SPLIT ? C::NW : 1)) * (float)(C::BM * 128 + C::BN * C::WB);
+  const float mb = 1e-6f * tiles * (float)(mine * (C::SPLIT ? C::NW : 1)) * (float)C::TILE_BYTES;
   return c.fixed + r * (c.round + c.stage * (float)mine) + c.mb * mb;
 }
 
-template <class C>   // MxSplit or MxCfg
+template <class C>   // MxVec, MxSplit or MxCfg
 struct MxForm {
   MxCost cost;
 };
@@ -941,6 +1075,8 @@ hipError_t launch_any(const MxArgs& a, bool y_bf16, hipStream_t stream) {
                                  MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 9.06f, 1.114f, 0.063f});
   else
     return launch_least<GROUPED>(a, y_bf16, stream,
+                                 MxForm<MxVec<4, 1>>{0.16f, 3.38f, 0.660f, 0.127f},
+                                 MxForm<MxVec<2, 4>>{2.65f, 0.43f, 0.915f, 0.030f},
                                  MxForm<MxSplit<A4, 1, 1, 16, 2>>{2.83f, 2.05f, 0.429f, 0.022f},
                                  MxForm<MxSplit<A4, 1, 1, 4, 2>>{3.27f, 1.59f, 0.188f, 0.034f},
                                  MxForm<MxSplit<A4, 1, 2, 4, 2>>{2.77f, 2.12f, 0.236f, 0.043f},

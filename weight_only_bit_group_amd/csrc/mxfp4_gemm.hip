@@ -1035,7 +1035,7 @@ struct MxCost {
 };
 
 template <class C, bool GROUPED>
-float estimate(const MxArgs& a, MxCost c) {
+float estimate(const MxArgs& a, MxCost c, int cus) {
   const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
   if (row_tiles<C, GROUPED>(a) * tiles_n >= (int64_t(1) << 32) / C::NT) return INFINITY;   // threads of a launch
   // grouped: an expert's last tile with half its rows, the lists being on the device
@@ -1043,7 +1043,7 @@ float estimate(const MxArgs& a, MxCost c) {
   const float tiles = (float)tiles_n * (GROUPED ? std::max(products, (float)a.M / C::BM + 0.5f * products * (C::BM > 1))
                                                 : (float)row_tiles<C, GROUPED>(a));
   const int64_t stages = (a.K + C::KS - 1) / C::KS, mine = C::SPLIT ? (stages + C::NW - 1) / C::NW : stages;
-  const float r = std::max(1.0f, tiles / (float)(device_cu_count() * C::PER_CU));
+  const float r = std::max(1.0f, tiles / (float)(cus * C::PER_CU));
   const float mb = 1e-6f * tiles * (float)(mine * (C::SPLIT ? C::NW : 1)) * (float)C::TILE_BYTES;
   return c.fixed + r * (c.round + c.stage * (float)mine) + c.mb * mb;
 }
@@ -1056,7 +1056,8 @@ struct MxForm {
 template <bool GROUPED, class... C>
 hipError_t launch_least(const MxArgs& a, bool y_bf16, hipStream_t stream, MxForm<C>... form) {
   using Fn = hipError_t (*)(const MxArgs&, bool, hipStream_t);
-  const float t[] = {estimate<C, GROUPED>(a, form.cost)...};
+  const int cus = device_cu_count();
+  const float t[] = {estimate<C, GROUPED>(a, form.cost, cus)...};
   const Fn fn[] = {launch<C, GROUPED>...};
   return fn[std::min_element(std::begin(t), std::end(t)) - std::begin(t)](a, y_bf16, stream);
 }

@@ -112,6 +112,7 @@ def test_experts_with_choices_that_add_nothing(ids_dtype):
     w1, w2, x = _ints(rng, e, 2 * inner, k), _ints(rng, e, k, inner), _ints(rng, 6, k)
     ids = np.array([[0, 1], [4, 4], [200, 2], [3, 3], [1, 99], [4, 0]])
     weights = rng.random((6, 2)).astype(np.float32)
+    weights[(ids < 0) | (ids >= e)] = np.nan
     m = L().MXFP4Experts.from_weights(dev(w1), dev(w2))
     step(f"MXFP4Experts with choices outside the experts, {ids_dtype}")
     poison = torch.full((1 << 20,), float("nan"), device="cuda")   # so that memory handed out next holds NaN

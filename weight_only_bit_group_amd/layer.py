@@ -339,11 +339,12 @@ class MXFP4Experts(torch.nn.Module):
         y = product(*_mx_rounded(h, self.act), self.down_codes, self.down_scales, offsets)
         back = torch.empty_like(order)
         back[order] = torch.arange(order.shape[0], device=order.device)
-        # (the rows behind the last expert were never written)
+        # (the rows behind the last expert were never written, and nothing is said of their weights)
         y = torch.where(valid[:, None], y[back], 0.0).view(t, top, self.features)
-        out = y[:, 0] * weights.reshape(t, top)[:, :1].float()
+        w = torch.where(valid, weights.reshape(-1).float(), 0.0).view(t, top, 1)
+        out = y[:, 0] * w[:, 0]
         for j in range(1, top):
-            out += y[:, j] * weights.reshape(t, top)[:, j:j + 1].float()
+            out += y[:, j] * w[:, j]
         return out.reshape(*x.shape[:-1], self.features)
 
     def extra_repr(self) -> str:

@@ -337,23 +337,32 @@ def aq_w8a16_gemm(X, codes, scales, zeros, group: int, out=None, workspace=None)
 # ---- MXFP4 -------------------------------------------------------------------------------
 # These calls also run on a device that is not the current one (every tensor has to be on
 # X's device), and X may have rows further apart than their length.  A call on a few rows is
-# a matter of microseconds on the host, so arguments are looked over in one expression each;
-# what fails it is named by the slower _mx_need.
+# a matter of microseconds on the host, so the module _aq_torch makes the common call whole;
+# where it returns None (a wrong argument, another device, an empty product, an error) the call
+# is gone through here.
 
-_MX_FN = {}   # name -> the library's function
+
+class _MxNative:
+    """The module's functions; the first use of one loads the library and the module."""
+
+    def __getattr__(self, name):
+        if name not in ("quantize", "dequantize", "gemm", "gemm_a4", "grouped_gemm", "grouped_gemm_a4"):
+            raise AttributeError(name)
+        _lib.load()
+        from . import _aq_torch   # an ImportError here: the module has not been built
+        fn = getattr(_aq_torch, name)
+        setattr(self, name, fn)
+        return fn
+
+
+_mx = _MxNative()
 
 
 def _mx_call(name: str, dev: int, *args) -> None:
-    fn = _MX_FN.get(name)
-    if fn is None:
-        fn = _MX_FN[name] = getattr(_lib.load(), name)
-    if torch._C._cuda_getDevice() == dev:
+    fn = getattr(_lib.load(), name)
+    with torch.cuda.device(dev):
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if st:
-        check(st, name)
+    check(st, name)
 
 
 def _mx_need(t, name: str, dtype, shape, dev: int):
@@ -393,16 +402,12 @@ _U8 = torch.uint8
 
 def _mx_codes(codes, scales, name: str, scales_name: str):
     """(rows, columns, device) of an MXFP4 matrix: codes [M, K/2], scales [M, K/32]."""
-    if not (isinstance(codes, torch.Tensor) and codes.is_cuda and codes.dtype is _U8 and codes.dim() == 2
-            and codes.is_contiguous()):
-        _need(codes, name, _U8, 2)
+    _need(codes, name, _U8, 2)
     m, half = codes.shape
     if half == 0 or half & 15:
         raise ValueError(f"K must be a positive multiple of 32 (got {2 * half})")
     dev = codes.get_device()
-    if not (isinstance(scales, torch.Tensor) and scales.dtype is _U8 and scales.shape == (m, half >> 4)
-            and scales.get_device() == dev and scales.is_contiguous()):
-        _mx_need(scales, scales_name, _U8, (m, half >> 4), dev)
+    _mx_need(scales, scales_name, _U8, (m, half >> 4), dev)
     return m, 2 * half, dev
 
 
@@ -410,12 +415,9 @@ def _mx_weights(codes, scales, k: int, dev: int, ndim: int):
     """The shape (N,) or (E, N) of MXFP4 weights with rows of k."""
     if not isinstance(codes, torch.Tensor) or codes.dim() != ndim:
         raise ValueError("codes must be [N, K/2]" if ndim == 2 else "codes must be [E, N, K/2]")
-    *lead, half = codes.shape
-    if not (half * 2 == k and codes.dtype is _U8 and codes.get_device() == dev and codes.is_contiguous()):
-        _mx_need(codes, "codes", _U8, (*lead, k // 2), dev)
-    if not (isinstance(scales, torch.Tensor) and scales.shape == (*lead, k >> 5) and scales.dtype is _U8
-            and scales.get_device() == dev and scales.is_contiguous()):
-        _mx_need(scales, "scales", _U8, (*lead, k >> 5), dev)
+    lead = codes.shape[:-1]
+    _mx_need(codes, "codes", _U8, (*lead, k // 2), dev)
+    _mx_need(scales, "scales", _U8, (*lead, k >> 5), dev)
     return lead
 
 
@@ -437,6 +439,10 @@ def _mx_out(out, m: int, n: int, out_dtype, like, dev: int):
 
 def aq_mxfp4_quantize(X, *, codes=None, scales=None):
     """(codes [M, K/2] u8, scales [M, K/32] u8) of X[M, K] (f32 or bf16; its rows may be strided)."""
+    if codes is None and scales is None:
+        pair = _mx.quantize(X)
+        if pair is not None:
+            return pair
     m, k, ld, dev = _mx_rows(X, "X", _MX_OUT)
     if codes is None:
         codes = X.new_empty((m, k >> 1), dtype=torch.uint8)
@@ -453,6 +459,9 @@ def aq_mxfp4_quantize(X, *, codes=None, scales=None):
 
 def aq_mxfp4_dequantize(codes, scales, out_dtype=None, out=None):
     """Y[M, K] (float32, or bfloat16: exact in both) = the values of codes [M, K/2] and scales [M, K/32]."""
+    y = _mx.dequantize(codes, scales, out_dtype, out)
+    if y is not None:
+        return y
     m, k, dev = _mx_codes(codes, scales, "codes", "scales")
     out, code = _mx_out(out, m, k, out_dtype, codes, dev)
     if m:
@@ -462,6 +471,9 @@ def aq_mxfp4_dequantize(codes, scales, out_dtype=None, out=None):
 
 def aq_mxfp4_gemm(X, codes, scales, out_dtype=None, out=None):
     """Y[M, N] (float32, or bfloat16) = X[M, K] (bf16; its rows may be strided) times the MXFP4 weights, transposed."""
+    y = _mx.gemm(X, codes, scales, out_dtype, out)
+    if y is not None:
+        return y
     m, k, ld, dev = _mx_rows(X, "X", (torch.bfloat16,))
     n, = _mx_weights(codes, scales, k, dev, 2)
     out, code = _mx_out(out, m, n, out_dtype, X, dev)
@@ -472,6 +484,9 @@ def aq_mxfp4_gemm(X, codes, scales, out_dtype=None, out=None):
 
 def aq_mxfp4_gemm_a4(X_codes, X_scales, codes, scales, out_dtype=None, out=None):
     """Y[M, N] (float32, or bfloat16) of MXFP4 activations (as aq_mxfp4_quantize returns them) and MXFP4 weights."""
+    y = _mx.gemm_a4(X_codes, X_scales, codes, scales, out_dtype, out)
+    if y is not None:
+        return y
     m, k, dev = _mx_codes(X_codes, X_scales, "X_codes", "X_scales")
     n, = _mx_weights(codes, scales, k, dev, 2)
     out, code = _mx_out(out, m, n, out_dtype, X_codes, dev)
@@ -483,9 +498,7 @@ def aq_mxfp4_gemm_a4(X_codes, X_scales, codes, scales, out_dtype=None, out=None)
 
 def _mx_lists(offsets, rows, e: int, t: int, dev: int) -> int:
     """Rows of Y: the length of rows, or all t rows of X."""
-    if not (isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32 and offsets.shape == (e + 1,)
-            and offsets.get_device() == dev and offsets.is_contiguous()):
-        _mx_need(offsets, "offsets", torch.int32, (e + 1,), dev)
+    _mx_need(offsets, "offsets", torch.int32, (e + 1,), dev)
     if rows is None:
         return t
     _need(rows, "rows", torch.int32, 1)
@@ -501,6 +514,9 @@ def aq_mxfp4_grouped_gemm(X, codes, scales, offsets, rows=None, out_dtype=None, 
     X [T, K] bf16 (its rows may be strided), codes [E, N, K/2], scales [E, N, K/32], offsets [E + 1] int32 and rows
     int32 on the device.  Rows of Y outside the offsets are not written.
     """
+    y = _mx.grouped_gemm(X, codes, scales, offsets, rows, out_dtype, out)
+    if y is not None:
+        return y
     t, k, ld, dev = _mx_rows(X, "X", (torch.bfloat16,))
     e, n = _mx_weights(codes, scales, k, dev, 3)
     m = _mx_lists(offsets, rows, e, t, dev)
@@ -513,6 +529,9 @@ def aq_mxfp4_grouped_gemm(X, codes, scales, offsets, rows=None, out_dtype=None, 
 
 def aq_mxfp4_grouped_gemm_a4(X_codes, X_scales, codes, scales, offsets, rows=None, out_dtype=None, out=None):
     """aq_mxfp4_grouped_gemm with the activations in MXFP4 (X_codes [T, K/2], X_scales [T, K/32])."""
+    y = _mx.grouped_gemm_a4(X_codes, X_scales, codes, scales, offsets, rows, out_dtype, out)
+    if y is not None:
+        return y
     t, k, dev = _mx_codes(X_codes, X_scales, "X_codes", "X_scales")
     e, n = _mx_weights(codes, scales, k, dev, 3)
     m = _mx_lists(offsets, rows, e, t, dev)

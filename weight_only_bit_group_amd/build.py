@@ -1,4 +1,4 @@
-"""Builds libaq.so (the gfx950 HIP kernels and the C ABI) in-tree with hipcc.
+"""Builds libaq.so (the gfx950 HIP kernels and the C ABI) in-tree with hipcc, and the torch binding's module.
 
     python -m weight_only_bit_group_amd.build        # or build() from Python
 
@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -25,6 +26,10 @@ PROBE_PATH = os.path.join(HERE, "libaq_probe.so")
 HIP_SOURCES = ("quant_pack.hip", "w4a16_gemv.hip", "decode_mfma.hip", "mfma_gemm.hip", "act_absmean.hip",
                "awq_search.hip", "fp4_gemv.hip", "fp4_quant.hip", "w8a16_gemv.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip")
 CPP_SOURCES = ("aq_api.cpp",)
+
+# the torch binding's native calls, a CPython module linked against libaq.so beside it
+TORCH_SOURCE = os.path.join(CSRC, "aq_torch.cpp")
+TORCH_PATH = os.path.join(HERE, "_aq_torch.so")
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
@@ -59,21 +64,52 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_torch() -> str:
+    """The binding's host code, against torch's and Python's headers; no device code in it."""
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(OBJ_DIR, os.path.basename(TORCH_SOURCE) + ".o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(ROOT, "include"),
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(_hipcc())), "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-c", TORCH_SOURCE, "-o", obj]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"g++ failed for {TORCH_SOURCE}:\n{proc.stdout}\n{proc.stderr}")
+    return obj
+
+
+def _link_torch(obj: str) -> None:
+    import torch
+
+    tmp = TORCH_PATH + ".tmp"
+    proc = subprocess.run(["g++", "-shared", "-fPIC", obj, "-L" + HERE, "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN",
+                           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
+                           "-lc10", "-lc10_hip", "-o", tmp], capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"link of the torch module failed:\n{proc.stdout}\n{proc.stderr}")
+    os.replace(tmp, TORCH_PATH)
+
+
 def build(verbose: bool = True) -> str:
-    """Compile every source for gfx950 and link libaq.so; returns the library path."""
+    """Compile every source for gfx950, link libaq.so and the binding's module; returns the library path."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     sources = list(HIP_SOURCES) + list(CPP_SOURCES)
-    jobs = min(len(sources) + 1, max(1, min(8, os.cpu_count() or 1)))
+    jobs = min(len(sources) + 2, max(1, min(8, os.cpu_count() or 1)))
     with ThreadPoolExecutor(max_workers=jobs) as pool:
         probe_obj = pool.submit(_compile, PROBE_SOURCE)
+        torch_obj = pool.submit(_compile_torch)
         objs = list(pool.map(_compile, sources))
-        probe_obj = probe_obj.result()
+        probe_obj, torch_obj = probe_obj.result(), torch_obj.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     proc = subprocess.run(cmd, capture_output=True, text=True)
     if proc.returncode != 0:
         raise RuntimeError(f"link failed:\n{proc.stdout}\n{proc.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_torch(torch_obj)
     tmp = PROBE_PATH + ".tmp"
     proc = subprocess.run([_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", probe_obj, "-o", tmp],
                           capture_output=True, text=True)
@@ -81,7 +117,7 @@ def build(verbose: bool = True) -> str:
         raise RuntimeError(f"probe link failed:\n{proc.stdout}\n{proc.stderr}")
     os.replace(tmp, PROBE_PATH)
     if verbose:
-        print(f"built {LIB_PATH} and {PROBE_PATH}")
+        print(f"built {LIB_PATH}, {TORCH_PATH} and {PROBE_PATH}")
     return LIB_PATH
 
 

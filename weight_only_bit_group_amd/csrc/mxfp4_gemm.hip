@@ -1017,8 +1017,8 @@ hipError_t launch(const MxArgs& a, bool y_bf16, hipStream_t stream) {
 // with r = the tiles over those that the device holds at once, at least 1: a block takes its
 // run of stages whether or not others run beside it, and every tile adds its traffic.
 //   The four figures of a form are least-squares fits of the relative error to graph-replayed
-// times of 520 products (drawn ones, M to 4100, N and K to 14400, to 100 experts; and M = 1 to
-// 4096 on weights of 1024 to 14336 rows and columns, 8 to 128 experts with 1 to 256 rows each),
+// times of 660 products (drawn ones, M to 4100, N and K to 14400, to 100 experts; and M = 1 to
+// 4096 on weights of 512 to 14336 rows and columns, 8 to 128 experts with 1 to 400 rows each),
 // of 27 forms; the one-row forms' to 135 products of one row or a few experts' rows.  The forms
 // kept lose 4% (A4), 5% (A16) and 3% (one row) of geometric-mean time against the best of all;
 // a rule on tile counts alone lost 12 and 14% on the drawn ones, one row without the one-row
@@ -1067,26 +1067,27 @@ hipError_t launch_any(const MxArgs& a, bool y_bf16, hipStream_t stream) {
   if constexpr (A4)
     return launch_least<GROUPED>(a, y_bf16, stream,
                                  MxForm<MxSplit<A4, 1, 1, 16, 2>>{2.97f, 2.02f, 0.363f, 0.023f},
-                                 MxForm<MxSplit<A4, 1, 1, 4, 2>>{2.47f, 2.38f, 0.189f, 0.042f},
-                                 MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.56f, 4.86f, 0.620f, 0.044f},
-                                 MxForm<MxSplit<A4, 2, 4, 4, 1>>{0.00f, 5.89f, 0.690f, 0.053f},
-                                 MxForm<MxSplit<A4, 4, 2, 8, 1>>{2.28f, 3.88f, 0.994f, 0.022f},
-                                 MxForm<MxCfg<A4, 2, 2, 2, 4>>{0.00f, 5.07f, 0.349f, 0.077f},
-                                 MxForm<MxCfg<A4, 2, 2, 4, 4>>{0.00f, 6.04f, 0.523f, 0.057f},
-                                 MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 9.06f, 1.114f, 0.063f});
+                                 MxForm<MxSplit<A4, 1, 1, 4, 2>>{2.49f, 2.33f, 0.187f, 0.043f},
+                                 MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.63f, 4.79f, 0.617f, 0.045f},
+                                 MxForm<MxSplit<A4, 2, 4, 4, 1>>{0.00f, 5.76f, 0.707f, 0.052f},
+                                 MxForm<MxSplit<A4, 4, 2, 8, 1>>{2.66f, 3.16f, 1.033f, 0.036f},
+                                 MxForm<MxCfg<A4, 2, 2, 2, 4>>{0.00f, 5.02f, 0.372f, 0.056f},
+                                 MxForm<MxCfg<A4, 2, 2, 4, 4>>{0.00f, 5.88f, 0.541f, 0.049f},
+                                 MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 8.83f, 1.121f, 0.058f});
   else
     return launch_least<GROUPED>(a, y_bf16, stream,
                                  MxForm<MxVec<4, 1>>{0.16f, 3.38f, 0.660f, 0.127f},
                                  MxForm<MxVec<2, 4>>{2.65f, 0.43f, 0.915f, 0.030f},
                                  MxForm<MxSplit<A4, 1, 1, 16, 2>>{2.83f, 2.05f, 0.429f, 0.022f},
-                                 MxForm<MxSplit<A4, 1, 1, 4, 2>>{3.27f, 1.59f, 0.188f, 0.034f},
-                                 MxForm<MxSplit<A4, 1, 2, 4, 2>>{2.77f, 2.12f, 0.236f, 0.043f},
-                                 MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.00f, 5.65f, 0.321f, 0.060f},
-                                 MxForm<MxSplit<A4, 2, 2, 8, 1>>{1.66f, 3.36f, 0.304f, 0.049f},
-                                 MxForm<MxSplit<A4, 4, 4, 4, 1>>{1.40f, 4.94f, 0.580f, 0.035f},
-                                 MxForm<MxCfg<A4, 1, 4, 4, 2>>{1.63f, 3.32f, 0.322f, 0.061f},
-                                 MxForm<MxCfg<A4, 2, 2, 4, 4>>{0.84f, 5.20f, 0.483f, 0.039f},
-                                 MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 8.97f, 1.022f, 0.057f});
+                                 MxForm<MxSplit<A4, 1, 1, 4, 2>>{3.35f, 1.48f, 0.185f, 0.036f},
+                                 MxForm<MxSplit<A4, 1, 2, 4, 2>>{2.92f, 1.95f, 0.233f, 0.045f},
+                                 MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.00f, 5.66f, 0.319f, 0.061f},
+                                 MxForm<MxSplit<A4, 2, 2, 8, 1>>{3.10f, 1.74f, 0.276f, 0.062f},
+                                 MxForm<MxSplit<A4, 4, 2, 8, 1>>{3.09f, 2.36f, 0.466f, 0.044f},
+                                 MxForm<MxSplit<A4, 4, 4, 4, 1>>{2.29f, 3.89f, 0.546f, 0.046f},
+                                 MxForm<MxCfg<A4, 1, 4, 4, 2>>{0.90f, 3.84f, 0.333f, 0.055f},
+                                 MxForm<MxCfg<A4, 2, 2, 4, 4>>{0.61f, 5.20f, 0.491f, 0.039f},
+                                 MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 8.91f, 1.030f, 0.053f});
 }
 
 }  // namespace

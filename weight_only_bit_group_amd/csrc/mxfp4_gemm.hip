@@ -10,7 +10,7 @@
 //
 // A16 runs on the bf16 matrix instructions: the weights' values have two significant bits
 // and an exponent in bf16's range, so v_cvt_scalef32_pk_bf16_fp4 turns a code pair and its
-// block factor into the exact bf16 pair.  A4 runs on the block-scaled matrix instructions,
+// block factor into the exact bf16 pair (one row alone: fp32 multiply-adds).  A4 runs on the block-scaled matrix instructions,
 // which take the codes and the E8M0 bytes as they are: four times the bf16 rate, and the
 // products of one block are exact.
 //
@@ -366,7 +366,9 @@ __global__ __launch_bounds__(C::NT) void mxfp4_gemv_kernel(MxArgs a) {
 // filled by its own LDS-DMA loads, so there is no barrier before the sums are joined: a wave
 // only waits for its own oldest loads, with R stages in flight.  The LDS layout and the
 // order of the weight rows are those of the larger tiles below; the scale bytes come straight
-// to the lanes that use them, 16 bytes of a row at a time.
+// to the lanes that use them, 16 bytes of a row at a time.  16 rows, graph-replayed: on [11008,
+// 2048] 7.1 us (A16) and 5.0 (A4), on [4096, 14336] 14.0 and 7.7; there the blocks of 16 columns
+// read 118 MB of activations beside 31 MB of weights, some 40 bytes a clock and compute unit.
 template <int ROWB>
 __device__ __forceinline__ int lds_unit(int r, int u) {
   return ROWB == 128 ? u ^ ((r >> 1) & 7) : u ^ ((r >> 3) & 1);
@@ -606,6 +608,11 @@ __global__ __launch_bounds__(C::NT) void mxfp4_split_kernel(MxArgs a) {
 // The weight rows of a wave are stored so that lane c of its FN operands holds rows
 // FN c .. FN c + FN - 1: its outputs of one row are neighbours and leave in one store, 16
 // lanes 64 to 256 contiguous bytes.
+//   M = 4096 on [11008, 2048], bf16 out, graph-replayed: A4 65 to 69 us (2.8 PFLOP/s), A16 158
+// (1.17).  A4 is bound by the card's power (the clock falls to about 1.7 GHz) and by what a
+// tile of 2048 k spends outside its loop (37%); M = N = 4096, K = 14336 reaches 4.0 PFLOP/s, A16
+// 1.34.  Deeper rings, larger wave tiles, 32 x 32 instructions and two blocks a compute unit
+// were within 5% or slower.
 template <bool A4_, int WM_, int WN_, int FM_, int FN_>
 struct MxCfg {
   static constexpr bool A4 = A4_;

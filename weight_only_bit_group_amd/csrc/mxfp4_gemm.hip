@@ -10,9 +10,9 @@
 //
 // A16 runs on the bf16 matrix instructions: the weights' values have two significant bits
 // and an exponent in bf16's range, so v_cvt_scalef32_pk_bf16_fp4 turns a code pair and its
-// block factor into the exact bf16 pair (one row alone: fp32 multiply-adds).  A4 runs on the block-scaled matrix instructions,
-// which take the codes and the E8M0 bytes as they are: four times the bf16 rate, and the
-// products of one block are exact.
+// block factor into the exact bf16 pair (one row alone: fp32 multiply-adds).  A4 runs on the
+// block-scaled matrix instructions, which take the codes and the E8M0 bytes as they are: four
+// times the bf16 rate, and the products of one block are exact.
 //
 // A block of a row is 32 k, 16 bytes of codes: one lane's operand of one A4 instruction
 // and of four A16 instructions.  A sum may take its k in any order as long as both

@@ -1033,7 +1033,8 @@ hipError_t launch(const MxArgs& a, bool y_bf16, hipStream_t stream) {
 //   M = 64 on [2048, 2048], A4: 16 x 16 over 4 waves 6.1, 32 x 64 6.5, tiles of 64 x 128 7.6
 //   M = 128 on [11008, 2048], A4: tiles of 64 x 128 9.0, of 128 x 128 9.9, 32 x 64 11.4;
 //     A16: 64 x 64 over 4 waves 14.8, tiles of 64 x 128 16.1, 32 x 32 over 8 waves 18.8
-//   M = 1024 there, A4: tiles of 256 x 256 21.9, of 128 x 128 25.0; A16: 49.5 against 46.4
+//   M = 1024 there, A4: tiles of 256 x 256 21.9, of 128 x 128 25.0 (what the estimates, 23.0 and
+//     22.5, choose); A16: 49.5 against 46.4
 //   M = 16 on [4096, 14336]: 16 x 16 over 16 waves 7.7 (A4) and 14.7 (A16), over 4 10.9 and 20.3
 //   4 rows for each of 128 experts of [4096, 2048], A4: 16 x 64 by one wave 101, 16 x 16 over
 //     4 waves 182

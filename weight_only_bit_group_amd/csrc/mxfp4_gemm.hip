@@ -86,7 +86,11 @@ __device__ __forceinline__ void drain_barrier() {
 // the compiler gives a 16 x 16 instruction another destination than its addend and then moves
 // accumulators about (60 moves for 64 instructions in the loop).  It does not see the hazards
 // either: s_nop 1 covers an operand that a VALU instruction wrote just before (free, the matrix
-// core is busy with the instruction before), settle() the results' first reads after the loop.
+// core is busy with the instruction before), settle() the results' first reads after the loop:
+// eight wait states have to lie between a result and its reader, and an accumulator is copied
+// nowhere before settle() (tests/test_mxfp4_code.py walks the compiled code for both).  A kernel
+// whose accumulators meet at a branch must not use these: the compiler may copy them there, ahead
+// of any wait that follows.
 template <int Q>   // the scale byte of both dwords that applies
 __device__ __forceinline__ void mfma_a4(f32x4& c, u32x4 x, u32x4 w, uint32_t sx, uint32_t sw) {
   asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] "
@@ -366,9 +370,13 @@ __global__ __launch_bounds__(C::NT) void mxfp4_gemv_kernel(MxArgs a) {
 // filled by its own LDS-DMA loads, so there is no barrier before the sums are joined: a wave
 // only waits for its own oldest loads, with R stages in flight.  The LDS layout and the
 // order of the weight rows are those of the larger tiles below; the scale bytes come straight
-// to the lanes that use them, 16 bytes of a row at a time.  16 rows, graph-replayed: on [11008,
-// 2048] 7.1 us (A16) and 5.0 (A4), on [4096, 14336] 14.0 and 7.7; there the blocks of 16 columns
-// read 118 MB of activations beside 31 MB of weights, some 40 bytes a clock and compute unit.
+// to the lanes that use them, 16 bytes of a row at a time.  A wave may run out of stages at any of
+// them, so accumulators meet at branches: the matrix instructions are builtins, whose waits the
+// compiler keeps (against inline assembly with its own wait at every stage's end: 16 rows on
+// [4096, 14336] 13.9 against 14.3 us (A16) and 8.0 against 8.3 (A4), 36 products 2% on average).
+//   16 rows, graph-replayed: on [11008, 2048] 6.9 us (A16) and 4.6 (A4), on [4096, 14336] 13.9 and
+// 8.0; there the blocks of 16 columns read 118 MB of activations beside 31 MB of weights, some 40
+// bytes a clock and compute unit.
 template <int ROWB>
 __device__ __forceinline__ int lds_unit(int r, int u) {
   return ROWB == 128 ? u ^ ((r >> 1) & 7) : u ^ ((r >> 3) & 1);
@@ -529,7 +537,9 @@ __global__ __launch_bounds__(C::NT) void mxfp4_split_kernel(MxArgs a) {
         for (int i = 0; i < C::FM; ++i)
 #pragma unroll
           for (int j = 0; j < C::FN; ++j)
-            mfma_a4<0>(acc[i][j], x[q][i], w[q][j], sx[i][2 * ST + q] >> (8 * g), sw[j][2 * ST + q] >> (8 * g));
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes8(x[q][i]), codes8(w[q][j]), acc[i][j], 4, 4, 0,
+                                                                         sx[i][2 * ST + q] >> (8 * g), 0,
+                                                                         sw[j][2 * ST + q] >> (8 * g));
     } else {
       uint64_t wc[C::FN];
 #pragma unroll
@@ -546,7 +556,8 @@ __global__ __launch_bounds__(C::NT) void mxfp4_split_kernel(MxArgs a) {
           const uint32_t byte = (sw[j][ST >> 1] >> (16 * (ST & 1) + 8 * (g >> 1))) & 255u;
           const bf16x8 b = mx_bf16x8((uint32_t)(wc[j] >> (32 * q)), __uint_as_float(byte << 23));
 #pragma unroll
-          for (int i = 0; i < C::FM; ++i) mfma_a16(acc[i][j], x[q][i], b);
+          for (int i = 0; i < C::FM; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[q][i]), b, acc[i][j], 0, 0, 0);
         }
     }
   };
@@ -563,7 +574,6 @@ __global__ __launch_bounds__(C::NT) void mxfp4_split_kernel(MxArgs a) {
       stage(s + 7, std::integral_constant<int, 7>{});
     }
   }
-  settle(acc);
 
   // ---- the waves' sums, added in wave order; lane c of operand j: column FN c + j ----
   float* part = reinterpret_cast<float*>(lds);

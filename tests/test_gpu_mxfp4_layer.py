@@ -157,3 +157,29 @@ def test_modules_refuse():
         L().MXFP4Linear.from_weight(torch.zeros(8, 48, device="cuda"))
     with pytest.raises(ValueError, match="already quantized"):
         L().plan_quantization(torch.nn.ModuleDict({"q": lin, "k": torch.nn.Linear(32, 32)}), ("q",))
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+def test_gradients_are_the_formulas_or_refused(act):
+    """Inputs that require a gradient: the same outputs, the router's weights' gradient, and an error for the rest."""
+    rng = np.random.default_rng(12)
+    e, k, inner, t, top = 5, 64, 32, 6, 2
+    lin = L().MXFP4Linear.from_weight(dev(_ints(rng, 40, k)), None, act)
+    m = L().MXFP4Experts.from_weights(dev(_ints(rng, e, 2 * inner, k)), dev(_ints(rng, e, k, inner)), act)
+    x, w = dev(_ints(rng, t, k)), dev(rng.random((t, top)).astype(np.float32))
+    ids = dev(np.stack([rng.permutation(e)[:top] for _ in range(t)]))
+    step(f"MXFP4 modules with inputs that require a gradient, {act}")
+    xg, wg = x.clone().requires_grad_(), w.clone().requires_grad_()
+    assert torch.equal(lin(xg), lin(x)) and torch.equal(m(xg, ids, wg), m(x, ids, w))
+    for y in (lin(xg), m(xg, ids, w), xg + m(xg, ids, wg)):
+        with pytest.raises(RuntimeError, match="has no backward pass"):
+            y.sum().backward()
+    dy = dev(rng.integers(-3, 4, (t, k)).astype(np.float32))
+    wg = w.clone().requires_grad_()   # (the refused passes may have reached the other)
+    m(x, ids, wg).backward(dy)
+    for j in range(top):
+        one = torch.zeros_like(w)
+        one[:, j] = 1
+        part = (m(x, ids, one) * dy).double()
+        # k products and sums in fp32, each off by half a step of the magnitudes at most
+        assert ((wg.grad[:, j] - part.sum(1)).abs() <= (k + 1) * 2.0 ** -24 * part.abs().sum(1)).all()

@@ -238,12 +238,34 @@ def _mx_rows(x: torch.Tensor, k: int) -> torch.Tensor:
     return x2
 
 
+class _NoBackward(torch.autograd.Function):
+    """compute(x), whose gradient is refused when it is asked for."""
+
+    @staticmethod
+    def forward(ctx, name, compute, x):
+        ctx.name = name
+        return compute(x)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError(f"{ctx.name} has no backward pass: the gradient of its input is not computed "
+                           "(run it under torch.no_grad(), or detach its input)")
+
+
+def _forward_only(name: str, compute, x: torch.Tensor) -> torch.Tensor:
+    """compute(x), a fresh tensor; part of the graph where x is, so that no gradient is lost in silence."""
+    if torch.is_grad_enabled() and x.requires_grad:
+        return _NoBackward.apply(name, compute, x)
+    return compute(x)
+
+
 class MXFP4Linear(torch.nn.Module):
     """y = x W^T (+ bias) with W in MXFP4 (codes [N, K/2], scales [N, K/32]).
 
     act="bf16" casts the input to bf16; act="mxfp4" quantizes it row by row to MXFP4, which
     runs on the block-scaled matrix instructions (four times the bf16 rate, coarser inputs).
-    The output is fp32.
+    The output is fp32.  There is no backward pass: an input that requires a gradient gets its
+    output, and an error when the gradient is asked for.
     """
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None,
@@ -264,9 +286,9 @@ class MXFP4Linear(torch.nn.Module):
         return cls(*B.aq_mxfp4_quantize(weight.detach().contiguous()), bias, act)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        x2 = _mx_rounded(_mx_rows(x, self.in_features), self.act)
         product = B.aq_mxfp4_gemm if self.act == "bf16" else B.aq_mxfp4_gemm_a4
-        y = product(*x2, self.codes, self.scales)
+        y = _forward_only("MXFP4Linear", lambda x2: product(*_mx_rounded(x2, self.act), self.codes, self.scales),
+                          _mx_rows(x, self.in_features))
         if self.bias is not None:
             y += self.bias
         return y.reshape(*x.shape[:-1], self.out_features)
@@ -287,6 +309,7 @@ class MXFP4Experts(torch.nn.Module):
     Both layers run as one product grouped by expert each, for all tokens, without reading a
     count back to the host.  A token's products are added in the order of its choices, in
     fp32: the result does not depend on how its choices were grouped.  The output is fp32.
+    weights are differentiable, the experts are not: an error when x's gradient is asked for.
     """
 
     def __init__(self, gate_up_codes: torch.Tensor, gate_up_scales: torch.Tensor, down_codes: torch.Tensor,
@@ -334,9 +357,13 @@ class MXFP4Experts(torch.nn.Module):
         offsets = torch.searchsorted(key, edges, out_int32=True)
         rows = (order // top).int()
         product = B.aq_mxfp4_grouped_gemm if self.act == "bf16" else B.aq_mxfp4_grouped_gemm_a4
-        h = product(*_mx_rounded(x2, self.act), self.gate_up_codes, self.gate_up_scales, offsets, rows)
-        h = torch.nn.functional.silu(h[:, :self.inner]) * h[:, self.inner:]
-        y = product(*_mx_rounded(h, self.act), self.down_codes, self.down_scales, offsets)
+
+        def experts(x2):
+            h = product(*_mx_rounded(x2, self.act), self.gate_up_codes, self.gate_up_scales, offsets, rows)
+            h = torch.nn.functional.silu(h[:, :self.inner]) * h[:, self.inner:]
+            return product(*_mx_rounded(h, self.act), self.down_codes, self.down_scales, offsets)
+
+        y = _forward_only("MXFP4Experts", experts, x2)
         back = torch.empty_like(order)
         back[order] = torch.arange(order.shape[0], device=order.device)
         # (the rows behind the last expert were never written, and nothing is said of their weights)

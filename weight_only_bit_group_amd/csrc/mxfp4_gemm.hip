@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdio>
 #include <iterator>
 #include <type_traits>
 
@@ -255,6 +256,7 @@ struct MxVec {
   static constexpr int KS = 2048;
   static constexpr int TILE_BYTES = 4096 + 1088 * BN;   // a stage's activations, codes and scale bytes
   static constexpr int PER_CU = 8;                      // blocks that a compute unit holds
+  static int describe(char* to, size_t n) { return snprintf(to, n, "vec %d over %d", NR, NW); }
   static_assert(4 % NW == 0, "whole groups of waves");
 };
 
@@ -413,6 +415,7 @@ struct MxSplit {
   static constexpr bool SPLIT = true, VEC = false;
   static constexpr int TILE_BYTES = BM * 128 + BN * WB;
   static constexpr int PER_CU = std::max(1, std::min(160 * 1024 / LDS, 32 / NW));   // blocks that a compute unit holds
+  static int describe(char* to, size_t n) { return snprintf(to, n, "split %d x %d over %d", FM, FN, NW); }
   static_assert((R - 1) * DMA < 64, "the loads in flight are counted in six bits");
 };
 
@@ -643,6 +646,7 @@ struct MxCfg {
   static constexpr int TILE_BYTES = BM * XB + BN * WB;
   // blocks that a compute unit holds; their registers leave room for 8 waves, or 12
   static constexpr int PER_CU = std::max(1, std::min(160 * 1024 / (2 * (BM * XB + BN * WB)), (FM * FN >= 16 ? 8 : 12) / NW));
+  static int describe(char* to, size_t n) { return snprintf(to, n, "tile %d x %d of %d x %d", WM, WN, FM, FN); }
   static_assert(BM * XB % (1024 * NW) == 0 && BN * WB % (1024 * NW) == 0, "whole loads per wave");
 };
 
@@ -1066,49 +1070,74 @@ float estimate(const MxArgs& a, MxCost c, int cus) {
   return c.fixed + r * (c.round + c.stage * (float)mine) + c.mb * mb;
 }
 
-template <class C>   // MxVec, MxSplit or MxCfg
+template <class C_>   // MxVec, MxSplit or MxCfg
 struct MxForm {
+  using C = C_;
   MxCost cost;
 };
 
-template <bool GROUPED, class... C>
-hipError_t launch_least(const MxArgs& a, bool y_bf16, hipStream_t stream, MxForm<C>... form) {
-  using Fn = hipError_t (*)(const MxArgs&, bool, hipStream_t);
-  const int cus = device_cu_count();
-  const float t[] = {estimate<C, GROUPED>(a, form.cost, cus)...};
-  const Fn fn[] = {launch<C, GROUPED>...};
-  return fn[std::min_element(std::begin(t), std::end(t)) - std::begin(t)](a, y_bf16, stream);
+// f(the forms of a product)
+template <bool A4, class F>
+auto with_forms(F f) {
+  if constexpr (A4)
+    return f(MxForm<MxSplit<A4, 1, 1, 16, 2>>{2.97f, 2.02f, 0.363f, 0.023f},
+             MxForm<MxSplit<A4, 1, 1, 4, 2>>{2.49f, 2.33f, 0.187f, 0.043f},
+             MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.63f, 4.79f, 0.617f, 0.045f},
+             MxForm<MxSplit<A4, 2, 4, 4, 1>>{0.00f, 5.76f, 0.707f, 0.052f},
+             MxForm<MxSplit<A4, 4, 2, 8, 1>>{2.66f, 3.16f, 1.033f, 0.036f},
+             MxForm<MxCfg<A4, 2, 2, 2, 4>>{0.00f, 5.02f, 0.372f, 0.056f},
+             MxForm<MxCfg<A4, 2, 2, 4, 4>>{0.00f, 5.88f, 0.541f, 0.049f},
+             MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 8.83f, 1.121f, 0.058f});
+  else
+    return f(MxForm<MxVec<4, 1>>{0.16f, 3.38f, 0.660f, 0.127f},
+             MxForm<MxVec<2, 4>>{2.65f, 0.43f, 0.915f, 0.030f},
+             MxForm<MxSplit<A4, 1, 1, 16, 2>>{2.83f, 2.05f, 0.429f, 0.022f},
+             MxForm<MxSplit<A4, 1, 1, 4, 2>>{3.35f, 1.48f, 0.185f, 0.036f},
+             MxForm<MxSplit<A4, 1, 2, 4, 2>>{2.92f, 1.95f, 0.233f, 0.045f},
+             MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.00f, 5.66f, 0.319f, 0.061f},
+             MxForm<MxSplit<A4, 2, 2, 8, 1>>{3.10f, 1.74f, 0.276f, 0.062f},
+             MxForm<MxSplit<A4, 4, 2, 8, 1>>{3.09f, 2.36f, 0.466f, 0.044f},
+             MxForm<MxSplit<A4, 4, 4, 4, 1>>{2.29f, 3.89f, 0.546f, 0.046f},
+             MxForm<MxCfg<A4, 1, 4, 4, 2>>{0.90f, 3.84f, 0.333f, 0.055f},
+             MxForm<MxCfg<A4, 2, 2, 4, 4>>{0.61f, 5.20f, 0.491f, 0.039f},
+             MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 8.91f, 1.030f, 0.053f});
+}
+
+// the index of the form that the product takes on a device of `cus` compute units
+template <bool A4, bool GROUPED>
+int least(const MxArgs& a, int cus) {
+  return with_forms<A4>([&](auto... form) {
+    const float t[] = {estimate<typename decltype(form)::C, GROUPED>(a, form.cost, cus)...};
+    return (int)(std::min_element(std::begin(t), std::end(t)) - std::begin(t));
+  });
 }
 
 template <bool A4, bool GROUPED>
 hipError_t launch_any(const MxArgs& a, bool y_bf16, hipStream_t stream) {
-  if constexpr (A4)
-    return launch_least<GROUPED>(a, y_bf16, stream,
-                                 MxForm<MxSplit<A4, 1, 1, 16, 2>>{2.97f, 2.02f, 0.363f, 0.023f},
-                                 MxForm<MxSplit<A4, 1, 1, 4, 2>>{2.49f, 2.33f, 0.187f, 0.043f},
-                                 MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.63f, 4.79f, 0.617f, 0.045f},
-                                 MxForm<MxSplit<A4, 2, 4, 4, 1>>{0.00f, 5.76f, 0.707f, 0.052f},
-                                 MxForm<MxSplit<A4, 4, 2, 8, 1>>{2.66f, 3.16f, 1.033f, 0.036f},
-                                 MxForm<MxCfg<A4, 2, 2, 2, 4>>{0.00f, 5.02f, 0.372f, 0.056f},
-                                 MxForm<MxCfg<A4, 2, 2, 4, 4>>{0.00f, 5.88f, 0.541f, 0.049f},
-                                 MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 8.83f, 1.121f, 0.058f});
-  else
-    return launch_least<GROUPED>(a, y_bf16, stream,
-                                 MxForm<MxVec<4, 1>>{0.16f, 3.38f, 0.660f, 0.127f},
-                                 MxForm<MxVec<2, 4>>{2.65f, 0.43f, 0.915f, 0.030f},
-                                 MxForm<MxSplit<A4, 1, 1, 16, 2>>{2.83f, 2.05f, 0.429f, 0.022f},
-                                 MxForm<MxSplit<A4, 1, 1, 4, 2>>{3.35f, 1.48f, 0.185f, 0.036f},
-                                 MxForm<MxSplit<A4, 1, 2, 4, 2>>{2.92f, 1.95f, 0.233f, 0.045f},
-                                 MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.00f, 5.66f, 0.319f, 0.061f},
-                                 MxForm<MxSplit<A4, 2, 2, 8, 1>>{3.10f, 1.74f, 0.276f, 0.062f},
-                                 MxForm<MxSplit<A4, 4, 2, 8, 1>>{3.09f, 2.36f, 0.466f, 0.044f},
-                                 MxForm<MxSplit<A4, 4, 4, 4, 1>>{2.29f, 3.89f, 0.546f, 0.046f},
-                                 MxForm<MxCfg<A4, 1, 4, 4, 2>>{0.90f, 3.84f, 0.333f, 0.055f},
-                                 MxForm<MxCfg<A4, 2, 2, 4, 4>>{0.61f, 5.20f, 0.491f, 0.039f},
-                                 MxForm<MxCfg<A4, 2, 4, 8, 4>>{0.00f, 8.91f, 1.030f, 0.053f});
+  return with_forms<A4>([&](auto... form) {
+    using Fn = hipError_t (*)(const MxArgs&, bool, hipStream_t);
+    const Fn fn[] = {launch<typename decltype(form)::C, GROUPED>...};
+    return fn[least<A4, GROUPED>(a, device_cu_count())](a, y_bf16, stream);
+  });
 }
 
 }  // namespace
+
+int mxfp4_form(bool a4, bool grouped, int M, int K, int N, int E, int cus) {
+  MxArgs a = {};
+  a.M = M, a.N = N, a.K = K, a.E = E;
+  return a4 ? grouped ? least<true, true>(a, cus) : least<true, false>(a, cus)
+            : grouped ? least<false, true>(a, cus) : least<false, false>(a, cus);
+}
+
+int mxfp4_form_name(bool a4, bool grouped, int i, char* to, size_t n) {
+  auto describe = [&](auto... form) {
+    using Fn = int (*)(char*, size_t);
+    const Fn fn[] = {decltype(form)::C::describe...};
+    return i >= 0 && i < (int)std::size(fn) ? fn[i](to, n) : -1;
+  };
+  return a4 ? with_forms<true>(describe) : with_forms<false>(describe);
+}
 
 hipError_t launch_mxfp4_gemm(const void* X, const uint8_t* XS, int64_t xrow, int M, int K, const uint8_t* codes,
                              const uint8_t* scales, int N, void* Y, bool y_bf16, hipStream_t stream) {

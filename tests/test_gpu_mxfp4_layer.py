@@ -183,3 +183,36 @@ def test_gradients_are_the_formulas_or_refused(act):
         part = (m(x, ids, one) * dy).double()
         # k products and sums in fp32, each off by half a step of the magnitudes at most
         assert ((wg.grad[:, j] - part.sum(1)).abs() <= (k + 1) * 2.0 ** -24 * part.abs().sum(1)).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("t,top", [(1, 8), (64, 8), (600, 8), (4096, 4)])
+def test_experts_captured_and_replayed(t, top, act):
+    """A captured call follows its inputs over several replays, with the program's own calls between them."""
+    rng = np.random.default_rng(t + top)
+    e, k, inner = 16, 64, 32
+    m = L().MXFP4Experts.from_weights(dev(_ints(rng, e, 2 * inner, k)), dev(_ints(rng, e, k, inner)), act)
+
+    def inputs():
+        ids = rng.integers(0, e + 1, (t, top))   # (choice e adds nothing)
+        return dev(rng.standard_normal((t, k)).astype(np.float32)).to(BF16), dev(ids), dev(rng.random((t, top)).astype(np.float32))
+
+    held = inputs()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        m(*held)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = m(*held)
+    for i in range(5):
+        step(f"MXFP4Experts {act}, {t} tokens of {top} choices, replay {i}")
+        new = inputs()
+        want = m(*new)
+        for old, value in zip(held, new):
+            old.copy_(value)
+        torch.cuda.synchronize()
+        graph.replay()
+        again = m(*new)
+        assert torch.equal(y, want) and torch.equal(again, want)

@@ -122,3 +122,15 @@ def test_experts_have_no_silent_gradient(monkeypatch):
         y = m(xg, ids, router(xg))
         with pytest.raises(RuntimeError, match="MXFP4Experts has no backward pass"):
             (xg + y if residual else y).sum().backward()
+
+
+def test_experts_refuse_a_capture_that_sorts_too_much(monkeypatch):
+    """More than 2^20 choices in a captured call: the sort of so many is not repeated faithfully by a replay."""
+    _with_products_on_the_host(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    g = torch.Generator().manual_seed(4)
+    m = L.MXFP4Experts(*_random_pair(g, 2, 64, k=32), *_random_pair(g, 2, 32, k=32))
+    t = (1 << 18) + 1
+    with pytest.raises(RuntimeError, match="choices in a captured call"):
+        m(torch.zeros(t, 32), torch.zeros(t, 4, dtype=torch.int32), torch.zeros(t, 4))
+    assert m(torch.zeros(5, 32), torch.zeros(5, 4, dtype=torch.int32), torch.zeros(5, 4)).shape == (5, 32)

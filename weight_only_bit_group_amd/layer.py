@@ -297,6 +297,11 @@ class MXFP4Linear(torch.nn.Module):
         return f"in_features={self.in_features}, out_features={self.out_features}, weights=mxfp4, act={self.act}"
 
 
+# torch's sort clears counters with memory-fill nodes above this size, which a graph's later replays
+# do not repeat faithfully; below it a captured call has kernels and copies on the device only.
+_CAPTURED_CHOICES = 1 << 20
+
+
 class MXFP4Experts(torch.nn.Module):
     """The experts of a mixture, gated MLPs with MXFP4 weights:
 
@@ -310,6 +315,7 @@ class MXFP4Experts(torch.nn.Module):
     count back to the host.  A token's products are added in the order of its choices, in
     fp32: the result does not depend on how its choices were grouped.  The output is fp32.
     weights are differentiable, the experts are not: an error when x's gradient is asked for.
+    A call may be captured into a graph up to 2^20 choices, and its replays follow x, ids and weights.
     """
 
     def __init__(self, gate_up_codes: torch.Tensor, gate_up_scales: torch.Tensor, down_codes: torch.Tensor,
@@ -350,6 +356,8 @@ class MXFP4Experts(torch.nn.Module):
             raise ValueError(f"ids must be integers (got {ids.dtype})")
         top = ids.shape[-1]
         flat = ids.reshape(-1).long()
+        if flat.shape[0] > _CAPTURED_CHOICES and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError(f"MXFP4Experts: at most {_CAPTURED_CHOICES} choices in a captured call (got {flat.shape[0]})")
         valid = (flat >= 0) & (flat < self.num_experts)
         # choices sorted by expert, those outside the range behind the last one
         key, order = torch.where(valid, flat, self.num_experts).sort(stable=True)

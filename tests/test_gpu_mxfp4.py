@@ -93,6 +93,35 @@ def test_quantize_every_bf16_value():
         assert np.array_equal(host(s), s0) and np.array_equal(host(c), c0)
 
 
+def _under(values, factor):
+    """Blocks of 31 of these values (zero in place of those too large for it) and one that fixes the scale byte."""
+    top = np.float64(2.0) ** (factor - 127 + 2)        # floor(log2 top) - 2 = factor - 127
+    v = np.where(np.abs(values) < 2 * top, values, 0)   # (NaN and infinities go too)
+    v = np.concatenate([v, np.zeros(-len(v) % 31)]).reshape(-1, 31)
+    at = factor % 32
+    return np.concatenate([v[:, :at], np.full((len(v), 1), top), v[:, at:]], 1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_quantize_every_bf16_value_under_every_factor(dtype):
+    """All finite bf16 values beside a maximum that fixes the scale byte, for each byte that the quantiser writes; in
+    fp32 also the borders between codes and the values next to them."""
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF16).double().numpy()
+    borders = np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])
+    step(f"aq_mxfp4_quantize every bf16 value under every factor, {dtype}")
+    for factor in range(253):
+        values = every
+        if dtype == F32:
+            b = (borders * 2.0 ** (factor - 127)).astype(np.float32)
+            near = np.concatenate([b, np.nextafter(b, np.float32(0)), np.nextafter(b, np.float32(np.inf))]).astype(np.float64)
+            values = np.concatenate([every, near, -near])
+        x = _under(values, factor)
+        c, s = B().aq_mxfp4_quantize(torch.from_numpy(x).to(dtype).cuda())
+        c0, s0 = O.quantize(x)
+        assert (s0 == factor).all()
+        assert np.array_equal(host(s), s0) and np.array_equal(host(c), c0), factor
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_quantize_strided_rows(dtype):
     wide = torch.randn(37, 512, device="cuda").to(dtype)

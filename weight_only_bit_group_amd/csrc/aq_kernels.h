@@ -71,7 +71,8 @@ hipError_t launch_mxfp4_grouped_gemm(const void* X, const uint8_t* XS, int64_t x
                                      const uint8_t* codes, const uint8_t* scales, int E, int N, const int32_t* offsets,
                                      const int32_t* rows, int M, void* Y, bool y_bf16, hipStream_t stream);
 // The kernel form that such a product takes on a device of `cus` compute units (E = 1: dense), and a
-// form's description (negative past the last): the tests hold that every form is run.
+// form's description (empty for one that the product does not have, negative past the last): the
+// tests hold that every form is run.
 extern "C" int mxfp4_form(bool a4, bool grouped, int M, int K, int N, int E, int cus);
 extern "C" int mxfp4_form_name(bool a4, bool grouped, int form, char* to, size_t n);
 // compute units of the current device (cached per device)

@@ -1051,7 +1051,9 @@ hipError_t launch(const MxArgs& a, bool y_bf16, hipStream_t stream) {
 //     22.5, choose); A16: 49.5 against 46.4
 //   M = 16 on [4096, 14336]: 16 x 16 over 16 waves 7.7 (A4) and 14.7 (A16), over 4 10.9 and 20.3
 //   4 rows for each of 128 experts of [4096, 2048], A4: 16 x 64 by one wave 101, 16 x 16 over
-//     4 waves 182
+//     4 waves 182; dense it would be chosen above some 80000 columns alone, where tiles of 64 x 128
+//     are faster (1 to 16 rows on [131072, 2048] 29 to 30 against 26 to 28, on [120000, 256] 14 against
+//     11), so it is compiled for experts only
 struct MxCost {
   float fixed, round, stage, mb;
 };
@@ -1070,9 +1072,11 @@ float estimate(const MxArgs& a, MxCost c, int cus) {
   return c.fixed + r * (c.round + c.stage * (float)mine) + c.mb * mb;
 }
 
-template <class C_>   // MxVec, MxSplit or MxCfg
+template <class C_, bool DENSE = true>   // MxVec, MxSplit or MxCfg; for products by expert alone without DENSE
 struct MxForm {
   using C = C_;
+  template <bool GROUPED>
+  static constexpr bool HAS = DENSE || GROUPED;
   MxCost cost;
 };
 
@@ -1082,7 +1086,7 @@ auto with_forms(F f) {
   if constexpr (A4)
     return f(MxForm<MxSplit<A4, 1, 1, 16, 2>>{2.97f, 2.02f, 0.363f, 0.023f},
              MxForm<MxSplit<A4, 1, 1, 4, 2>>{2.49f, 2.33f, 0.187f, 0.043f},
-             MxForm<MxSplit<A4, 1, 4, 1, 2>>{0.63f, 4.79f, 0.617f, 0.045f},
+             MxForm<MxSplit<A4, 1, 4, 1, 2>, false>{0.63f, 4.79f, 0.617f, 0.045f},
              MxForm<MxSplit<A4, 2, 4, 4, 1>>{0.00f, 5.76f, 0.707f, 0.052f},
              MxForm<MxSplit<A4, 4, 2, 8, 1>>{2.66f, 3.16f, 1.033f, 0.036f},
              MxForm<MxCfg<A4, 2, 2, 2, 4>>{0.00f, 5.02f, 0.372f, 0.056f},
@@ -1107,16 +1111,23 @@ auto with_forms(F f) {
 template <bool A4, bool GROUPED>
 int least(const MxArgs& a, int cus) {
   return with_forms<A4>([&](auto... form) {
-    const float t[] = {estimate<typename decltype(form)::C, GROUPED>(a, form.cost, cus)...};
+    const float t[] = {decltype(form)::template HAS<GROUPED> ? estimate<typename decltype(form)::C, GROUPED>(a, form.cost, cus)
+                                                              : INFINITY...};
     return (int)(std::min_element(std::begin(t), std::end(t)) - std::begin(t));
   });
+}
+
+template <class Form, bool GROUPED>
+auto launch_of() -> hipError_t (*)(const MxArgs&, bool, hipStream_t) {
+  if constexpr (Form::template HAS<GROUPED>) return launch<typename Form::C, GROUPED>;
+  else return nullptr;
 }
 
 template <bool A4, bool GROUPED>
 hipError_t launch_any(const MxArgs& a, bool y_bf16, hipStream_t stream) {
   return with_forms<A4>([&](auto... form) {
     using Fn = hipError_t (*)(const MxArgs&, bool, hipStream_t);
-    const Fn fn[] = {launch<typename decltype(form)::C, GROUPED>...};
+    const Fn fn[] = {launch_of<decltype(form), GROUPED>()...};
     return fn[least<A4, GROUPED>(a, device_cu_count())](a, y_bf16, stream);
   });
 }
@@ -1134,7 +1145,8 @@ int mxfp4_form_name(bool a4, bool grouped, int i, char* to, size_t n) {
   auto describe = [&](auto... form) {
     using Fn = int (*)(char*, size_t);
     const Fn fn[] = {decltype(form)::C::describe...};
-    return i >= 0 && i < (int)std::size(fn) ? fn[i](to, n) : -1;
+    const bool has[] = {(grouped ? decltype(form)::template HAS<true> : decltype(form)::template HAS<false>)...};
+    return i < 0 || i >= (int)std::size(fn) ? -1 : has[i] ? fn[i](to, n) : snprintf(to, n, "%s", "");
   };
   return a4 ? with_forms<true>(describe) : with_forms<false>(describe);
 }

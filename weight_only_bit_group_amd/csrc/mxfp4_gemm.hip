@@ -10,7 +10,7 @@
 //
 // A16 runs on the bf16 matrix instructions: the weights' values have two significant bits
 // and an exponent in bf16's range, so v_cvt_scalef32_pk_bf16_fp4 turns a code pair and its
-// block factor into the exact bf16 pair (one row alone: fp32 multiply-adds).  A4 runs on the
+// block factor into the exact bf16 pair (row by row: fp32 multiply-adds).  A4 runs on the
 // block-scaled matrix instructions, which take the codes and the E8M0 bytes as they are: four
 // times the bf16 rate, and the products of one block are exact.
 //
@@ -238,15 +238,20 @@ __device__ __forceinline__ i32x8 codes8(u32x4 v) {
   return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
 }
 
-// ---- one row, A16 --------------------------------------------------------------------------
-// Bound by the weight bytes, so every wave has all it can in flight: NR weight rows, a 16-byte
-// unit (a block of 32 k) of each per lane and 2048 k, straight to registers, the next 2048 k
-// requested before these are used.  The products are fp32 fused multiply-adds of the weights'
-// exact fp32 values (1.5 VALU operations a weight; the matrix instructions of the form below
-// would leave 15 of 16 rows empty, and its LDS ring holds fewer bytes in flight: one row on
-// [11008, 2048] 6.9 against 5.8 us, on [2048, 11008] 9.8 against 6.3, 8 experts' rows of
-// [1536, 2048] 8.6 against 6.5, graph-replayed; two rows 6.9 against 7.1).  NW waves of a block
-// share long rows ([2048, 11008] by one wave each 9.8), their sums are added in wave order.
+// ---- single rows, A16 ----------------------------------------------------------------------
+// Every row of Y by itself, a block of it for each 4 NR / NW columns; bound by the weight bytes,
+// so every wave has all it can in flight: NR weight rows, a 16-byte unit (a block of 32 k) of
+// each per lane and 2048 k, straight to registers, the next 2048 k requested before these are
+// used.  The products are fp32 fused multiply-adds of the weights' exact fp32 values (1.5 VALU
+// operations a weight; the matrix instructions of the form below would leave 15 of 16 rows
+// empty, and its LDS ring holds fewer bytes in flight: one row on [11008, 2048] 5.0 against 6.3
+// us, on [2048, 11008] 5.3 against 9.2, 8 experts' rows of [1536, 2048] 5.9 against 7.9,
+// graph-replayed).  NW waves of a block share long rows ([2048, 11008] by one wave each 8.8),
+// their sums are added in wave order.
+//   More rows read the weights again, which the L2 holds for small ones: several rows take this
+// form too where tiles of 16 rows would leave the device empty (16 rows on [512, 2048] 3.6
+// against 4.3 us, 40 on [70, 576] 3.0 against 3.4, 64 on [94, 31424] 22.9 against 25.8, two on
+// [11008, 2048] 6.3 of either form).
 template <int NR_, int NW_>
 struct MxVec {
   static constexpr bool SPLIT = true, VEC = true;
@@ -1040,20 +1045,25 @@ hipError_t launch(const MxArgs& a, bool y_bf16, hipStream_t stream) {
 //   The four figures of a form are least-squares fits of the relative error to graph-replayed
 // times of 660 products (drawn ones, M to 4100, N and K to 14400, to 100 experts; and M = 1 to
 // 4096 on weights of 512 to 14336 rows and columns, 8 to 128 experts with 1 to 400 rows each),
-// of 27 forms; the one-row forms' to 135 products of one row or a few experts' rows.  The forms
+// of 27 forms; the single-row forms' to 135 products of one row or a few experts' rows.  The forms
 // kept lose 4% (A4), 5% (A16) and 3% (one row) of geometric-mean time against the best of all;
-// a rule on tile counts alone lost 12 and 14% on the drawn ones, one row without the one-row
-// forms 29%.  Both sides, us:
-//   M = 64 on [2048, 2048], A4: 16 x 16 over 4 waves 6.1, 32 x 64 6.5, tiles of 64 x 128 7.6
-//   M = 128 on [11008, 2048], A4: tiles of 64 x 128 9.0, of 128 x 128 9.9, 32 x 64 11.4;
-//     A16: 64 x 64 over 4 waves 14.8, tiles of 64 x 128 16.1, 32 x 32 over 8 waves 18.8
-//   M = 1024 there, A4: tiles of 256 x 256 21.9, of 128 x 128 25.0 (what the estimates, 23.0 and
-//     22.5, choose); A16: 49.5 against 46.4
-//   M = 16 on [4096, 14336]: 16 x 16 over 16 waves 7.7 (A4) and 14.7 (A16), over 4 10.9 and 20.3
-//   4 rows for each of 128 experts of [4096, 2048], A4: 16 x 64 by one wave 101, 16 x 16 over
-//     4 waves 182; dense it would be chosen above some 80000 columns alone, where tiles of 64 x 128
-//     are faster (1 to 16 rows on [131072, 2048] 29 to 30 against 26 to 28, on [120000, 256] 14 against
-//     11), so it is compiled for experts only
+// a rule on tile counts alone lost 12 and 14% on the drawn ones, one row without the single-row
+// forms 29%.  Outside their fit, over 220 dense products of 2 to 2000 rows for which the estimates
+// choose a single-row form and 110 grouped ones of 2 to 500 rows, the choice loses 1.7 and 2.5%
+// against the best form (1.38 and 1.41 times at worst), and 28 and 30% if they were kept for one
+// row.  Both sides, graph-replayed, us:
+//   M = 64 on [2048, 2048], A4: 16 x 16 over 4 waves 3.6, 32 x 64 5.3, tiles of 64 x 128 6.4
+//   M = 128 on [11008, 2048], A4: tiles of 64 x 128 9.3, of 128 x 128 10.4, 32 x 64 11.6;
+//     A16: 64 x 64 over 4 waves 15.0, 32 x 32 over 8 waves 18.0, tiles of 64 x 128 20.8
+//   M = 1024 there, A4: tiles of 256 x 256 24.1, of 128 x 128 26.3 (what the estimates
+//     choose); A16: 54.3 against 51.1
+//   M = 16 on [4096, 14336]: 16 x 16 over 16 waves 8.1 (A4) and 13.3 (A16), over 4 10.6 and 18.7
+//   4 rows for each of 128 experts of [4096, 2048], A4: 16 x 64 by one wave 121, 16 x 16 over
+//     4 waves 191; dense it would be chosen above some 80000 columns alone, where tiles of 64 x 128
+//     are faster (1 to 16 rows on [131072, 2048] 29 to 30 against 26 to 28, on [120000, 256] 14
+//     against 11), so it is compiled for experts only
+//   M = 1 on [131072, 2048], A16, wider than any product of the fit: 16 x 32 over 4 waves 43 (what
+//     the estimates choose), a row by itself 32; on [65536, 2048] 19.7 and 18.8
 struct MxCost {
   float fixed, round, stage, mb;
 };

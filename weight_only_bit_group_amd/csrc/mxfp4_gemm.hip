@@ -616,8 +616,9 @@ __global__ __launch_bounds__(C::NT) void mxfp4_split_kernel(MxArgs a) {
 // ---- many rows ----------------------------------------------------------------------------
 // WM x WN waves, each a (16 FM) x (16 FN) tile of 16 x 16 outputs.  (Against 32 x 32 x 64 and
 // 32 x 32 x 16 the instructions 16 x 16 x 128 and 16 x 16 x 32 touch each accumulator half as
-// often: on random operands, where the card's power sets the clock, 7.3 against 6.3 PFLOP/s
-// and 2.06 against 1.82 in a loop of nothing else.)  K advances in stages of 128 bytes of an
+// often: on random operands, where the card's power sets the clock, 7.1 against 6.3 PFLOP/s
+// and 2.0 against 1.8 in a loop of nothing else that adds in place; on zeros both run at 2.4 GHz,
+// 9.6 and 2.4.)  K advances in stages of 128 bytes of an
 // activation row (A4: 256 k, A16: 64 k) through two LDS buffers filled by LDS-DMA, one
 // barrier a stage.  The scale bytes of two stages are loaded at once, through registers.
 // A tile row keeps its 16-byte units permuted so that the 16 rows which a phase of a

@@ -9,7 +9,9 @@
 //                    256-thread blocks: the fastest a kernel that reads exactly those
 //                    bytes once can be, at that launch shape
 //   aqp_mfma_loop    back-to-back independent bf16 MFMAs (32x32x16 or 16x16x32) on every
-//                    SIMD, no memory traffic: the sustained dense bf16 MFMA rate
+//                    SIMD, no memory traffic: the sustained dense bf16 MFMA rate (of the
+//                    32x32x16 loop; the 16x16x32 one is compiled with its accumulators moved
+//                    between registers in every round, 52 moves for 8 MFMAs, and measures that)
 //
 // Every kernel keeps its results alive with a store that is taken only for a value
 // the inputs cannot produce, so the loads and MFMAs are not removed and nothing is

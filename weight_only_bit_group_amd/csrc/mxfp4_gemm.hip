@@ -381,9 +381,9 @@ __global__ __launch_bounds__(C::NT) void mxfp4_gemv_kernel(MxArgs a) {
 // them, so accumulators meet at branches: the matrix instructions are builtins, whose waits the
 // compiler keeps (against inline assembly with its own wait at every stage's end: 16 rows on
 // [4096, 14336] 13.9 against 14.3 us (A16) and 8.0 against 8.3 (A4), 36 products 2% on average).
-//   16 rows, graph-replayed: on [11008, 2048] 6.9 us (A16) and 4.6 (A4), on [4096, 14336] 13.9 and
-// 8.0; there the blocks of 16 columns read 118 MB of activations beside 31 MB of weights, some 40
-// bytes a clock and compute unit.
+//   16 rows, graph-replayed, over several runs: on [11008, 2048] 6.7 to 7.1 us (A16) and 4.6 to 5.0
+// (A4), on [4096, 14336] 13.3 to 14.3 and 8.0 to 8.1; there the blocks of 16 columns read 118 MB of
+// activations beside 31 MB of weights, some 40 bytes a clock and compute unit.
 template <int ROWB>
 __device__ __forceinline__ int lds_unit(int r, int u) {
   return ROWB == 128 ? u ^ ((r >> 1) & 7) : u ^ ((r >> 3) & 1);
@@ -627,10 +627,13 @@ __global__ __launch_bounds__(C::NT) void mxfp4_split_kernel(MxArgs a) {
 // The weight rows of a wave are stored so that lane c of its FN operands holds rows
 // FN c .. FN c + FN - 1: its outputs of one row are neighbours and leave in one store, 16
 // lanes 64 to 256 contiguous bytes.
-//   M = 4096 on [11008, 2048], bf16 out, graph-replayed: A4 65 to 69 us (2.8 PFLOP/s), A16 158
-// (1.17).  A4 is bound by the card's power (the clock falls to about 1.7 GHz) and by what a
-// tile of 2048 k spends outside its loop (37%); M = N = 4096, K = 14336 reaches 4.0 PFLOP/s, A16
-// 1.34.  Deeper rings, larger wave tiles, 32 x 32 instructions and two blocks a compute unit
+//   M = 4096 on [11008, 2048], bf16 out, graph-replayed: A4 67 us (2.7 PFLOP/s), A16 159 to 163 (1.15);
+// M = N = 4096, K = 14336: A4 118 (4.1), A16 364 (1.32).  A stage's matrix instructions are 2048
+// cycles of the 3050 (A4) and 2850 (A16) that it takes, the LDS is active for 990 and 1160; a tile
+// of 2048 k spends 36% (A4) and 10% (A16) of its cycles outside its loop, where the one block of a
+// compute unit leaves the matrix cores idle, and 688 tiles are 2.7 rounds.  The cycles are the same
+// on zeros, at 2.39 GHz (A4 51 us) in place of the 1.95 that the card's power allows on random
+// operands.  Deeper rings, larger wave tiles, 32 x 32 instructions and two blocks a compute unit
 // were within 5% or slower.
 template <bool A4_, int WM_, int WN_, int FM_, int FN_>
 struct MxCfg {

@@ -378,8 +378,9 @@ aq_status aq_mxfp4_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scales, int6
  * NULL (then T >= M); X [T, K].  Both lists are read on the device at the time the call
  * runs, so a captured call follows their contents.  An expert may have no rows.  Rows of Y
  * outside offsets[0] .. offsets[E] - 1 are left as they were.  A list entry outside its
- * range never leads outside the buffers: offsets are clamped to 0 .. M and to be
- * ascending, a row of Y whose rows[r] is outside X becomes NaN.
+ * range never leads outside the buffers: offsets are clamped to 0 .. M, an expert that ends
+ * before it starts has no rows, a row of Y whose rows[r] is outside X becomes NaN.  Rows that
+ * more than one expert claims, where offsets do not ascend, are unspecified.
  * Errors: as the products above; EINVAL also for E <= 0 or E >= 2^20, E * N >= 2^27,
  *         T < 0 or T >= 2^30, T < M without rows, T = 0 with M > 0, NULL / misaligned
  *         offsets or rows (4 bytes).

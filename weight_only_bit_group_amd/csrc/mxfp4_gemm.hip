@@ -126,8 +126,8 @@ struct MxTile {
 // Tile t of a grouped launch: the experts' rows cut into pieces of BM, each times the
 // column tiles, the columns fastest.  The launch has at least as many blocks as tiles;
 // blocks past them get false.  Every wave scans the offsets by itself, 64 experts at a
-// time.  Offsets are clamped to the rows of Y and to be ascending, so no value of theirs
-// leads outside the buffers.
+// time.  Offsets are clamped to the rows of Y and an expert's end to its start, so no value of
+// theirs leads outside the buffers.
 template <int BM>
 __device__ __forceinline__ bool grouped_tile(const MxArgs& a, int tiles_n, int bn, int block, MxTile& out) {
   const int lane = threadIdx.x & 63;

@@ -146,3 +146,68 @@ def test_what_is_not_finite_stays_in_its_row_and_column(lib, a4, grouped, name):
         assert bool(y[:, col].isnan().all())
         assert bool(y[row][cols].isnan().all() if a4 else y[row][cols].isinf().all())
         assert torch.equal(y[rows][:, cols], ref[rows][:, cols])
+
+
+def _few_codes(g, *lead, k):
+    """Codes of 0, 1 and -1 with factors 1: sums of K below 2^24 products are exact."""
+    nibbles = torch.tensor([0, 2, 10], dtype=U8, device="cuda")
+    pick = torch.randint(0, 3, (2, *lead, k // 2), generator=g, device="cuda")
+    return nibbles[pick[0]] | (nibbles[pick[1]] << 4), torch.full((*lead, k // 32), 127, dtype=U8, device="cuda")
+
+
+@pytest.mark.parametrize("a4", [False, True])
+@pytest.mark.parametrize("m,n,k", [(1, 19, (1 << 22) - 32), (3, 40, 2097184), (150, 70, 1048608), (2000003, 9, 64), (5, 4194303, 32)])
+def test_longest_rows_and_tallest_matrices(a4, m, n, k):
+    """Rows of nearly 2^22 k, two million rows, the most columns."""
+    from weight_only_bit_group_amd import binding as B
+    step(f"mxfp4 gemm a4={a4} {m}x{n}x{k}")
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    c, s = _few_codes(g, n, k=k)
+    if a4:
+        x = _few_codes(g, m, k=k)
+        xv = _values(*x)
+        y = B.aq_mxfp4_gemm_a4(*x, c, s)
+    else:
+        xv = torch.randint(-1, 2, (m, k), generator=g, device="cuda").double()
+        y = B.aq_mxfp4_gemm(xv.to(BF16), c, s)
+    assert torch.equal(y, (xv @ _values(c, s).t()).float())
+
+
+@pytest.mark.parametrize("a4", [False, True])
+@pytest.mark.parametrize("m,e", [(1000, 70001), (5, 1000003)])
+def test_very_many_experts(a4, m, e):
+    from weight_only_bit_group_amd import binding as B
+    n, k = 17, 64
+    step(f"mxfp4 grouped a4={a4} {m} rows over {e} experts")
+    g = torch.Generator(device="cuda").manual_seed(e)
+    c, s = _few_codes(g, e, n, k=k)
+    chosen = torch.sort(torch.randint(0, e, (m,), generator=g, device="cuda"))[0]
+    chosen[-1] = e - 1
+    off = torch.searchsorted(chosen, torch.arange(e + 1, device="cuda"), out_int32=True)
+    if a4:
+        x = _few_codes(g, m, k=k)
+        xv = _values(*x)
+        y = B.aq_mxfp4_grouped_gemm_a4(*x, c, s, off)
+    else:
+        xv = torch.randint(-1, 2, (m, k), generator=g, device="cuda").double()
+        y = B.aq_mxfp4_grouped_gemm(xv.to(BF16), c, s, off)
+    ref = (xv.unsqueeze(1) * _values(c[chosen], s[chosen])).sum(-1)
+    assert torch.equal(y, ref.float())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_quantize_and_read_back_beyond_32_bits(dtype):
+    """A matrix of more than 2^32 elements: every slice of rows as quantised by itself, and read back."""
+    from weight_only_bit_group_amd import binding as B
+    m, k = 66000, 65536 + 32
+    assert m * k > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(m, k, dtype=dtype, device="cuda").normal_(generator=g)
+    step(f"aq_mxfp4_quantize {m}x{k} {dtype}")
+    c, s = B.aq_mxfp4_quantize(x)
+    y = B.aq_mxfp4_dequantize(c, s, out_dtype=dtype)
+    for lo in range(0, m, 6000):
+        part = slice(lo, min(lo + 6000, m))
+        c1, s1 = B.aq_mxfp4_quantize(x[part])
+        assert torch.equal(c[part], c1) and torch.equal(s[part], s1)
+        assert torch.equal(y[part], B.aq_mxfp4_dequantize(c1, s1, out_dtype=dtype))

@@ -186,7 +186,7 @@ def test_gradients_are_the_formulas_or_refused(act):
 
 
 @pytest.mark.parametrize("act", ["bf16", "mxfp4"])
-@pytest.mark.parametrize("t,top", [(1, 8), (64, 8), (600, 8), (4096, 4)])
+@pytest.mark.parametrize("t,top", [(1, 8), (64, 8), (600, 8), (4096, 4), (1 << 17, 8)])
 def test_experts_captured_and_replayed(t, top, act):
     """A captured call follows its inputs over several replays, with the program's own calls between them."""
     rng = np.random.default_rng(t + top)

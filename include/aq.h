@@ -393,6 +393,29 @@ aq_status aq_mxfp4_grouped_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scal
                                    const int32_t* offsets, const int32_t* rows, int64_t M, void* Y, int32_t y_dtype,
                                    void* stream);
 
+/*
+ * FP8: E4M3 codes (one byte; 4 exponent bits of bias 7, 3 mantissa bits, largest magnitude 448, 0x7F / 0xFF NaN,
+ * no infinities: the 8-bit floating point format of the Open Compute Project that the matrix cores of gfx950
+ * multiply) with one fp32 scale for each block of 128 k of a row (block_rows 1, activations) or of 128 rows by
+ * 128 k (block_rows 128, weights).  The last block along k or the rows may be shorter: kb = ceil(K / 128),
+ * nb = ceil(N / 128).  A code c of a block with scale S stands for c S.
+ *
+ * aq_fp8_quantize: with a = max |x| of a block,
+ *   S = max(fl32(a / 448), 2^-126),   code = nearest E4M3 of fl32(x / S), ties to the even code
+ *   (IEEE divisions); the sign bit is x's, also of a zero.  A block that holds a NaN or an infinity gets S = NaN and
+ *   codes 0 (inputs need not be finite).
+ * X: E matrices [N, K] one behind the other, fp32 or bf16 (x_dtype), rows ldx elements apart (ldx >= K, a multiple
+ * of 16 bytes); codes [E, N, K]; scales [E, N, kb] (block_rows 1) or [E, nb, kb] (block_rows 128).
+ * aq_fp8_dequantize: Y [E, N, K] = fl32(c S), in bf16 rounded once more to nearest even.
+ * Errors: EINVAL for a bad dtype, block_rows other than 1 and 128, E <= 0, N < 0, E * N >= 2^30, K <= 0 or K % 16,
+ *         E * N * K >= 2^36, ldx < K or rows that are not 16 bytes aligned, NULL / misaligned pointers (X, Y, codes
+ *         16 bytes, scales 4).
+ */
+aq_status aq_fp8_quantize(const void* X, int32_t x_dtype, int64_t E, int64_t N, int64_t K, int64_t ldx,
+                          int32_t block_rows, uint8_t* codes, float* scales, void* stream);
+aq_status aq_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t E, int64_t N, int64_t K,
+                            int32_t block_rows, void* Y, int32_t y_dtype, void* stream);
+
 /* Thread-local text for the last non-OK status of this thread ("" if none). */
 const char* aq_last_error(void);
 

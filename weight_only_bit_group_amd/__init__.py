@@ -12,7 +12,8 @@ __all__ = ["aq_quantize_pack", "aq_w4a16_gemv", "aq_w4a16_gemm", "aq_w4a16_gemm_
            "aq_act_absmean_workspace", "aq_awq_search", "aq_awq_search_workspace", "aq_fp4_gemm",
            "aq_fp4_gemm_workspace", "aq_fp4_quantize", "aq_fp4_quantize_workspace", "aq_quantize_pack8",
            "aq_w8a16_gemv", "aq_w8a16_gemm", "aq_w8a16_gemm_workspace", "aq_mxfp4_quantize", "aq_mxfp4_dequantize",
-           "aq_mxfp4_gemm", "aq_mxfp4_gemm_a4", "aq_mxfp4_grouped_gemm", "aq_mxfp4_grouped_gemm_a4"]
+           "aq_mxfp4_gemm", "aq_mxfp4_gemm_a4", "aq_mxfp4_grouped_gemm", "aq_mxfp4_grouped_gemm_a4",
+           "aq_fp8_quantize", "aq_fp8_dequantize"]
 
 
 def __getattr__(name):

@@ -541,3 +541,87 @@ def aq_mxfp4_grouped_gemm_a4(X_codes, X_scales, codes, scales, offsets, rows=Non
                  scales.data_ptr(), e, n, offsets.data_ptr(), None if rows is None else rows.data_ptr(), m,
                  out.data_ptr(), code)
     return out
+
+
+# ---- FP8 (E4M3, a scale for each block of 128) ---------------------------------------------
+# As the MXFP4 calls these run on the device of their tensors.  Codes are float8_e4m3fn; uint8
+# tensors of the same bytes are taken too.
+
+_F8 = torch.float8_e4m3fn
+
+
+def _f8_codes(t, name: str, shape, dev: int) -> None:
+    """Raises unless t holds dense FP8 codes of this shape on device dev."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    _mx_need(t, name, _U8 if t.dtype == _U8 else _F8, shape, dev)
+
+
+def _f8_matrix(X, name: str, types):
+    """(shape [.., N, K], E, N, K, row stride, device) of a matrix or a stack of them whose rows are dense."""
+    if not isinstance(X, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not X.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (got {X.device})")
+    if X.dtype not in types:
+        raise ValueError(f"{name} must be {' or '.join(str(t) for t in types)} (got {X.dtype})")
+    if X.dim() not in (2, 3):
+        raise ValueError(f"{name} must have 2 or 3 dimensions")
+    n, k = X.shape[-2:]
+    e = X.shape[0] if X.dim() == 3 else 1
+    if k == 0 or k % 16:
+        raise ValueError(f"K must be a positive multiple of 16 (got {k})")
+    ld = k
+    if not X.is_contiguous() and X.numel():
+        ld = X.stride(-2) if n > 1 else X.stride(0) if e > 1 and X.dim() == 3 else k
+        if X.stride(-1) != 1 or ld < k or (e > 1 and X.stride(0) != n * ld):
+            raise ValueError(f"{name} must have dense rows, evenly spaced (strides {X.stride()})")
+    return tuple(X.shape), e, n, k, ld, X.get_device()
+
+
+def _f8_scales(shape, block_rows: int):
+    """The shape of the scales of codes [.., N, K]."""
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128 (got {block_rows})")
+    return (*shape[:-2], -(-shape[-2] // block_rows), -(-shape[-1] // 128))
+
+
+def aq_fp8_quantize(X, block_rows: int = 1, *, codes=None, scales=None):
+    """(codes [.., N, K] float8_e4m3fn, scales f32) of X [N, K] or [E, N, K] (f32 or bf16; its rows may be strided).
+
+    block_rows=1: a scale for 128 k of each row, scales [.., N, ceil(K / 128)] (activations);
+    block_rows=128: for 128 rows by 128 k, scales [.., ceil(N / 128), ceil(K / 128)] (weights).
+    """
+    shape, e, n, k, ld, dev = _f8_matrix(X, "X", _MX_OUT)
+    sshape = _f8_scales(shape, block_rows)
+    if codes is None:
+        codes = X.new_empty(shape, dtype=_F8)
+    else:
+        _f8_codes(codes, "codes", shape, dev)
+    if scales is None:
+        scales = X.new_empty(sshape, dtype=torch.float32)
+    else:
+        _mx_need(scales, "scales", torch.float32, sshape, dev)
+    if e and n:
+        _mx_call("aq_fp8_quantize", dev, X.data_ptr(), _MX_OUT[X.dtype], e, n, k, ld, block_rows, codes.data_ptr(),
+                 scales.data_ptr())
+    return codes, scales
+
+
+def aq_fp8_dequantize(codes, scales, block_rows: int = 1, out_dtype=None, out=None):
+    """Y [.., N, K] (float32, or bfloat16) = the values of codes [.., N, K] and their scales (as aq_fp8_quantize)."""
+    shape, e, n, k, _, dev = _f8_matrix(codes, "codes", (_F8, _U8))
+    _f8_codes(codes, "codes", shape, dev)
+    _mx_need(scales, "scales", torch.float32, _f8_scales(shape, block_rows), dev)
+    if out_dtype is None:
+        out_dtype = torch.float32 if out is None else out.dtype
+    code = _MX_OUT.get(out_dtype)
+    if code is None:
+        raise ValueError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
+    if out is None:
+        out = codes.new_empty(shape, dtype=out_dtype)
+    else:
+        _mx_need(out, "Y", out_dtype, shape, dev)
+    if e and n:
+        _mx_call("aq_fp8_dequantize", dev, codes.data_ptr(), scales.data_ptr(), e, n, k, block_rows, out.data_ptr(), code)
+    return out

@@ -24,7 +24,8 @@ PROBE_SOURCE = os.path.join(CSRC, "probe", "ceiling.hip")
 PROBE_PATH = os.path.join(HERE, "libaq_probe.so")
 
 HIP_SOURCES = ("quant_pack.hip", "w4a16_gemv.hip", "decode_mfma.hip", "mfma_gemm.hip", "act_absmean.hip",
-               "awq_search.hip", "fp4_gemv.hip", "fp4_quant.hip", "w8a16_gemv.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip")
+               "awq_search.hip", "fp4_gemv.hip", "fp4_quant.hip", "w8a16_gemv.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip",
+               "fp8_quant.hip")
 CPP_SOURCES = ("aq_api.cpp",)
 
 # the torch binding's native calls, a CPython module linked against libaq.so beside it

@@ -665,4 +665,49 @@ aq_status aq_mxfp4_grouped_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scal
                     Y, y_dtype, stream);
 }
 
+// E matrices [N, K] of FP8 blocks; the kernels count rows and blocks of 128 k in 32 bits
+static aq_status check_fp8_matrix(const char* fn, int64_t E, int64_t N, int64_t K, int32_t block_rows) {
+  AQ_REQUIRE(block_rows == 1 || block_rows == 128, "%s: block_rows must be 1 or 128 (got %d)", fn, block_rows);
+  AQ_REQUIRE(E > 0 && E < kDimLimit && N >= 0 && N < kDimLimit && E * N < kDimLimit,
+             "%s: E must be positive and E * N below 2^30 (E %lld, N %lld)", fn, (long long)E, (long long)N);
+  AQ_REQUIRE(K > 0 && K < kDimLimit && K % 16 == 0, "%s: K must be a positive multiple of 16 (got %lld)", fn,
+             (long long)K);
+  AQ_REQUIRE(E * N * K < (int64_t(1) << 36), "%s: E * N * K must be below 2^36", fn);
+  return AQ_OK;
+}
+
+aq_status aq_fp8_quantize(const void* X, int32_t x_dtype, int64_t E, int64_t N, int64_t K, int64_t ldx,
+                          int32_t block_rows, uint8_t* codes, float* scales, void* stream) {
+  const char* fn = "aq_fp8_quantize";
+  AQ_REQUIRE(x_dtype == AQ_F32 || x_dtype == AQ_BF16, "%s: x_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, x_dtype);
+  const aq_status st = check_fp8_matrix(fn, E, N, K, block_rows);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(ldx >= K && ldx < kDimLimit * 2 && ldx % (x_dtype == AQ_BF16 ? 8 : 4) == 0,
+             "%s: ldx (%lld) must be at least K and a multiple of 16 bytes", fn, (long long)ldx);
+  AQ_PTR(X, 16, "X");
+  AQ_PTR(codes, 16, "codes");
+  AQ_PTR(scales, 4, "scales");
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (N == 0) return ok();
+  return runtime_status(aq::launch_fp8_quantize(X, x_dtype == AQ_BF16, E, N, K, ldx, block_rows > 1, codes, scales,
+                                                (hipStream_t)stream),
+                        fn);
+}
+
+aq_status aq_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t E, int64_t N, int64_t K,
+                            int32_t block_rows, void* Y, int32_t y_dtype, void* stream) {
+  const char* fn = "aq_fp8_dequantize";
+  AQ_REQUIRE(y_dtype == AQ_F32 || y_dtype == AQ_BF16, "%s: y_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, y_dtype);
+  const aq_status st = check_fp8_matrix(fn, E, N, K, block_rows);
+  if (st != AQ_OK) return st;
+  AQ_PTR(codes, 16, "codes");
+  AQ_PTR(scales, 4, "scales");
+  AQ_PTR(Y, 16, "Y");
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (N == 0) return ok();
+  return runtime_status(aq::launch_fp8_dequantize(codes, scales, E, N, K, block_rows > 1, Y, y_dtype == AQ_BF16,
+                                                  (hipStream_t)stream),
+                        fn);
+}
+
 }  // extern "C"

@@ -75,6 +75,11 @@ hipError_t launch_mxfp4_grouped_gemm(const void* X, const uint8_t* XS, int64_t x
 // tests hold that every form is run.
 extern "C" int mxfp4_form(bool a4, bool grouped, int M, int K, int N, int E, int cus);
 extern "C" int mxfp4_form_name(bool a4, bool grouped, int form, char* to, size_t n);
+// FP8 blocks: E matrices of N rows, rows ldx elements apart; blocks: one scale for 128 x 128, else for 128 k of a row
+hipError_t launch_fp8_quantize(const void* X, bool x_bf16, int64_t E, int64_t N, int64_t K, int64_t ldx, bool blocks,
+                               uint8_t* codes, float* scales, hipStream_t stream);
+hipError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t E, int64_t N, int64_t K, bool blocks,
+                                 void* Y, bool y_bf16, hipStream_t stream);
 // compute units of the current device (cached per device)
 int device_cu_count();
 int64_t sumsq_gemm_blocks(int64_t M, int64_t N);

@@ -416,6 +416,41 @@ aq_status aq_fp8_quantize(const void* X, int32_t x_dtype, int64_t E, int64_t N, 
 aq_status aq_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t E, int64_t N, int64_t K,
                             int32_t block_rows, void* Y, int32_t y_dtype, void* stream);
 
+/*
+ * Products with FP8 weights (block_rows 128), any M >= 0:
+ *   Y[m, n] = sum_b sx[m, b] sw[n / 128, b] sum_{k in b} cx[m, k] cw[n, k]        b: blocks of 128 k
+ * aq_fp8_gemm     X given in FP8 (block_rows 1, as aq_fp8_quantize writes it)
+ * aq_fp8_linear   X [M, K] fp32 or bf16 (x_dtype, rows ldx elements apart), rounded on the way in as aq_fp8_quantize
+ *                 does: the result is that of the two calls, bit for bit.  workspace: caller-owned device memory of
+ *                 at least aq_fp8_linear_workspace(M, K) bytes, 16-byte aligned, used only during the call.
+ * fp32 Y: the products' sums are fp32 throughout (codes in bf16, on the bf16 matrix instructions).  bf16 Y: the FP8
+ * matrix instructions, twice as fast, which cut the products of eight neighbouring k off at 2^-13 of the largest of
+ * them and add the rest in fp32 (1.5e-5 of the result on normal values), then one rounding to nearest even.
+ * A block's factor is fl32(sx sw): the product of two scales of one block has to be a normal fp32 number (or
+ * the block's codes add nothing).  A call gives the same bits every time, and a row's outputs do not depend on the other rows' values.
+ * codes [N, K], scales [ceil(N / 128), ceil(K / 128)].
+ * Errors: EINVAL for a bad dtype, M < 0 or M >= 2^30, N < 0 or N >= 2^22, K <= 0, K >= 2^22 or K % 16, M * N >= 2^37,
+ *         M * K >= 2^36, ldx as aq_fp8_quantize, a small workspace, NULL / misaligned pointers (X, codes and workspace
+ *         16 bytes, scales 4, Y one element).
+ */
+aq_status aq_fp8_gemm(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
+                      const float* scales, int64_t N, void* Y, int32_t y_dtype, void* stream);
+size_t aq_fp8_linear_workspace(int64_t M, int64_t K);
+aq_status aq_fp8_linear(const void* X, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
+                        const float* scales, int64_t N, void* Y, int32_t y_dtype, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * The same product grouped by expert: E weight matrices codes [E, N, K], scales [E, ceil(N / 128), ceil(K / 128)];
+ * offsets, rows, T, M and what they may hold as for aq_mxfp4_grouped_gemm (a row of Y whose rows[r] is outside X
+ * becomes NaN, rows of Y outside the offsets are left as they were).
+ * Errors: as aq_fp8_gemm (T * K in place of M * K); EINVAL also for E <= 0 or E >= 2^20, E * N >= 2^27, T < 0 or
+ *         T >= 2^30, T < M without rows, T = 0 with M > 0, NULL / misaligned offsets or rows (4 bytes).
+ */
+aq_status aq_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, int64_t T, int64_t K, const uint8_t* codes,
+                              const float* scales, int64_t E, int64_t N, const int32_t* offsets, const int32_t* rows,
+                              int64_t M, void* Y, int32_t y_dtype, void* stream);
+
 /* Thread-local text for the last non-OK status of this thread ("" if none). */
 const char* aq_last_error(void);
 

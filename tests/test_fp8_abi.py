@@ -61,3 +61,63 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         B.aq_fp8_quantize([1.0])
     with pytest.raises(ValueError, match="block_rows"):
         B._f8_scales((4, 64), 16)
+
+
+def _g(lib, X=FAKE, XS=FAKE, M=4, K=64, C=FAKE, S=FAKE, N=8, Y=FAKE, dt=0):
+    return lib.aq_fp8_gemm(X, XS, M, K, C, S, N, Y, dt, None)
+
+
+def _l(lib, X=FAKE, xdt=1, M=4, K=64, ldx=None, C=FAKE, S=FAKE, N=8, Y=FAKE, dt=0, W=FAKE, wb=None):
+    return lib.aq_fp8_linear(X, xdt, M, K, K if ldx is None else ldx, C, S, N, Y, dt, W, 1 << 40 if wb is None else wb, None)
+
+
+def _e(lib, X=FAKE, XS=FAKE, T=4, K=64, C=FAKE, S=FAKE, E=2, N=8, off=FAKE, rows=None, M=4, Y=FAKE, dt=0):
+    return lib.aq_fp8_grouped_gemm(X, XS, T, K, C, S, E, N, off, rows, M, Y, dt, None)
+
+
+@pytest.mark.parametrize("kw", [dict(dt=2), dict(K=0), dict(K=40), dict(K=1 << 22), dict(N=-1), dict(N=1 << 22), dict(M=-1),
+                                dict(M=BIG), dict(X=None), dict(X=FAKE + 8), dict(C=None), dict(C=FAKE + 4), dict(S=None),
+                                dict(S=FAKE + 2), dict(Y=None), dict(Y=FAKE + 2), dict(dt=1, Y=FAKE + 1)])
+def test_products_einval(lib, kw):
+    for call in (_g, _l, _e):
+        assert call(lib, **kw) == _lib.AQ_EINVAL, call
+
+
+def test_products_einval_of_sizes_past_the_offsets(lib):
+    for call, kw in ((_g, {}), (_l, {}), (_e, dict(T=1 << 24))):
+        assert call(lib, M=1 << 24, K=1 << 12, **kw) == _lib.AQ_EINVAL and "2^36" in _lib.last_error()
+    for call, kw in ((_g, {}), (_l, {}), (_e, dict(T=1 << 20))):
+        assert call(lib, M=1 << 20, N=1 << 17, **kw) == _lib.AQ_EINVAL and "2^37" in _lib.last_error()
+
+
+@pytest.mark.parametrize("kw,frag", [(dict(xdt=3), "x_dtype"), (dict(ldx=56), "ldx"), (dict(ldx=68), "ldx"), (dict(W=None), "workspace"),
+                                     (dict(W=FAKE + 8), "workspace"), (dict(wb=4 * 64 + 15), "workspace")])
+def test_linear_einval(lib, kw, frag):
+    assert _l(lib, **kw) == _lib.AQ_EINVAL and frag in _lib.last_error()
+
+
+def test_linear_workspace(lib):
+    assert lib.aq_fp8_linear_workspace(4, 64) == 4 * 64 + 16 and lib.aq_fp8_linear_workspace(3, 272) == 3 * (272 + 12)
+    assert lib.aq_fp8_linear_workspace(0, 64) == lib.aq_fp8_linear_workspace(4, 40) == lib.aq_fp8_linear_workspace(-1, 64) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(E=0), dict(E=-1), dict(E=1 << 20), dict(E=1 << 19, N=1 << 8), dict(T=-1), dict(T=BIG, M=4),
+                                dict(T=3), dict(T=0, rows=FAKE), dict(off=None), dict(off=FAKE + 2), dict(rows=FAKE + 2),
+                                dict(XS=None), dict(XS=FAKE + 1)])
+def test_grouped_einval(lib, kw):
+    assert _e(lib, **kw) == _lib.AQ_EINVAL
+
+
+def test_empty_products_and_injected_failures(lib, monkeypatch):
+    assert _g(lib, M=0) == _g(lib, N=0) == _l(lib, N=0) == _l(lib, M=0, W=None) == _e(lib, M=0, T=0) == _e(lib, N=0) == _lib.AQ_OK
+    monkeypatch.setenv("AQ_FAULT_INJECT", "launch")
+    assert _g(lib) == _l(lib) == _e(lib) == _lib.AQ_ERUNTIME
+
+
+def test_binding_products_refuse_host_tensors():
+    c, s = torch.zeros(4, 64, dtype=torch.float8_e4m3fn), torch.zeros(4, 1)
+    w, ws = torch.zeros(8, 64, dtype=torch.float8_e4m3fn), torch.zeros(1, 1)
+    for call in (lambda: B.aq_fp8_gemm(c, s, w, ws), lambda: B.aq_fp8_linear(c.float(), w, ws),
+                 lambda: B.aq_fp8_grouped_gemm(c, s, w[None], ws[None], torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call()

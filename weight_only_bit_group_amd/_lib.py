@@ -46,6 +46,10 @@ SIGNATURES = {
     "aq_mxfp4_grouped_gemm_a4": (_I32, [_P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P]),
     "aq_fp8_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _I64, _I32, _P, _P, _P]),
     "aq_fp8_dequantize": (_I32, [_P, _P, _I64, _I64, _I64, _I32, _P, _I32, _P]),
+    "aq_fp8_gemm": (_I32, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P]),
+    "aq_fp8_linear_workspace": (_SZ, [_I64, _I64]),
+    "aq_fp8_linear": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _SZ, _P]),
+    "aq_fp8_grouped_gemm": (_I32, [_P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P]),
     "aq_last_error": (ctypes.c_char_p, []),
 }
 

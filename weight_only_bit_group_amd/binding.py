@@ -625,3 +625,82 @@ def aq_fp8_dequantize(codes, scales, block_rows: int = 1, out_dtype=None, out=No
     if e and n:
         _mx_call("aq_fp8_dequantize", dev, codes.data_ptr(), scales.data_ptr(), e, n, k, block_rows, out.data_ptr(), code)
     return out
+
+
+def _f8_rows(codes, scales):
+    """(rows, columns, device) of FP8 activations: codes [M, K], scales [M, ceil(K / 128)]."""
+    if getattr(codes, "ndim", 2) != 2:
+        raise ValueError("X_codes must have 2 dimensions")
+    (m, k), *_, dev = _f8_matrix(codes, "X_codes", (_F8, _U8))
+    _f8_codes(codes, "X_codes", (m, k), dev)
+    _mx_need(scales, "X_scales", torch.float32, (m, -(-k // 128)), dev)
+    return m, k, dev
+
+
+def _f8_weights(codes, scales, k: int, dev: int, ndim: int):
+    """The shape (N,) or (E, N) of FP8 weights with rows of k."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != ndim:
+        raise ValueError("codes must be [N, K]" if ndim == 2 else "codes must be [E, N, K]")
+    lead = codes.shape[:-1]
+    _f8_codes(codes, "codes", (*lead, k), dev)
+    _mx_need(scales, "scales", torch.float32, _f8_scales((*lead, k), 128), dev)
+    return lead
+
+
+def aq_fp8_gemm(X_codes, X_scales, codes, scales, out_dtype=None, out=None):
+    """Y[M, N] (float32, or bfloat16) of FP8 activations (as aq_fp8_quantize returns them) and FP8 weights, transposed.
+
+    codes [N, K], scales [ceil(N / 128), ceil(K / 128)] (as aq_fp8_quantize with block_rows=128 returns them).
+    """
+    m, k, dev = _f8_rows(X_codes, X_scales)
+    n, = _f8_weights(codes, scales, k, dev, 2)
+    out, code = _mx_out(out, m, n, out_dtype, X_codes, dev)
+    if m and n:
+        _mx_call("aq_fp8_gemm", dev, X_codes.data_ptr(), X_scales.data_ptr(), m, k, codes.data_ptr(), scales.data_ptr(), n,
+                 out.data_ptr(), code)
+    return out
+
+
+def aq_fp8_linear_workspace(M: int, K: int) -> int:
+    return int(_lib.load().aq_fp8_linear_workspace(M, K))
+
+
+def aq_fp8_linear(X, codes, scales, out_dtype=None, out=None, workspace=None):
+    """Y[M, N] (float32, or bfloat16) = X[M, K] (f32 or bf16, rounded to FP8 on the way; its rows may be strided) times
+    the FP8 weights, transposed.
+
+    workspace: None allocates it; a uint8 device tensor is used as given.
+    """
+    if getattr(X, "ndim", 2) != 2:
+        raise ValueError("X must have 2 dimensions")
+    (m, k), _, _, _, ld, dev = _f8_matrix(X, "X", _MX_OUT)
+    n, = _f8_weights(codes, scales, k, dev, 2)
+    out, code = _mx_out(out, m, n, out_dtype, X, dev)
+    if m and n:
+        if workspace is None:
+            workspace = X.new_empty(aq_fp8_linear_workspace(m, k), dtype=_U8)
+        else:
+            _need(workspace, "workspace", _U8, 1)
+            if workspace.get_device() != dev:
+                raise ValueError(f"workspace must be on cuda:{dev} (got {workspace.device})")
+        _mx_call("aq_fp8_linear", dev, X.data_ptr(), _MX_OUT[X.dtype], m, k, ld, codes.data_ptr(), scales.data_ptr(), n,
+                 out.data_ptr(), code, workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def aq_fp8_grouped_gemm(X_codes, X_scales, codes, scales, offsets, rows=None, out_dtype=None, out=None):
+    """Y[M, N]: rows offsets[e] .. offsets[e + 1] - 1 are X's rows (or those that ``rows`` [M] lists) times expert
+    e's FP8 weights, transposed.
+
+    X_codes [T, K], X_scales [T, ceil(K / 128)], codes [E, N, K], scales [E, ceil(N / 128), ceil(K / 128)], offsets
+    [E + 1] int32 and rows int32 on the device.  Rows of Y outside the offsets are not written.
+    """
+    t, k, dev = _f8_rows(X_codes, X_scales)
+    e, n = _f8_weights(codes, scales, k, dev, 3)
+    m = _mx_lists(offsets, rows, e, t, dev)
+    out, code = _mx_out(out, m, n, out_dtype, X_codes, dev)
+    if m and n:
+        _mx_call("aq_fp8_grouped_gemm", dev, X_codes.data_ptr(), X_scales.data_ptr(), t, k, codes.data_ptr(),
+                 scales.data_ptr(), e, n, offsets.data_ptr(), None if rows is None else rows.data_ptr(), m, out.data_ptr(),
+                 code)
+    return out

@@ -25,7 +25,7 @@ PROBE_PATH = os.path.join(HERE, "libaq_probe.so")
 
 HIP_SOURCES = ("quant_pack.hip", "w4a16_gemv.hip", "decode_mfma.hip", "mfma_gemm.hip", "act_absmean.hip",
                "awq_search.hip", "fp4_gemv.hip", "fp4_quant.hip", "w8a16_gemv.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip",
-               "fp8_quant.hip")
+               "fp8_quant.hip", "fp8_gemm.hip")
 CPP_SOURCES = ("aq_api.cpp",)
 
 # the torch binding's native calls, a CPython module linked against libaq.so beside it
@@ -51,9 +51,10 @@ def _hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build libaq)")
 
 
-# Per-file extra flags: the GEMMs keep MFMA accumulators in VGPRs (the fp32
+# Per-file extra flags: these GEMMs keep MFMA accumulators in VGPRs (the fp32
 # group rescale operates on them with plain VALU FMAs).
-FILE_FLAGS = {"mfma_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]}
+FILE_FLAGS = {"mfma_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"],
+              "fp8_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]}
 
 
 def _compile(src: str) -> str:

@@ -710,4 +710,88 @@ aq_status aq_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t E
                         fn);
 }
 
+// X: T rows of codes.  The kernels count X in 16-byte units of 32 bits, a tile's weights in bytes of 31, and a launch
+// of the largest tiles, a thread for 128 outputs, has fewer than 2^32 threads.
+static aq_status check_fp8_product(const char* fn, int64_t T, int64_t M, int64_t K, const uint8_t* codes,
+                                   const float* scales, int64_t E, int64_t N, const void* Y, int32_t y_dtype) {
+  AQ_REQUIRE(y_dtype == AQ_F32 || y_dtype == AQ_BF16, "%s: y_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, y_dtype);
+  AQ_REQUIRE(M >= 0 && M < kDimLimit, "%s: M out of range (%lld)", fn, (long long)M);
+  AQ_REQUIRE(T >= 0 && T < kDimLimit, "%s: T out of range (%lld)", fn, (long long)T);
+  AQ_REQUIRE(K > 0 && K < kGemmDimLimit && K % 16 == 0, "%s: K must be a positive multiple of 16 below 2^22 (got %lld)",
+             fn, (long long)K);
+  AQ_REQUIRE(N >= 0 && N < kGemmDimLimit, "%s: N out of range (%lld)", fn, (long long)N);
+  AQ_REQUIRE(T * K < (int64_t(1) << 36), "%s: X must be below 2^36 bytes (%lld rows)", fn, (long long)T);
+  AQ_REQUIRE(M * N < (int64_t(1) << 37), "%s: M * N must be below 2^37 (M %lld, N %lld)", fn, (long long)M, (long long)N);
+  AQ_REQUIRE(E > 0 && E < (int64_t(1) << 20), "%s: E out of range (%lld)", fn, (long long)E);
+  AQ_REQUIRE(E * N < (int64_t(1) << 27), "%s: E * N must be below 2^27 (E %lld, N %lld)", fn, (long long)E, (long long)N);
+  AQ_PTR(codes, 16, "codes");
+  AQ_PTR(scales, 4, "scales");
+  AQ_PTR(Y, y_dtype == AQ_BF16 ? 2 : 4, "Y");
+  return AQ_OK;
+}
+
+aq_status aq_fp8_gemm(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
+                      const float* scales, int64_t N, void* Y, int32_t y_dtype, void* stream) {
+  const char* fn = "aq_fp8_gemm";
+  const aq_status st = check_fp8_product(fn, M, M, K, codes, scales, 1, N, Y, y_dtype);
+  if (st != AQ_OK) return st;
+  AQ_PTR(x_codes, 16, "x_codes");
+  AQ_PTR(x_scales, 4, "x_scales");
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (M == 0 || N == 0) return ok();
+  return runtime_status(aq::launch_fp8_gemm(x_codes, x_scales, (int)M, (int)K, codes, scales, 1, (int)N, nullptr, nullptr,
+                                            (int)M, Y, y_dtype == AQ_BF16, (hipStream_t)stream),
+                        fn);
+}
+
+size_t aq_fp8_linear_workspace(int64_t M, int64_t K) {
+  if (M <= 0 || M >= kDimLimit || K <= 0 || K >= kGemmDimLimit || K % 16) return 0;
+  return (size_t)M * (size_t)K + (size_t)M * (size_t)((K + 127) / 128) * sizeof(float);
+}
+
+aq_status aq_fp8_linear(const void* X, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
+                        const float* scales, int64_t N, void* Y, int32_t y_dtype, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const char* fn = "aq_fp8_linear";
+  AQ_REQUIRE(x_dtype == AQ_F32 || x_dtype == AQ_BF16, "%s: x_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, x_dtype);
+  aq_status st = check_fp8_product(fn, M, M, K, codes, scales, 1, N, Y, y_dtype);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(ldx >= K && ldx < kDimLimit * 2 && ldx % (x_dtype == AQ_BF16 ? 8 : 4) == 0,
+             "%s: ldx (%lld) must be at least K and a multiple of 16 bytes", fn, (long long)ldx);
+  AQ_PTR(X, 16, "X");
+  const size_t need = aq_fp8_linear_workspace(M, K);
+  if (M > 0) {
+    AQ_PTR(workspace, 16, "workspace");
+    AQ_REQUIRE(workspace_bytes >= need, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+  }
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (M == 0 || N == 0) return ok();
+  auto* x_codes = static_cast<uint8_t*>(workspace);
+  auto* x_scales = reinterpret_cast<float*>(x_codes + M * K);
+  hipError_t e = aq::launch_fp8_quantize(X, x_dtype == AQ_BF16, 1, M, K, ldx, false, x_codes, x_scales, (hipStream_t)stream);
+  if (e == hipSuccess)
+    e = aq::launch_fp8_gemm(x_codes, x_scales, (int)M, (int)K, codes, scales, 1, (int)N, nullptr, nullptr, (int)M, Y,
+                            y_dtype == AQ_BF16, (hipStream_t)stream);
+  return runtime_status(e, fn);
+}
+
+aq_status aq_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, int64_t T, int64_t K, const uint8_t* codes,
+                              const float* scales, int64_t E, int64_t N, const int32_t* offsets, const int32_t* rows,
+                              int64_t M, void* Y, int32_t y_dtype, void* stream) {
+  const char* fn = "aq_fp8_grouped_gemm";
+  const aq_status st = check_fp8_product(fn, T, M, K, codes, scales, E, N, Y, y_dtype);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(M == 0 || (T > 0 && (rows != nullptr || T >= M)), "%s: X has %lld rows for %lld rows of Y", fn, (long long)T,
+             (long long)M);
+  AQ_PTR(x_codes, 16, "x_codes");
+  AQ_PTR(x_scales, 4, "x_scales");
+  AQ_PTR(offsets, 4, "offsets");
+  AQ_REQUIRE(aligned(rows, 4), "%s: rows must be 4-byte aligned", fn);
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (M == 0 || N == 0) return ok();
+  return runtime_status(aq::launch_fp8_gemm(x_codes, x_scales, (int)T, (int)K, codes, scales, (int)E, (int)N, offsets, rows,
+                                            (int)M, Y, y_dtype == AQ_BF16, (hipStream_t)stream),
+                        fn);
+}
+
 }  // extern "C"

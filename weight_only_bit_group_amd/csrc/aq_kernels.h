@@ -80,6 +80,11 @@ hipError_t launch_fp8_quantize(const void* X, bool x_bf16, int64_t E, int64_t N,
                                uint8_t* codes, float* scales, hipStream_t stream);
 hipError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t E, int64_t N, int64_t K, bool blocks,
                                  void* Y, bool y_bf16, hipStream_t stream);
+// Products of FP8 rows X [T, K] with scales XS [T, ceil(K / 128)] and weights in 128 x 128 blocks.  offsets NULL: dense
+// (E = 1, T = M); else grouped by expert, rows NULL or [M]
+hipError_t launch_fp8_gemm(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
+                           int N, const int32_t* offsets, const int32_t* rows, int M, void* Y, bool y_bf16,
+                           hipStream_t stream);
 // compute units of the current device (cached per device)
 int device_cu_count();
 int64_t sumsq_gemm_blocks(int64_t M, int64_t N);

@@ -45,6 +45,7 @@ extern "C" {
 
 typedef enum { AQ_OK = 0, AQ_EINVAL = 1, AQ_ERUNTIME = 2 } aq_status;
 typedef enum { AQ_F32 = 0, AQ_BF16 = 1 } aq_dtype;
+typedef enum { AQ_SOFTMAX = 0, AQ_SIGMOID = 1 } aq_score;
 
 /*
  * Group-wise asymmetric INT4 quantization and packing.
@@ -450,6 +451,75 @@ aq_status aq_fp8_linear(const void* X, int32_t x_dtype, int64_t M, int64_t K, in
 aq_status aq_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, int64_t T, int64_t K, const uint8_t* codes,
                               const float* scales, int64_t E, int64_t N, const int32_t* offsets, const int32_t* rows,
                               int64_t M, void* Y, int32_t y_dtype, void* stream);
+
+/*
+ * The gated activation between an expert's products: h = silu(g) u of rows [g | u] (H [M, 2 I], fp32 or bf16),
+ * silu(g) = g / (1 + exp(-g)) in fp32, rounded to FP8 rows as aq_fp8_quantize rounds (block_rows 1): codes [M, I],
+ * scales [M, ceil(I / 128)].  end: NULL, or a device int32: rows from *end on are neither read nor written.
+ * Errors: EINVAL for a bad dtype, M < 0 or M >= 2^30, I <= 0, I >= 2^22 or I % 16, M * I >= 2^36, NULL / misaligned
+ *         pointers (H, codes 16 bytes; scales, end 4).
+ */
+aq_status aq_fp8_swiglu_quantize(const void* H, int32_t h_dtype, int64_t M, int64_t I, const int32_t* end, uint8_t* codes,
+                                 float* scales, void* stream);
+
+/*
+ * Routing of tokens to experts.  For each token with logits l [E] (fp32 or bf16, rows ld elements apart):
+ *   s = softmax(l) or sigmoid(l) (score: AQ_SOFTMAX, AQ_SIGMOID);  key = s + bias (fp32 [E]), or, when bias is NULL,
+ *   the logits order the experts;
+ *   an expert with l = -inf or key = -inf is never chosen;
+ *   groups > 1: the experts form `groups` equal runs of neighbours; a run's score is the sum of its two highest keys
+ *   (s without a bias; the highest alone where only one can be chosen), and only the experts of the top_groups best
+ *   runs (ties: the lower one) can be chosen;
+ *   chosen: the `top` highest keys, in descending order, ties to the lowest index; when fewer than top can be
+ *   chosen, the slots left over get id -1 and weight 0;
+ *   weight of choice j: scale * s_j / sum_i s_i over the chosen ones (renormalize; 0 where that sum is 0), or
+ *   scale * s_j.
+ * Everything is formed in 64 bits and the weights are rounded once.  A token with a NaN among its keys, or +inf under
+ * softmax, gets ids 0 .. top - 1 and weights NaN.
+ * ids [T, top] int32, weights [T, top] fp32.
+ * aq_moe_route_backward: dlogits [T, E] (the logits' type, dense) = the gradient of sum(dweights * weights) at
+ * those choices (ids and weights as aq_moe_route wrote them; a bias has no gradient).  NaN weights give the chosen
+ * experts NaN.
+ * Errors: EINVAL for a bad dtype or score, T < 0 or T >= 2^30, E <= 0 or E > 1024, top <= 0, top > E or top > 64,
+ *         T * top >= 2^31, ld < E or ld >= 2^30, groups <= 0, groups > 64 or E % groups, top_groups <= 0,
+ *         top_groups > groups or fewer than top experts in them, a scale that is not finite, NULL / misaligned
+ *         pointers (one element).
+ */
+aq_status aq_moe_route(const void* logits, int32_t l_dtype, int64_t T, int64_t E, int64_t ld, int64_t top, int32_t score,
+                       const float* bias, int32_t groups, int32_t top_groups, int32_t renormalize, float scale,
+                       int32_t* ids, float* weights, void* stream);
+aq_status aq_moe_route_backward(const void* logits, int32_t l_dtype, int64_t T, int64_t E, int64_t ld, int64_t top,
+                                int32_t score, int32_t renormalize, float scale, const int32_t* ids, const float* weights,
+                                const float* dweights, void* dlogits, void* stream);
+
+/*
+ * A router's choices grouped by expert, in front of the grouped products.  ids [T, top] int32; choice i = t top + j
+ * with an id outside 0 .. E - 1 belongs to no expert.
+ *   offsets [E + 1]: the choices of expert e take the slots offsets[e] .. offsets[e + 1] - 1, in the order of i;
+ *   rows [T top]:    the token of each slot (slots from offsets[E] on: not written);
+ *   slots [T top]:   the slot of each choice, -1 for one without an expert.
+ * workspace: aq_moe_group_workspace(T, top, E) bytes of device memory (0 up to 16384 choices), 4-byte aligned, used
+ * only during the call.
+ * Errors: EINVAL for T < 0 or T >= 2^30, E <= 0 or E > 1024, top <= 0, T * top >= 2^31, a small workspace, NULL /
+ *         misaligned pointers (4 bytes).  T = 0 writes the offsets.
+ */
+size_t aq_moe_group_workspace(int64_t T, int64_t top, int64_t E);
+aq_status aq_moe_group(const int32_t* ids, int64_t T, int64_t top, int64_t E, int32_t* offsets, int32_t* rows,
+                       int32_t* slots, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The weighted sum over a token's choices, behind the grouped products:
+ *   out[t] = sum_j weights[t, j] Y[slots[t, j]]        in the order of j, fp32 sums
+ * Y [R, K] fp32 or bf16, slots [T, top] int32 (outside 0 .. R - 1: adds nothing, whatever its weight holds), weights
+ * [T, top] fp32, out [T, K] fp32 or bf16 rounded once.
+ * aq_moe_combine_backward: dweights[t, j] = sum_k dout[t, k] Y[slots[t, j], k], fp32 sums; 0 for a slot outside.
+ * Errors: EINVAL for a bad dtype, T < 0 or T >= 2^30, top <= 0, T * top >= 2^31, R < 0, R >= 2^31 or R = 0 with T > 0,
+ *         K <= 0, K >= 2^22 or K % 8, T * K >= 2^36, NULL / misaligned pointers (Y, out, dout 16 bytes, others 4).
+ */
+aq_status aq_moe_combine(const void* Y, int32_t y_dtype, int64_t R, int64_t K, const int32_t* slots, const float* weights,
+                         int64_t T, int64_t top, void* out, int32_t out_dtype, void* stream);
+aq_status aq_moe_combine_backward(const void* Y, int32_t y_dtype, int64_t R, int64_t K, const int32_t* slots, int64_t T,
+                                  int64_t top, const void* dout, int32_t dout_dtype, float* dweights, void* stream);
 
 /* Thread-local text for the last non-OK status of this thread ("" if none). */
 const char* aq_last_error(void);

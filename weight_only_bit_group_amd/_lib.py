@@ -50,6 +50,13 @@ SIGNATURES = {
     "aq_fp8_linear_workspace": (_SZ, [_I64, _I64]),
     "aq_fp8_linear": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _SZ, _P]),
     "aq_fp8_grouped_gemm": (_I32, [_P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P]),
+    "aq_fp8_swiglu_quantize": (_I32, [_P, _I32, _I64, _I64, _P, _P, _P, _P]),
+    "aq_moe_route": (_I32, [_P, _I32, _I64, _I64, _I64, _I64, _I32, _P, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P]),
+    "aq_moe_route_backward": (_I32, [_P, _I32, _I64, _I64, _I64, _I64, _I32, _I32, ctypes.c_float, _P, _P, _P, _P, _P]),
+    "aq_moe_group_workspace": (_SZ, [_I64, _I64, _I64]),
+    "aq_moe_group": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "aq_moe_combine": (_I32, [_P, _I32, _I64, _I64, _P, _P, _I64, _I64, _P, _I32, _P]),
+    "aq_moe_combine_backward": (_I32, [_P, _I32, _I64, _I64, _P, _I64, _I64, _P, _I32, _P, _P]),
     "aq_last_error": (ctypes.c_char_p, []),
 }
 

@@ -704,3 +704,155 @@ def aq_fp8_grouped_gemm(X_codes, X_scales, codes, scales, offsets, rows=None, ou
                  scales.data_ptr(), e, n, offsets.data_ptr(), None if rows is None else rows.data_ptr(), m, out.data_ptr(),
                  code)
     return out
+
+
+def aq_fp8_swiglu_quantize(H, end=None, *, codes=None, scales=None):
+    """(codes [M, I] float8_e4m3fn, scales [M, ceil(I / 128)] f32) of silu(g) * u for rows [g | u] of H [M, 2 I] (f32 or
+    bf16); end: rows from this device count (int32 [1]) on are left out."""
+    if getattr(H, "ndim", 2) != 2:
+        raise ValueError("H must have 2 dimensions")
+    (m, k), *_, dev = _f8_matrix(H, "H", _MX_OUT)
+    _need(H, "H", H.dtype)
+    if k % 32:
+        raise ValueError(f"H must be [M, 2 I] with I a multiple of 16 (got {list(H.shape)})")
+    shape = (m, k // 2)
+    if end is not None:
+        _mx_need(end, "end", torch.int32, (1,), dev)
+    if codes is None:
+        codes = H.new_empty(shape, dtype=_F8)
+    else:
+        _f8_codes(codes, "codes", shape, dev)
+    if scales is None:
+        scales = H.new_empty(_f8_scales(shape, 1), dtype=torch.float32)
+    else:
+        _mx_need(scales, "scales", torch.float32, _f8_scales(shape, 1), dev)
+    if m:
+        _mx_call("aq_fp8_swiglu_quantize", dev, H.data_ptr(), _MX_OUT[H.dtype], m, k // 2, _ptr(end), codes.data_ptr(),
+                 scales.data_ptr())
+    return codes, scales
+
+
+# ---- routing to experts --------------------------------------------------------------------
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _logits(logits):
+    """(T, E, row stride, device) of router logits [T, E] whose rows are dense."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError(f"logits must be a GPU tensor (got {logits.device})")
+    if logits.dtype not in _MX_OUT:
+        raise ValueError(f"logits must be float32 or bfloat16 (got {logits.dtype})")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    t, e = logits.shape
+    ld = logits.stride(0) if t > 1 else e
+    if t and e and (logits.stride(1) != 1 and e > 1 or ld < e):
+        raise ValueError(f"logits must have dense rows (strides {logits.stride()})")
+    return t, e, ld, logits.get_device()
+
+
+def _score(score: str) -> int:
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid' (got {score!r})")
+    return _SCORES[score]
+
+
+def aq_moe_route(logits, top: int, *, score: str = "softmax", bias=None, groups: int = 1, top_groups: int | None = None,
+                 renormalize: bool = True, scale: float = 1.0):
+    """(ids [T, top] int32, weights [T, top] f32) of router logits [T, E] (f32 or bf16; rows may be strided).
+
+    score: "softmax" or "sigmoid"; bias [E] f32 is added to the scores for the choice alone; groups > 1 keeps the
+    experts of the top_groups best runs of E / groups neighbours; renormalize divides a token's weights by their sum.
+    An expert whose logit is -inf is never chosen; slots left over get id -1 and weight 0.
+    """
+    t, e, ld, dev = _logits(logits)
+    if bias is not None:
+        _mx_need(bias, "bias", torch.float32, (e,), dev)
+    if not 0 < top <= min(e, 64):
+        raise ValueError(f"top must be 1 .. 64 and at most E (got {top} of {e})")
+    ids = logits.new_empty((t, top), dtype=torch.int32)
+    weights = logits.new_empty((t, top), dtype=torch.float32)
+    _mx_call("aq_moe_route", dev, logits.data_ptr() or 16, _MX_OUT[logits.dtype], t, e, ld, top, _score(score), _ptr(bias),
+             groups, groups if top_groups is None else top_groups, int(renormalize), float(scale), ids.data_ptr() or 16,
+             weights.data_ptr() or 16)
+    return ids, weights
+
+
+def aq_moe_route_backward(logits, ids, weights, dweights, *, score: str = "softmax", renormalize: bool = True,
+                          scale: float = 1.0):
+    """dlogits [T, E] (the logits' type): the gradient of sum(dweights * weights) at the choices that aq_moe_route made."""
+    t, e, ld, dev = _logits(logits)
+    if getattr(ids, "ndim", 0) != 2:
+        raise ValueError("ids must be [T, top]")
+    shape = (t, ids.shape[1])
+    _mx_need(ids, "ids", torch.int32, shape, dev)
+    _mx_need(weights, "weights", torch.float32, shape, dev)
+    _mx_need(dweights, "dweights", torch.float32, shape, dev)
+    dlogits = torch.empty((t, e), dtype=logits.dtype, device=logits.device)
+    if t:
+        _mx_call("aq_moe_route_backward", dev, logits.data_ptr(), _MX_OUT[logits.dtype], t, e, ld, shape[1], _score(score),
+                 int(renormalize), float(scale), ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr())
+    return dlogits
+
+
+def aq_moe_group_workspace(T: int, top: int, E: int) -> int:
+    return int(_lib.load().aq_moe_group_workspace(T, top, E))
+
+
+def aq_moe_group(ids, E: int, workspace=None):
+    """(offsets [E + 1], rows [T * top], slots [T, top]), int32: choices ids [T, top] (int32) grouped by expert.
+
+    Expert e's choices take the slots offsets[e] .. offsets[e + 1] - 1 in the order of their tokens; rows gives each
+    slot's token, slots each choice's slot, -1 for an id outside 0 .. E - 1.  rows[offsets[E]:] is not written.
+    """
+    _need(ids, "ids", torch.int32, 2)
+    t, top = ids.shape
+    dev = ids.get_device()
+    if not 0 < E <= 1024 or top == 0:
+        raise ValueError(f"ids must be [T, top] of 1 .. 1024 experts (got {list(ids.shape)}, E {E})")
+    offsets, rows, slots = ids.new_empty(E + 1), ids.new_empty(t * top), torch.empty_like(ids)
+    if workspace is None:
+        need = aq_moe_group_workspace(t, top, E)
+        workspace = ids.new_empty(need, dtype=_U8) if need else None
+    else:
+        _need(workspace, "workspace", _U8, 1)
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace must be on cuda:{dev} (got {workspace.device})")
+    # (an empty tensor has no address; nothing is read there)
+    _mx_call("aq_moe_group", dev, ids.data_ptr() or 16, t, top, E, offsets.data_ptr(), rows.data_ptr() or 16,
+             slots.data_ptr() or 16, _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return offsets, rows, slots
+
+
+def _combine_args(Y, slots):
+    _need(Y, "Y", Y.dtype if isinstance(Y, torch.Tensor) and Y.dtype in _MX_OUT else torch.float32, 2)
+    dev = Y.get_device()
+    _need(slots, "slots", torch.int32, 2)
+    _mx_need(slots, "slots", torch.int32, slots.shape, dev)
+    return *Y.shape, *slots.shape, dev
+
+
+def aq_moe_combine(Y, slots, weights, out_dtype=None, out=None):
+    """out [T, K] (float32, or bfloat16) = sum_j weights[t, j] Y[slots[t, j]] of Y [R, K] (f32 or bf16), slots [T, top]
+    int32 (outside 0 .. R - 1: adds nothing) and weights [T, top] f32."""
+    r, k, t, top, dev = _combine_args(Y, slots)
+    _mx_need(weights, "weights", torch.float32, (t, top), dev)
+    out, code = _mx_out(out, t, k, out_dtype, Y, dev)
+    if t and k:
+        _mx_call("aq_moe_combine", dev, Y.data_ptr() or 16, _MX_OUT[Y.dtype], r, k, slots.data_ptr(), weights.data_ptr(), t, top,
+                 out.data_ptr(), code)
+    return out
+
+
+def aq_moe_combine_backward(Y, slots, dout):
+    """dweights [T, top] f32 = sum_k dout[t, k] Y[slots[t, j], k]; 0 for a slot outside 0 .. R - 1."""
+    r, k, t, top, dev = _combine_args(Y, slots)
+    _mx_need(dout, "dout", dout.dtype if getattr(dout, "dtype", None) in _MX_OUT else torch.float32, (t, k), dev)
+    dweights = torch.zeros((t, top), dtype=torch.float32, device=Y.device) if k == 0 else Y.new_empty((t, top), dtype=torch.float32)
+    if t and k:
+        _mx_call("aq_moe_combine_backward", dev, Y.data_ptr() or 16, _MX_OUT[Y.dtype], r, k, slots.data_ptr(), t, top,
+                 dout.data_ptr(), _MX_OUT[dout.dtype], dweights.data_ptr())
+    return dweights

@@ -25,7 +25,7 @@ PROBE_PATH = os.path.join(HERE, "libaq_probe.so")
 
 HIP_SOURCES = ("quant_pack.hip", "w4a16_gemv.hip", "decode_mfma.hip", "mfma_gemm.hip", "act_absmean.hip",
                "awq_search.hip", "fp4_gemv.hip", "fp4_quant.hip", "w8a16_gemv.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip",
-               "fp8_quant.hip", "fp8_gemm.hip")
+               "fp8_quant.hip", "fp8_gemm.hip", "moe_route.hip", "moe_group.hip")
 CPP_SOURCES = ("aq_api.cpp",)
 
 # the torch binding's native calls, a CPython module linked against libaq.so beside it

@@ -794,4 +794,147 @@ aq_status aq_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, int
                         fn);
 }
 
+aq_status aq_fp8_swiglu_quantize(const void* H, int32_t h_dtype, int64_t M, int64_t I, const int32_t* end, uint8_t* codes,
+                                 float* scales, void* stream) {
+  const char* fn = "aq_fp8_swiglu_quantize";
+  AQ_REQUIRE(h_dtype == AQ_F32 || h_dtype == AQ_BF16, "%s: h_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, h_dtype);
+  AQ_REQUIRE(M >= 0 && M < kDimLimit, "%s: M out of range (%lld)", fn, (long long)M);
+  AQ_REQUIRE(I > 0 && I < kGemmDimLimit && I % 16 == 0, "%s: I must be a positive multiple of 16 below 2^22 (got %lld)",
+             fn, (long long)I);
+  AQ_REQUIRE(M * I < (int64_t(1) << 36), "%s: M * I must be below 2^36", fn);
+  AQ_PTR(H, 16, "H");
+  AQ_PTR(codes, 16, "codes");
+  AQ_PTR(scales, 4, "scales");
+  AQ_REQUIRE(aligned(end, 4), "%s: end must be 4-byte aligned", fn);
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (M == 0) return ok();
+  return runtime_status(aq::launch_fp8_swiglu_quantize(H, h_dtype == AQ_BF16, M, (int)I, end, codes, scales,
+                                                       (hipStream_t)stream),
+                        fn);
+}
+
+// T tokens with `top` of E experts each
+static aq_status check_choices(const char* fn, int64_t T, int64_t E, int64_t top) {
+  AQ_REQUIRE(T >= 0 && T < kDimLimit, "%s: T out of range (%lld)", fn, (long long)T);
+  AQ_REQUIRE(E > 0 && E <= 1024, "%s: E must be 1 .. 1024 (got %lld)", fn, (long long)E);
+  AQ_REQUIRE(top > 0 && T * top < (int64_t(1) << 31), "%s: top must be positive and T * top below 2^31 (T %lld, top %lld)",
+             fn, (long long)T, (long long)top);
+  return AQ_OK;
+}
+
+static aq_status route_args(const char* fn, const void* logits, int32_t l_dtype, int64_t T, int64_t E, int64_t ld,
+                            int64_t top, int32_t score, const int32_t* ids, const float* weights) {
+  AQ_REQUIRE(l_dtype == AQ_F32 || l_dtype == AQ_BF16, "%s: l_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, l_dtype);
+  AQ_REQUIRE(score == AQ_SOFTMAX || score == AQ_SIGMOID, "%s: score must be AQ_SOFTMAX or AQ_SIGMOID (got %d)", fn, score);
+  const aq_status st = check_choices(fn, T, E, top);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(top <= E && top <= 64, "%s: top must be at most E and 64 (got %lld of %lld)", fn, (long long)top, (long long)E);
+  AQ_REQUIRE(ld >= E && ld < kDimLimit, "%s: ld (%lld) must be at least E", fn, (long long)ld);
+  AQ_PTR(logits, l_dtype == AQ_BF16 ? 2 : 4, "logits");
+  AQ_PTR(ids, 4, "ids");
+  AQ_PTR(weights, 4, "weights");
+  return AQ_OK;
+}
+
+aq_status aq_moe_route(const void* logits, int32_t l_dtype, int64_t T, int64_t E, int64_t ld, int64_t top, int32_t score,
+                       const float* bias, int32_t groups, int32_t top_groups, int32_t renormalize, float scale,
+                       int32_t* ids, float* weights, void* stream) {
+  const char* fn = "aq_moe_route";
+  const aq_status st = route_args(fn, logits, l_dtype, T, E, ld, top, score, ids, weights);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(groups > 0 && groups <= 64 && E % groups == 0, "%s: groups must be 1 .. 64 and divide E (got %d of %lld)", fn,
+             groups, (long long)E);
+  AQ_REQUIRE(top_groups > 0 && top_groups <= groups && top <= E / groups * top_groups,
+             "%s: top_groups must be 1 .. groups and hold top experts (got %d)", fn, top_groups);
+  AQ_REQUIRE(std::isfinite(scale), "%s: scale must be finite", fn);
+  AQ_REQUIRE(aligned(bias, 4), "%s: bias must be 4-byte aligned", fn);
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (T == 0) return ok();
+  const aq::RouteArgs a = {logits, bias, T, ld, (int)E, (int)top, groups, top_groups, 0, score == AQ_SIGMOID,
+                           renormalize != 0, scale, ids, weights};
+  return runtime_status(aq::launch_moe_route(a, l_dtype == AQ_BF16, (hipStream_t)stream), fn);
+}
+
+aq_status aq_moe_route_backward(const void* logits, int32_t l_dtype, int64_t T, int64_t E, int64_t ld, int64_t top,
+                                int32_t score, int32_t renormalize, float scale, const int32_t* ids, const float* weights,
+                                const float* dweights, void* dlogits, void* stream) {
+  const char* fn = "aq_moe_route_backward";
+  const aq_status st = route_args(fn, logits, l_dtype, T, E, ld, top, score, ids, weights);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(std::isfinite(scale), "%s: scale must be finite", fn);
+  AQ_PTR(dweights, 4, "dweights");
+  AQ_PTR(dlogits, l_dtype == AQ_BF16 ? 2 : 4, "dlogits");
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (T == 0) return ok();
+  const aq::RouteArgs a = {logits, nullptr, T, ld, (int)E, (int)top, 1, 1, 0, score == AQ_SIGMOID, renormalize != 0, scale,
+                           const_cast<int32_t*>(ids), const_cast<float*>(weights)};
+  return runtime_status(aq::launch_moe_route_backward(a, l_dtype == AQ_BF16, dweights, dlogits, (hipStream_t)stream), fn);
+}
+
+size_t aq_moe_group_workspace(int64_t T, int64_t top, int64_t E) {
+  if (T <= 0 || T >= kDimLimit || top <= 0 || T * top >= (int64_t(1) << 31) || E <= 0 || E > 1024) return 0;
+  return aq::moe_group_workspace_bytes(T * top, (int)E);
+}
+
+aq_status aq_moe_group(const int32_t* ids, int64_t T, int64_t top, int64_t E, int32_t* offsets, int32_t* rows,
+                       int32_t* slots, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "aq_moe_group";
+  const aq_status st = check_choices(fn, T, E, top);
+  if (st != AQ_OK) return st;
+  AQ_PTR(ids, 4, "ids");
+  AQ_PTR(offsets, 4, "offsets");
+  AQ_PTR(rows, 4, "rows");
+  AQ_PTR(slots, 4, "slots");
+  const size_t need = aq_moe_group_workspace(T, top, E);
+  AQ_REQUIRE(workspace_bytes >= need, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+  if (need) AQ_PTR(workspace, 4, "workspace");
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  return runtime_status(aq::launch_moe_group(ids, T * top, (int)top, (int)E, offsets, rows, slots,
+                                             static_cast<uint32_t*>(workspace), (hipStream_t)stream),
+                        fn);
+}
+
+static aq_status check_combine(const char* fn, const void* Y, int32_t y_dtype, int64_t R, int64_t K, const int32_t* slots,
+                               int64_t T, int64_t top, int32_t out_dtype) {
+  AQ_REQUIRE(y_dtype == AQ_F32 || y_dtype == AQ_BF16, "%s: y_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, y_dtype);
+  AQ_REQUIRE(out_dtype == AQ_F32 || out_dtype == AQ_BF16, "%s: out_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, out_dtype);
+  const aq_status st = check_choices(fn, T, 1, top);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(R >= 0 && R < (int64_t(1) << 31) && (R > 0 || T == 0), "%s: R out of range (%lld)", fn, (long long)R);
+  AQ_REQUIRE(K > 0 && K < kGemmDimLimit && K % 8 == 0, "%s: K must be a positive multiple of 8 below 2^22 (got %lld)", fn,
+             (long long)K);
+  AQ_REQUIRE(T * K < (int64_t(1) << 36) && T * top < (int64_t(1) << 31), "%s: T * K must be below 2^36", fn);
+  AQ_PTR(Y, 16, "Y");
+  AQ_PTR(slots, 4, "slots");
+  return AQ_OK;
+}
+
+aq_status aq_moe_combine(const void* Y, int32_t y_dtype, int64_t R, int64_t K, const int32_t* slots, const float* weights,
+                         int64_t T, int64_t top, void* out, int32_t out_dtype, void* stream) {
+  const char* fn = "aq_moe_combine";
+  const aq_status st = check_combine(fn, Y, y_dtype, R, K, slots, T, top, out_dtype);
+  if (st != AQ_OK) return st;
+  AQ_PTR(weights, 4, "weights");
+  AQ_PTR(out, 16, "out");
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (T == 0) return ok();
+  return runtime_status(aq::launch_moe_combine(Y, y_dtype == AQ_BF16, R, K, slots, weights, T, (int)top, out,
+                                               out_dtype == AQ_BF16, (hipStream_t)stream),
+                        fn);
+}
+
+aq_status aq_moe_combine_backward(const void* Y, int32_t y_dtype, int64_t R, int64_t K, const int32_t* slots, int64_t T,
+                                  int64_t top, const void* dout, int32_t dout_dtype, float* dweights, void* stream) {
+  const char* fn = "aq_moe_combine_backward";
+  const aq_status st = check_combine(fn, Y, y_dtype, R, K, slots, T, top, dout_dtype);
+  if (st != AQ_OK) return st;
+  AQ_PTR(dout, 16, "dout");
+  AQ_PTR(dweights, 4, "dweights");
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (T == 0) return ok();
+  return runtime_status(aq::launch_moe_combine_backward(Y, y_dtype == AQ_BF16, R, K, slots, T, (int)top, dout,
+                                                        dout_dtype == AQ_BF16, dweights, (hipStream_t)stream),
+                        fn);
+}
+
 }  // extern "C"

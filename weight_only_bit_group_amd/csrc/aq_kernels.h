@@ -85,6 +85,33 @@ hipError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int6
 hipError_t launch_fp8_gemm(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
                            int N, const int32_t* offsets, const int32_t* rows, int M, void* Y, bool y_bf16,
                            hipStream_t stream);
+// Routing: T tokens, rows of logits ld elements apart
+struct RouteArgs {
+  const void* logits;
+  const float* bias;   // [E] or NULL
+  int64_t T, ld;
+  int E, top;
+  int groups, top_groups;
+  int lanes;           // of a wave for each group (set by the launch)
+  bool sigmoid, renormalize;
+  float scale;
+  int32_t* ids;        // [T, top]
+  float* weights;      // [T, top]
+};
+hipError_t launch_moe_route(RouteArgs a, bool l_bf16, hipStream_t stream);
+// dlogits [T, E] in the logits' type
+hipError_t launch_moe_route_backward(const RouteArgs& a, bool l_bf16, const float* grad, void* dlogits, hipStream_t stream);
+// C choices of experts 0 .. E - 1 (others: none) sorted by expert; work: moe_group_workspace_bytes of device memory
+size_t moe_group_workspace_bytes(int64_t C, int E);
+hipError_t launch_moe_group(const int32_t* ids, int64_t C, int top, int E, int32_t* offsets, int32_t* rows, int32_t* slots,
+                            uint32_t* work, hipStream_t stream);
+// rows [gate | up] of 2 I values -> FP8 rows of I; end NULL or the device's count of rows that matter
+hipError_t launch_fp8_swiglu_quantize(const void* H, bool h_bf16, int64_t M, int I, const int32_t* end, uint8_t* codes,
+                                      float* scales, hipStream_t stream);
+hipError_t launch_moe_combine(const void* Y, bool y_bf16, int64_t R, int64_t K, const int32_t* slots, const float* weights,
+                              int64_t T, int top, void* out, bool out_bf16, hipStream_t stream);
+hipError_t launch_moe_combine_backward(const void* Y, bool y_bf16, int64_t R, int64_t K, const int32_t* slots, int64_t T,
+                                       int top, const void* dout, bool dout_bf16, float* dweights, hipStream_t stream);
 // compute units of the current device (cached per device)
 int device_cu_count();
 int64_t sumsq_gemm_blocks(int64_t M, int64_t N);

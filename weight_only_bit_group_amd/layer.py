@@ -28,6 +28,9 @@ this module only arranges tensors and swaps modules.
   * ``MXFP4Linear`` and ``MXFP4Experts``: weights in MXFP4 blocks of 32, the
     activations kept in bf16 or quantized to MXFP4 on the way in; the experts of
     a mixture run as two products grouped by expert.
+  * ``FP8Linear`` and ``FP8Experts``: weights in FP8 (E4M3) blocks of 128 x 128, the activations rounded to FP8 blocks
+    of 128 on the way in; ``route``: a router's logits to the choices and weights that the experts take,
+    differentiable.
 """
 from __future__ import annotations
 
@@ -113,7 +116,7 @@ class W4A16Linear(torch.nn.Module):
 
 
 def _weight_of(linear) -> torch.Tensor:
-    if isinstance(linear, (W4A16Linear, MXFP4Linear)):
+    if isinstance(linear, (W4A16Linear, MXFP4Linear, FP8Linear)):
         raise ValueError("layer is already quantized")
     if not isinstance(linear, torch.nn.Linear):
         raise TypeError(f"expected torch.nn.Linear, got {type(linear).__name__}")
@@ -386,6 +389,194 @@ class MXFP4Experts(torch.nn.Module):
         return f"experts={self.num_experts}, features={self.features}, inner={self.inner}, weights=mxfp4, act={self.act}"
 
 
+def _f8_pair(codes: torch.Tensor, scales: torch.Tensor, name: str, ndim: int) -> None:
+    """Checks codes [.., N, K] (float8_e4m3fn or uint8) and scales [.., ceil(N / 128), ceil(K / 128)] (float32)."""
+    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or scales.dtype != torch.float32:
+        raise ValueError(f"{name}: codes must be float8_e4m3fn (or uint8) and scales float32")
+    if codes.dim() != ndim or codes.shape[-1] == 0 or codes.shape[-1] % 16 \
+            or tuple(scales.shape) != (*codes.shape[:-2], -(-codes.shape[-2] // 128), -(-codes.shape[-1] // 128)):
+        raise ValueError(f"{name}: codes [.., N, K] and scales [.., ceil(N / 128), ceil(K / 128)] expected "
+                         f"(got {list(codes.shape)} and {list(scales.shape)})")
+
+
+def _f8_out(out_dtype) -> torch.dtype:
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
+    return out_dtype
+
+
+def _f8_rows(x: torch.Tensor, k: int) -> torch.Tensor:
+    x2 = _mx_rows(x, k)
+    return x2 if x2.dtype in (torch.bfloat16, torch.float32) else x2.float()
+
+
+class FP8Linear(torch.nn.Module):
+    """y = x W^T (+ bias) with W in FP8 (codes [N, K], scales [ceil(N / 128), ceil(K / 128)]).
+
+    The input is rounded row by row to FP8 blocks of 128.  The output is out_dtype: float32 with sums in fp32
+    throughout, or bfloat16 on the FP8 matrix instructions, twice as fast for many rows.  There is no backward pass: an
+    input that requires a gradient gets its output, and an error when the gradient is asked for.
+    """
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None,
+                 out_dtype: torch.dtype = torch.float32):
+        super().__init__()
+        _f8_pair(codes, scales, "FP8Linear", 2)
+        self.out_dtype = _f8_out(out_dtype)
+        self.out_features, self.in_features = codes.shape
+        self.register_buffer("codes", codes.contiguous())
+        self.register_buffer("scales", scales.contiguous())
+        self.register_buffer("bias", None if bias is None else bias.detach().float().contiguous())
+
+    @classmethod
+    def from_weight(cls, weight: torch.Tensor, bias: torch.Tensor | None = None,
+                    out_dtype: torch.dtype = torch.float32) -> "FP8Linear":
+        """Quantize W [N, K] (fp32 or bf16, on the GPU; K a multiple of 16)."""
+        _f8_out(out_dtype)
+        return cls(*B.aq_fp8_quantize(weight.detach().contiguous(), 128), bias, out_dtype)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        y = _forward_only("FP8Linear", lambda x2: B.aq_fp8_linear(x2, self.codes, self.scales, self.out_dtype),
+                          _f8_rows(x, self.in_features))
+        if self.bias is not None:
+            y += self.bias
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+    def extra_repr(self) -> str:
+        return f"in_features={self.in_features}, out_features={self.out_features}, weights=fp8"
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top, bias, how):
+        ids, weights = B.aq_moe_route(logits, top, bias=bias, **how)
+        ctx.save_for_backward(logits, ids, weights)
+        ctx.how = {k: how[k] for k in ("score", "renormalize", "scale")}
+        ctx.mark_non_differentiable(ids)
+        return ids, weights
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, dweights):
+        logits, ids, weights = ctx.saved_tensors
+        return B.aq_moe_route_backward(logits, ids, weights, dweights.float().contiguous(), **ctx.how), None, None, None
+
+
+def route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, score: str = "softmax", groups: int = 1,
+          top_groups: int | None = None, renormalize: bool = True, scale: float = 1.0):
+    """(ids [.., top] int32, weights [.., top] float32) of a router's logits [.., E], as FP8Experts and MXFP4Experts take
+    them; see ``binding.aq_moe_route`` for the arguments.  weights are differentiable with respect to the logits, the
+    choice is not, and the bias (which only balances the choice) gets no gradient."""
+    lead, e = logits.shape[:-1], logits.shape[-1]
+    l2 = logits.reshape(-1, e)
+    if l2.dtype not in (torch.float32, torch.bfloat16):
+        l2 = l2.float()
+    if l2.shape[0] > 1 and (l2.stride(1) != 1 or l2.stride(0) < e):
+        l2 = l2.contiguous()
+    bias = None if bias is None else bias.detach().float().contiguous()
+    how = dict(score=score, groups=groups, top_groups=top_groups, renormalize=renormalize, scale=scale)
+    if torch.is_grad_enabled() and l2.requires_grad:
+        ids, weights = _Route.apply(l2, top, bias, how)
+    else:
+        ids, weights = B.aq_moe_route(l2, top, bias=bias, **how)
+    return ids.view(*lead, top), weights.view(*lead, top)
+
+
+class _Combine(torch.autograd.Function):
+    """The weighted sum over a token's choices, differentiable in the weights."""
+
+    @staticmethod
+    def forward(ctx, name, y, slots, weights, out_dtype):
+        ctx.name = name
+        ctx.save_for_backward(y, slots)
+        return B.aq_moe_combine(y, slots, weights, out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        if ctx.needs_input_grad[1]:
+            _NoBackward.backward(ctx, grad)
+        y, slots = ctx.saved_tensors
+        if grad.dtype not in (torch.float32, torch.bfloat16):
+            grad = grad.float()
+        return None, None, None, B.aq_moe_combine_backward(y, slots, grad.contiguous()), None
+
+
+class FP8Experts(torch.nn.Module):
+    """The experts of a mixture, gated MLPs with FP8 weights:
+
+        y[t] = sum_j w[t, j] D_e Q(silu(G_e Q(x[t])) * U_e Q(x[t])),   e = ids[t, j]
+
+    with Q the rounding to FP8 blocks of 128.  gate_up holds [G_e; U_e] as codes [E, 2I, K] and scales
+    [E, ceil(2I / 128), ceil(K / 128)], down D_e as codes [E, K, I] and scales [E, ceil(K / 128), ceil(I / 128)]; E is at
+    most 1024.  ``forward(x, ids, weights)`` takes x [.., K] with the router's choices ids [.., top] (any integer
+    type) and weights [.., top], as ``route`` gives them; a choice outside 0 .. E - 1 (the filling of a padded batch, an
+    expert of another rank) adds nothing.  Both layers run as one product grouped by expert each, without reading a
+    count back to the host, so a call may be captured into a graph whose replays follow x, ids and weights.  A token's
+    products are added in the order of its choices, in fp32.  The output is out_dtype; with bfloat16 the products of
+    a choice are rounded to bfloat16 before they are added.  weights are differentiable, the experts are not: an error
+    when x's gradient is asked for.
+    """
+
+    def __init__(self, gate_up_codes: torch.Tensor, gate_up_scales: torch.Tensor, down_codes: torch.Tensor,
+                 down_scales: torch.Tensor, out_dtype: torch.dtype = torch.float32):
+        super().__init__()
+        _f8_pair(gate_up_codes, gate_up_scales, "gate_up", 3)
+        _f8_pair(down_codes, down_scales, "down", 3)
+        self.out_dtype = _f8_out(out_dtype)
+        self.num_experts, rows, self.features = gate_up_codes.shape
+        self.inner = down_codes.shape[2]
+        if rows != 2 * self.inner or tuple(down_codes.shape[:2]) != (self.num_experts, self.features):
+            raise ValueError(f"gate_up [E, 2I, K] and down [E, K, I] expected, codes are {list(gate_up_codes.shape)} "
+                             f"and {list(down_codes.shape)}")
+        if not 0 < self.num_experts <= 1024:
+            raise ValueError(f"1 to 1024 experts expected (got {self.num_experts})")
+        self.register_buffer("gate_up_codes", gate_up_codes.contiguous())
+        self.register_buffer("gate_up_scales", gate_up_scales.contiguous())
+        self.register_buffer("down_codes", down_codes.contiguous())
+        self.register_buffer("down_scales", down_scales.contiguous())
+
+    @classmethod
+    def from_weights(cls, gate_up: torch.Tensor, down: torch.Tensor, out_dtype: torch.dtype = torch.float32) -> "FP8Experts":
+        """Quantize gate_up [E, 2I, K] and down [E, K, I] (fp32 or bf16, on the GPU)."""
+        _f8_out(out_dtype)
+        for w, name in ((gate_up, "gate_up"), (down, "down")):
+            if w.dim() != 3:
+                raise ValueError(f"{name} must have 3 dimensions")
+        return cls(*B.aq_fp8_quantize(gate_up.detach().contiguous(), 128), *B.aq_fp8_quantize(down.detach().contiguous(), 128),
+                   out_dtype)
+
+    def forward(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor) -> torch.Tensor:
+        x2 = _f8_rows(x, self.features)
+        if ids.shape != weights.shape or ids.shape[:-1] != x.shape[:-1] or ids.dim() < 1 or ids.shape[-1] == 0:
+            raise ValueError(f"ids and weights must be {[*x.shape[:-1], 'top']} (got {list(ids.shape)} and "
+                             f"{list(weights.shape)})")
+        if ids.is_floating_point() or ids.is_complex() or ids.dtype == torch.bool:
+            raise ValueError(f"ids must be integers (got {ids.dtype})")
+        top = ids.shape[-1]
+        if ids.dtype != torch.int32:   # (numbers that 32 bits do not hold are outside the experts too)
+            ids = ids.long().clamp(-1, self.num_experts).int()
+        offsets, rows, slots = B.aq_moe_group(ids.reshape(-1, top).contiguous(), self.num_experts)
+
+        def experts(x2):
+            if rows.shape[0] == 0:
+                return x2.new_empty(0, self.features, dtype=self.out_dtype)
+            h = B.aq_fp8_grouped_gemm(*B.aq_fp8_quantize(x2), self.gate_up_codes, self.gate_up_scales, offsets, rows)
+            h = B.aq_fp8_swiglu_quantize(h, offsets[-1:])
+            return B.aq_fp8_grouped_gemm(*h, self.down_codes, self.down_scales, offsets, out_dtype=self.out_dtype)
+
+        y = _forward_only("FP8Experts", experts, x2)
+        w = weights.reshape(-1, top).float().contiguous()
+        if torch.is_grad_enabled() and (w.requires_grad or y.requires_grad):
+            out = _Combine.apply("FP8Experts", y, slots, w, self.out_dtype)
+        else:
+            out = B.aq_moe_combine(y, slots, w, self.out_dtype)
+        return out.reshape(*x.shape[:-1], self.features)
+
+    def extra_repr(self) -> str:
+        return f"experts={self.num_experts}, features={self.features}, inner={self.inner}, weights=fp8"
+
+
 @dataclass(frozen=True)
 class LayerQuantPolicy:
     """Per-layer override of the base configuration; None fields inherit it."""
@@ -410,7 +601,7 @@ def plan_quantization(model: torch.nn.Module, target_modules, bits: int = 4, gro
     symmetric, 8-bit asymmetric).
     """
     named = dict(model.named_modules())
-    quantized = [n for n, m in named.items() if isinstance(m, (W4A16Linear, W8A16Linear, MXFP4Linear))]
+    quantized = [n for n, m in named.items() if isinstance(m, (W4A16Linear, W8A16Linear, MXFP4Linear, FP8Linear))]
     linears = [n for n, m in named.items() if isinstance(m, torch.nn.Linear)]
     if not linears and not quantized:
         raise ValueError("the model contains no torch.nn.Linear")

@@ -85,6 +85,10 @@ hipError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int6
 hipError_t launch_fp8_gemm(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
                            int N, const int32_t* offsets, const int32_t* rows, int M, void* Y, bool y_bf16,
                            hipStream_t stream);
+// The kernel form that such a product takes on a device of `cus` compute units (E = 1: dense), and a form's
+// description (negative past the last): the tests hold that every form is run.
+extern "C" int fp8_form(bool y_bf16, bool grouped, int M, int K, int N, int E, int cus);
+extern "C" int fp8_form_name(bool y_bf16, int form, char* to, size_t n);
 // Routing: T tokens, rows of logits ld elements apart
 struct RouteArgs {
   const void* logits;

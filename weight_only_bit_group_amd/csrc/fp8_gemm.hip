@@ -113,6 +113,184 @@ __device__ __forceinline__ void store_columns(const F8Args& a, int r, int col, c
   }
 }
 
+// ---- few rows -------------------------------------------------------------------------------
+// Bound by the weight bytes.  A block's NW waves share K: each takes every NW-th stage (one block of 128 k) of the
+// (16 FM) x (16 FN) tile through LDS buffers of its own, filled by its own LDS-DMA, so there is no barrier before the
+// sums are joined, in wave order: a wave only waits for its own oldest loads, with R stages in flight.  (Straight to
+// registers, in the order that the instructions take, neighbouring lanes read 16 bytes of different rows: four times
+// the requests, 23 us against 13 for 16 rows on [4096, 14336].)
+//   Activation rows past the tile's are not fetched: their LDS bytes are whatever was there, in columns of the result
+// that are not stored.
+template <int FM_, int FN_, int NW_, int R_>
+struct F8Split {
+  static constexpr int FM = FM_, FN = FN_, NW = NW_, R = R_;
+  static constexpr int BM = 16 * FM, BN = 16 * FN, NT = 64 * NW;
+  static constexpr bool SPLIT = true;
+  static constexpr int DMA = 2 * FM + 2 * FN + 1;               // loads of a stage
+  static constexpr int STAGE = 2048 * (FM + FN) + 256;          // its LDS bytes: activations, weights, scales
+  static constexpr int PART = FM * FN * 1024;                   // bytes of a wave's sums
+  static constexpr int LDS = NW * (R * STAGE > PART ? R * STAGE : PART);
+  static constexpr int PER_CU = std::max(1, std::min(160 * 1024 / LDS, 32 / NW));   // blocks that a compute unit holds
+  static int describe(char* to, size_t n) { return snprintf(to, n, "split %d x %d over %d", FM, FN, NW); }
+  static_assert(FM <= 4 && 128 % BN == 0, "one load of scales, one weight scale a stage");
+  static_assert((R - 1) * DMA < 64 && LDS <= 160 * 1024, "loads in flight are counted in six bits");
+};
+
+template <class C, bool GROUPED, bool BF16>
+__global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
+  using Op = Operand<!BF16>;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int tiles_n = (a.N + C::BN - 1) / C::BN;
+  Tile t;
+  if constexpr (GROUPED) {
+    if (!grouped_tile<C::BM>(a, tiles_n, C::BN, blockIdx.x, t)) return;   // the whole block
+  } else {
+    // the row tiles of a column run side by side: they share its weights in the L2
+    const int tiles_m = (a.M + C::BM - 1) / C::BM;
+    const int i = tile_of_block(blockIdx.x, tiles_m * tiles_n);
+    t.e = 0;
+    t.r0 = (i % tiles_m) * C::BM;
+    t.r1 = min(t.r0 + C::BM, a.M);
+    t.n0 = (i / tiles_m) * C::BN;
+  }
+  const int count = (a.nkb - wid + C::NW - 1) / C::NW;   // this wave's stages: wid, wid + NW, ..
+  uint8_t* mine = lds + wid * C::R * C::STAGE;
+  auto xrow = [&](int i) -> int64_t {
+    const int r = min(t.r0 + i, t.r1 - 1);
+    return GROUPED ? max(source_row(a, r), 0) : r;
+  };
+  // LDS row 16 j + 4 g' + v of the weights is row 4 FN g' + 4 j + v of the tile
+  auto wrow = [&](int i) { return min(4 * C::FN * ((i & 15) >> 2) + 4 * (i >> 4) + (i & 3), a.N - 1 - t.n0); };
+  // load j covers rows 8 j .. 8 j + 7; the permutation's period is 16 rows
+  const int unit = swizzle(lane >> 3, lane & 7);
+  const uint8_t* wtile = a.W + ((int64_t)t.e * a.N + t.n0) * a.K;
+  uint32_t xsrc[2 * C::FM], wsrc[2 * C::FN];   // units from X (X is below 2^36 bytes), bytes from wtile
+#pragma unroll
+  for (int j = 0; j < 2 * C::FM; ++j) xsrc[j] = (uint32_t)((xrow(8 * j + (lane >> 3)) * a.K) >> 4) + (unit ^ (4 * (j & 1)));
+#pragma unroll
+  for (int j = 0; j < 2 * C::FN; ++j)
+    wsrc[j] = (uint32_t)wrow(8 * j + (lane >> 3)) * (uint32_t)a.K + 16u * (unit ^ (4 * (j & 1)));
+  const float* ssrc = a.XS + xrow(lane % C::BM) * a.nkb;
+  const int last = a.nkb - 1, left = (a.K - last * 128) >> 4;   // units of the last block; those past it: its last one
+  const int rows = t.r1 - t.r0;
+  auto issue = [&](int i, int slot) {
+    const int s = wid + i * C::NW;
+    const uint8_t* x = a.X + (int64_t)s * 128;
+    const uint8_t* w = uniform(wtile + (int64_t)s * 128);
+    const uint32_t base = lds_addr(mine + slot * C::STAGE);
+    const bool tail = s == last;
+#pragma unroll
+    for (int j = 0; j < 2 * C::FM; ++j) {
+      const int back = tail ? max((unit ^ (4 * (j & 1))) - left + 1, 0) : 0;
+      // (eight lanes at least, so that the load is counted)
+      if (lane < 8 || 8 * j + (lane >> 3) < rows)
+        dma16_at(x + 16 * (uint64_t)(xsrc[j] - back), __builtin_amdgcn_readfirstlane(base + 1024 * j));
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * C::FN; ++j) {
+      const int back = tail ? max((unit ^ (4 * (j & 1))) - left + 1, 0) : 0;
+      dma16_from(w, wsrc[j] - 16 * back, __builtin_amdgcn_readfirstlane(base + 1024 * (2 * C::FM + j)));
+    }
+    dma4_at(ssrc + s, __builtin_amdgcn_readfirstlane(base + 2048 * (C::FM + C::FN)));
+  };
+  f32x4 acc[C::FM][C::FN];
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const float* wscale = a.WS + ((int64_t)t.e * a.nnb + (t.n0 >> 7)) * a.nkb;
+  float scales = 0.0f;   // lane l: the weights' scale of the wave's stage i0 + l
+#pragma unroll
+  for (int i = 0; i < C::R; ++i)
+    if (i < count) issue(i, i);
+  for (int i0 = 0; i0 < count; i0 += 64) {
+    scales = wscale[min(wid + (i0 + lane) * C::NW, last)];
+    const int stop = min(i0 + 64, count);
+    for (int n = i0; n < stop; ++n) {
+      const int s = wid + n * C::NW, slot = n % C::R;
+      if (n + C::R < count) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((C::R - 1) * C::DMA) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      const uint8_t* xt = mine + slot * C::STAGE;
+      const uint8_t* wt = xt + 2048 * C::FM;
+      const float* st = reinterpret_cast<const float*>(xt + 2048 * (C::FM + C::FN));
+      auto half = [](const uint8_t* tile, int r, int u) {
+        return *reinterpret_cast<const u32x4*>(tile + 128 * r + 16 * swizzle(r, u));
+      };
+      u32x4 x[C::FM][2], w[C::FN][2];
+      float f[C::FM];
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        x[i][0] = half(xt, 16 * i + l16, g);
+        x[i][1] = half(xt, 16 * i + l16, 4 + g);
+        f[i] = st[16 * i + l16];
+      }
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        w[j][0] = half(wt, 16 * j + l16, g);
+        w[j][1] = half(wt, 16 * j + l16, 4 + g);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (n + C::R < count) issue(n + C::R, slot);
+      // units past K are zero; by a mask: the compiler loses the wait between a matrix instruction and its result's
+      // reader where a branch comes between them
+      const uint32_t keep0 = s == last && g >= left ? 0u : ~0u, keep1 = s == last && 4 + g >= left ? 0u : ~0u;
+      const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scales), n - i0));
+      Op wo[C::FN];
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) wo[j] = Op(w[j][0], w[j][1]);
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        const Op xo(x[i][0] & keep0, x[i][1] & keep1);
+        const float by = f[i] * sw;
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+          const f32x4 p = block_sum(wo[j], xo);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[v], by, acc[i][j][v]);
+        }
+      }
+    }
+  }
+
+  auto store = [&](int i, const f32x4 (&v)[C::FN]) {
+    const int r = t.r0 + 16 * i + l16;
+    if (r >= t.r1) return;
+    const bool lost = GROUPED && source_row(a, r) < 0;
+    float o[4 * C::FN];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[4 * j + c] = lost ? __builtin_nanf("") : v[j][c];
+    store_columns<BF16, 4 * C::FN>(a, r, t.n0 + 4 * C::FN * g, o);
+  };
+  if constexpr (C::NW == 1) {
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) store(i, acc[i]);
+  } else {
+    f32x4* sums = reinterpret_cast<f32x4*>(lds);
+    __syncthreads();   // (every wave has read its last stage)
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) sums[((wid * C::FM + i) * C::FN + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    for (int i = wid; i < C::FM; i += C::NW) {
+      f32x4 v[C::FN];
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) v[j] = sums[(i * C::FN + j) * 64 + lane];
+#pragma unroll
+      for (int k = 1; k < C::NW; ++k)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) v[j] += sums[((k * C::FM + i) * C::FN + j) * 64 + lane];
+      store(i, v);
+    }
+  }
+}
+
 // ---- tiles ----------------------------------------------------------------------------------
 // WM x WN waves, each (16 FM) activation rows x (16 FN) weight rows.  K advances in stages of one block, 128 bytes of
 // a row, through two LDS buffers filled by LDS-DMA.
@@ -123,8 +301,14 @@ struct F8Cfg {
   static constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
   static constexpr int A_DMA = BM / 8 / NW;   // loads per wave and stage, 1 KiB each
   static constexpr int B_DMA = BN / 8 / NW;
-  static constexpr int S_DMA = (BM + 63) / 64;   // loads of the activations' scales per stage, one a wave
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && S_DMA <= NW && 128 % (16 * FN) == 0, "whole loads per wave");
+  static constexpr bool SPLIT = false;
+  static constexpr int S_ROWS = BM / NW;      // rows whose scales a wave loads per stage, by one load of a dword a lane
+  static constexpr int LDS = 2 * 128 * (BM + BN) + 512 * NW;
+  // blocks that a compute unit holds; their registers leave room for 8 waves, or 12
+  static constexpr int PER_CU = std::max(1, std::min(160 * 1024 / LDS, (FM * FN >= 16 ? 8 : 12) / NW));
+  static int describe(char* to, size_t n) { return snprintf(to, n, "tile %d x %d of %d x %d", WM, WN, FM, FN); }
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && 128 % (16 * FN) == 0, "whole loads per wave");
+  static_assert(S_ROWS % 16 == 0 && S_ROWS <= 64, "the scales of 16 rows lie together");
 };
 
 template <class C, bool GROUPED, bool BF16>
@@ -132,7 +316,7 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
   using Op = Operand<!BF16>;
   __shared__ __attribute__((aligned(1024))) uint8_t Xs[2][C::BM * 128];
   __shared__ __attribute__((aligned(1024))) uint8_t Ws[2][C::BN * 128];
-  __shared__ __attribute__((aligned(256))) float Ss[2][C::S_DMA * 64];
+  __shared__ __attribute__((aligned(256))) float Ss[2][C::NW * 64];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -143,11 +327,11 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
   if constexpr (GROUPED) {
     if (!grouped_tile<C::BM>(a, tiles_n, C::BN, blockIdx.x, t)) return;   // the whole block
   } else {
-    // groups of row tiles walked column by column, so the tiles that an XCD runs together
-    // share their rows and columns in its L2
+    // groups of four row tiles walked column by column: the 32 tiles that an XCD runs together are four rows of
+    // eight (an eighth of the row tiles, two rows of 16, costs 3% at 4096 rows)
     const int tiles_m = (a.M + C::BM - 1) / C::BM;
     const int i = tile_of_block(blockIdx.x, tiles_m * tiles_n);
-    const int gmax = max(1, (tiles_m + 7) / 8);
+    const int gmax = min(tiles_m, 4);
     const int grp = i / (gmax * tiles_n);
     const int gm = min(tiles_m - grp * gmax, gmax);
     const int within = i - grp * gmax * tiles_n;
@@ -176,7 +360,7 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
     xsrc[j] = (uint32_t)((xrow(8 * (j * C::NW + wid) + (lane >> 3)) * a.K) >> 4) + unit;
 #pragma unroll
   for (int j = 0; j < C::B_DMA; ++j) wsrc[j] = (uint32_t)wrow(8 * (j * C::NW + wid) + (lane >> 3)) * (uint32_t)a.K + 16u * unit;
-  const float* ssrc = a.XS + xrow(min(64 * wid + lane, C::BM - 1)) * a.nkb;
+  const float* ssrc = a.XS + xrow(C::S_ROWS * wid + lane % C::S_ROWS) * a.nkb;
   const int left = (a.K - last * 128) >> 4;   // units of the last block
   const uint32_t back = max(unit - left + 1, 0);
   auto issue = [&](int s, int buf) {
@@ -188,11 +372,12 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
       dma16_at(x + 16 * (uint64_t)(xsrc[j] - b), lds_addr(&Xs[buf][1024 * (C::NW * j + wid)]));
 #pragma unroll
     for (int j = 0; j < C::B_DMA; ++j) dma16_from(w, wsrc[j] - 16 * b, lds_addr(&Ws[buf][1024 * (C::NW * j + wid)]));
-    if (wid < C::S_DMA) dma4_at(ssrc + s, lds_addr(&Ss[buf][64 * wid]));
+    dma4_at(ssrc + s, lds_addr(&Ss[buf][64 * wid]));
   };
-  // (uniform over the wave: the constant address space makes it a scalar load)
+  // (uniform over the wave: the constant address space makes it a scalar load; a wave whose columns are all past N reads
+  // the last block's)
   const auto* wscale = (const __attribute__((address_space(4))) float*)(uint64_t)uniform(reinterpret_cast<const uint8_t*>(
-      a.WS + ((int64_t)t.e * a.nnb + ((t.n0 + wn * 16 * C::FN) >> 7)) * a.nkb));
+      a.WS + ((int64_t)t.e * a.nnb + min((t.n0 + wn * 16 * C::FN) >> 7, a.nnb - 1)) * a.nkb));
 
   f32x4 acc[C::FM][C::FN];
 #pragma unroll
@@ -202,60 +387,80 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
 
   // units g and 4 + g of this lane's first operand rows; the rows of the next operand, 16 further, are permuted alike
   const int xat = 128 * (wm * 16 * C::FM + l16) + 16 * swizzle(l16, g), wat = 128 * (wn * 16 * C::FN + l16) + 16 * swizzle(l16, g);
-  auto half = [](const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); };
-  // One stage.  Row block i's operand is read while the products of the one before run, and a block's results are
-  // added one row block later, when they have left the matrix core.  The last stage, which may be part-filled, is
-  // compiled apart, so that the others have no branch; it requests nothing.
+  // Operands are read ahead: row block i + 1's activations while the products of row block i run, the next stage's
+  // weights into the registers that the last row block's products have just used.  Before those comes the hand-over:
+  // by then every wave has its last operands of the stage, so its buffer is free for the stage after next.  A result
+  // is added when its registers are needed again, FN products later, when it has left the matrix core; the order of
+  // additions and products is fixed, or the compiler gathers the products and waits for their results.  No stage but
+  // the last, which may be part-filled, has a branch: near the end the last stage is requested again, into a buffer
+  // that is not read.
+  static_assert(C::FM % 2 == 0, "row blocks alternate between two sets of registers");
+  u32x4 wr[C::FN][2], xr[2][2];
+  f32x4 p[C::FN];
+  float fr[2], sw, swnext, before = 0.0f;
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto load_w = [&](const uint8_t* tile, int j) {
+    wr[j][0] = *reinterpret_cast<const u32x4*>(tile + wat + 2048 * j);
+    wr[j][1] = *reinterpret_cast<const u32x4*>(tile + (wat ^ 64) + 2048 * j);
+  };
+  auto load_x = [&](int buf, int i) {
+    xr[i & 1][0] = *reinterpret_cast<const u32x4*>(&Xs[buf][xat + 2048 * i]);
+    xr[i & 1][1] = *reinterpret_cast<const u32x4*>(&Xs[buf][(xat ^ 64) + 2048 * i]);
+    // (row r's is the r % S_ROWS-th of wave r / S_ROWS)
+    const int r = wm * 16 * C::FM + 16 * i;
+    fr[i & 1] = Ss[buf][64 * (r / C::S_ROWS) + r % C::S_ROWS + l16];
+  };
+  auto add = [&](int i, int j) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[j][v], before, acc[i][j][v]);
+  };
   auto stage = [&](int s, auto last_) {
     constexpr bool LAST = decltype(last_)::value;
     const int buf = s & 1;
-    if constexpr (!LAST) issue(s + 1, buf ^ 1);
-    const float sw = wscale[s];
-    const uint8_t *wlo = &Ws[buf][wat], *whi = &Ws[buf][wat ^ 64], *xlo = &Xs[buf][xat], *xhi = &Xs[buf][xat ^ 64];
-    const float* sx = &Ss[buf][wm * 16 * C::FM + l16];
+    const uint32_t keep0 = LAST && g >= left ? 0u : ~0u, keep1 = LAST && 4 + g >= left ? 0u : ~0u;
     Op w[C::FN];
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) w[j] = Op(half(wlo + 2048 * j), half(whi + 2048 * j));
-    u32x4 x[2][2];
-    f32x4 p[2][C::FN];
-    float f[2];
-    auto load_x = [&](int i) {
-      x[i & 1][0] = half(xlo + 2048 * i);
-      x[i & 1][1] = half(xhi + 2048 * i);
-      f[i & 1] = sx[16 * i] * sw;
-      if constexpr (LAST) {
-        if (g >= left) x[i & 1][0] = u32x4{0, 0, 0, 0};
-        if (4 + g >= left) x[i & 1][1] = u32x4{0, 0, 0, 0};
-      }
-    };
-    auto add = [&](int i, float by) {
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[i & 1][j][v], by, acc[i][j][v]);
-    };
-    load_x(0);
-    float before = 0.0f;
+    for (int j = 0; j < C::FN; ++j) w[j] = Op(wr[j][0], wr[j][1]);
+    const float by = sw;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
-      const float now = f[i & 1];
-      const Op xi(x[i & 1][0], x[i & 1][1]);
-      if (i + 1 < C::FM) load_x(i + 1);
+      const bool hand = !LAST && i + 1 == C::FM;
+      if (hand) {
+        drain_barrier();
+        swnext = wscale[s + 1];
+      }
+      const Op x = LAST ? Op(xr[i & 1][0] & keep0, xr[i & 1][1] & keep1) : Op(xr[i & 1][0], xr[i & 1][1]);
+      const float f = fr[i & 1] * by;
+      if (hand) load_x(buf ^ 1, 0);
+      else if (i + 1 < C::FM) load_x(buf, i + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) p[i & 1][j] = block_sum(w[j], xi);
-      if (i > 0) add(i - 1, before);
-      before = now;
+      for (int j = 0; j < C::FN; ++j) {
+        add((i + C::FM - 1) % C::FM, j);
+        p[j] = block_sum(w[j], x);
+        if (hand) load_w(&Ws[buf ^ 1][0], j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (hand) issue(min(s + 2, last), buf);
+      before = f;
       __builtin_amdgcn_sched_barrier(0);
     }
-    add(C::FM - 1, before);
+    if (!LAST) sw = swnext;
   };
   issue(0, 0);
   drain_barrier();
-  for (int s = 0; s < last; ++s) {
-    stage(s, std::false_type{});
-    drain_barrier();
-  }
+  issue(min(1, last), 1);
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) load_w(&Ws[0][0], j);
+  load_x(0, 0);
+  sw = wscale[0];
+  for (int s = 0; s < last; ++s) stage(s, std::false_type{});
   stage(last, std::true_type{});
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) add(C::FM - 1, j);
+  // no load may land in LDS that the next block owns by then
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
 #pragma unroll
   for (int i = 0; i < C::FM; ++i) {
@@ -281,19 +486,114 @@ template <class C, bool GROUPED, bool BF16>
 hipError_t launch(const F8Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
   const dim3 grid((unsigned)(row_tiles<C, GROUPED>(a) * tiles_n)), block(C::NT);
-  hipLaunchKernelGGL((fp8_tile_kernel<C, GROUPED, BF16>), grid, block, 0, stream, a);
+  if constexpr (C::SPLIT) {
+    const auto kernel = fp8_split_kernel<C, GROUPED, BF16>;
+    if (C::LDS > 64 * 1024) {
+      // the kernel's limit of dynamic LDS, raised once per device (bit d of done)
+      static std::atomic<uint64_t> done{0};
+      int dev = 0;
+      hipError_t e = hipGetDevice(&dev);
+      if (e != hipSuccess) return e;
+      const uint64_t bit = uint64_t(1) << (dev & 63);
+      if (!(done.load(std::memory_order_acquire) & bit)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+        if (e != hipSuccess) return e;
+        done.fetch_or(bit, std::memory_order_acq_rel);
+      }
+    }
+    hipLaunchKernelGGL(kernel, grid, block, C::LDS, stream, a);
+  } else {
+    hipLaunchKernelGGL((fp8_tile_kernel<C, GROUPED, BF16>), grid, block, 0, stream, a);
+  }
   return hipGetLastError();
+}
+
+// The form of a product: the one whose estimated time is the least,
+//   fixed + r (round + stage * stages of a wave) + mb * (MB through LDS-DMA)     [us]
+// with r = the tiles over those that the device holds at once, at least 1: a block takes its run of stages whether or
+// not others run beside it, and every tile adds its traffic.  The four figures of a form are least-squares fits of the
+// relative error, its best cases weighted most, to graph-replayed times of 193 products (M = 1 to 4096 on weights of
+// 512 to 14336 rows and columns, drawn ones of M to 4096, N to 14336 and K to 14336, to 128 experts with 1 to 32768
+// rows) of 14 forms.  The forms kept lose 1% of geometric-mean time against the best of all, the estimates' choice of
+// them 3% (bf16 out) and 5% (fp32 out), 1.4 times at worst.  Both sides, graph-replayed, us:
+//   M = 1 on [11008, 2048], fp32 out: 16 x 64 over 8 waves 7.2, 16 x 16 over 4 waves 8.6, tiles of 64 x 128 16.3
+//   M = 16 on [4096, 14336], fp32 out: 16 x 16 over 16 waves 16.2, 16 x 64 over 8 waves 28.8, tiles of 64 x 128 98.9
+//   M = 128 on [11008, 2048], bf16 out: tiles of 64 x 128 18, of 128 x 128 20, 32 x 64 over 4 waves 22
+//   M = 4096 there: tiles of 256 x 256 136, of 128 x 128 142
+struct F8Cost {
+  float fixed, round, stage, mb;
+};
+
+template <class C, bool GROUPED>
+float estimate(const F8Args& a, F8Cost c, int cus) {
+  const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
+  if (row_tiles<C, GROUPED>(a) * tiles_n >= (int64_t(1) << 32) / C::NT) return INFINITY;   // threads of a launch
+  // grouped: an expert's last tile with half its rows, the lists being on the device
+  const float products = (float)std::min(a.M, a.E);
+  const float tiles = (float)tiles_n * (GROUPED ? std::max(products, (float)a.M / C::BM + 0.5f * products)
+                                                : (float)row_tiles<C, GROUPED>(a));
+  const int mine = C::SPLIT ? (a.nkb + C::NW - 1) / C::NW : a.nkb;
+  const float r = std::max(1.0f, tiles / (float)(cus * C::PER_CU));
+  const float mb = 1e-6f * tiles * (float)(mine * (C::SPLIT ? C::NW : 1)) * 128.0f * (float)(C::BM + C::BN);
+  return c.fixed + r * (c.round + c.stage * (float)mine) + c.mb * mb;
+}
+
+template <class C_>
+struct F8Form {
+  using C = C_;
+  F8Cost cost;
+};
+
+// f(the forms of a product)
+template <bool BF16, class F>
+auto with_forms(F f) {
+  if constexpr (BF16)
+    return f(F8Form<F8Split<1, 1, 16, 1>>{{0.000f, 2.616f, 0.605f, 0.055f}}, F8Form<F8Split<1, 1, 4, 4>>{{0.735f, 2.076f, 0.251f, 0.052f}},
+             F8Form<F8Split<1, 4, 8, 1>>{{0.989f, 2.705f, 0.614f, 0.040f}}, F8Form<F8Split<1, 4, 2, 3>>{{0.931f, 2.521f, 0.461f, 0.060f}},
+             F8Form<F8Split<2, 4, 4, 1>>{{0.281f, 3.417f, 0.656f, 0.050f}}, F8Form<F8Cfg<2, 2, 2, 4>>{{2.990f, 0.875f, 0.490f, 0.070f}},
+             F8Form<F8Cfg<2, 2, 4, 4>>{{1.234f, 3.150f, 0.743f, 0.056f}}, F8Form<F8Cfg<2, 4, 8, 4>>{{0.000f, 9.719f, 1.253f, 0.086f}});
+  else
+    return f(F8Form<F8Split<1, 1, 16, 1>>{{3.012f, 0.000f, 0.562f, 0.047f}}, F8Form<F8Split<1, 1, 4, 4>>{{2.203f, 0.750f, 0.344f, 0.057f}},
+             F8Form<F8Split<1, 4, 8, 1>>{{2.190f, 1.209f, 1.005f, 0.029f}}, F8Form<F8Split<1, 4, 2, 3>>{{2.108f, 1.458f, 0.502f, 0.054f}},
+             F8Form<F8Split<2, 4, 4, 1>>{{0.286f, 3.508f, 0.802f, 0.048f}}, F8Form<F8Cfg<1, 4, 4, 2>>{{0.000f, 4.378f, 0.535f, 0.088f}},
+             F8Form<F8Cfg<2, 2, 4, 4>>{{0.000f, 5.215f, 0.705f, 0.116f}});
+}
+
+// the index of the form that the product takes on a device of `cus` compute units
+template <bool GROUPED, bool BF16>
+int least(const F8Args& a, int cus) {
+  return with_forms<BF16>([&](auto... form) {
+    const float t[] = {estimate<typename decltype(form)::C, GROUPED>(a, form.cost, cus)...};
+    return (int)(std::min_element(std::begin(t), std::end(t)) - std::begin(t));
+  });
 }
 
 template <bool GROUPED, bool BF16>
 hipError_t launch_any(const F8Args& a, hipStream_t stream) {
-  using Large = F8Cfg<2, 4, BF16 ? 8 : 4, 4>;
-  using Small = F8Cfg<2, 2, 2, 4>;
-  const int64_t tiles = row_tiles<Large, GROUPED>(a) * ((a.N + Large::BN - 1) / Large::BN);
-  return tiles >= device_cu_count() ? launch<Large, GROUPED, BF16>(a, stream) : launch<Small, GROUPED, BF16>(a, stream);
+  return with_forms<BF16>([&](auto... form) {
+    using Fn = hipError_t (*)(const F8Args&, hipStream_t);
+    const Fn fn[] = {launch<typename decltype(form)::C, GROUPED, BF16>...};
+    return fn[least<GROUPED, BF16>(a, device_cu_count())](a, stream);
+  });
 }
 
 }  // namespace
+
+int fp8_form(bool y_bf16, bool grouped, int M, int K, int N, int E, int cus) {
+  F8Args a = {};
+  a.M = M, a.N = N, a.K = K, a.E = E, a.nkb = (K + 127) / 128, a.nnb = (N + 127) / 128;
+  return y_bf16 ? grouped ? least<true, true>(a, cus) : least<false, true>(a, cus)
+                : grouped ? least<true, false>(a, cus) : least<false, false>(a, cus);
+}
+
+int fp8_form_name(bool y_bf16, int i, char* to, size_t n) {
+  auto describe = [&](auto... form) {
+    using Fn = int (*)(char*, size_t);
+    const Fn fn[] = {decltype(form)::C::describe...};
+    return i < 0 || i >= (int)std::size(fn) ? -1 : fn[i](to, n);
+  };
+  return y_bf16 ? with_forms<true>(describe) : with_forms<false>(describe);
+}
 
 hipError_t launch_fp8_gemm(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
                            int N, const int32_t* offsets, const int32_t* rows, int M, void* Y, bool y_bf16,

@@ -14,7 +14,8 @@ __all__ = ["aq_quantize_pack", "aq_w4a16_gemv", "aq_w4a16_gemm", "aq_w4a16_gemm_
            "aq_w8a16_gemv", "aq_w8a16_gemm", "aq_w8a16_gemm_workspace", "aq_mxfp4_quantize", "aq_mxfp4_dequantize",
            "aq_mxfp4_gemm", "aq_mxfp4_gemm_a4", "aq_mxfp4_grouped_gemm", "aq_mxfp4_grouped_gemm_a4",
            "aq_fp8_quantize", "aq_fp8_dequantize", "aq_fp8_gemm", "aq_fp8_linear",
-           "aq_fp8_linear_workspace", "aq_fp8_grouped_gemm", "aq_fp8_swiglu_quantize", "aq_moe_route", "aq_moe_route_backward",
+           "aq_fp8_linear_workspace", "aq_fp8_grouped_gemm", "aq_fp8_swiglu_quantize",
+           "aq_fp8_experts", "aq_fp8_experts_workspace", "aq_moe_route", "aq_moe_route_backward",
            "aq_moe_group", "aq_moe_group_workspace", "aq_moe_combine", "aq_moe_combine_backward"]
 
 

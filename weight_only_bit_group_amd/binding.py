@@ -346,7 +346,9 @@ class _MxNative:
     """The module's functions; the first use of one loads the library and the module."""
 
     def __getattr__(self, name):
-        if name not in ("quantize", "dequantize", "gemm", "gemm_a4", "grouped_gemm", "grouped_gemm_a4"):
+        if name not in ("quantize", "dequantize", "gemm", "gemm_a4", "grouped_gemm", "grouped_gemm_a4", "fp8_quantize",
+                        "fp8_dequantize", "fp8_gemm", "fp8_grouped_gemm", "fp8_linear", "fp8_experts", "route",
+                        "route_backward"):
             raise AttributeError(name)
         _lib.load()
         from . import _aq_torch   # an ImportError here: the module has not been built
@@ -544,7 +546,7 @@ def aq_mxfp4_grouped_gemm_a4(X_codes, X_scales, codes, scales, offsets, rows=Non
 
 
 # ---- FP8 (E4M3, a scale for each block of 128) ---------------------------------------------
-# As the MXFP4 calls these run on the device of their tensors.  Codes are float8_e4m3fn; uint8
+# As the MXFP4 calls these run on the device of their tensors, and the common call through _aq_torch.  Codes are float8_e4m3fn; uint8
 # tensors of the same bytes are taken too.
 
 _F8 = torch.float8_e4m3fn
@@ -592,6 +594,10 @@ def aq_fp8_quantize(X, block_rows: int = 1, *, codes=None, scales=None):
     block_rows=1: a scale for 128 k of each row, scales [.., N, ceil(K / 128)] (activations);
     block_rows=128: for 128 rows by 128 k, scales [.., ceil(N / 128), ceil(K / 128)] (weights).
     """
+    if codes is None and scales is None:
+        pair = _mx.fp8_quantize(X, block_rows)
+        if pair is not None:
+            return pair
     shape, e, n, k, ld, dev = _f8_matrix(X, "X", _MX_OUT)
     sshape = _f8_scales(shape, block_rows)
     if codes is None:
@@ -610,6 +616,9 @@ def aq_fp8_quantize(X, block_rows: int = 1, *, codes=None, scales=None):
 
 def aq_fp8_dequantize(codes, scales, block_rows: int = 1, out_dtype=None, out=None):
     """Y [.., N, K] (float32, or bfloat16) = the values of codes [.., N, K] and their scales (as aq_fp8_quantize)."""
+    y = _mx.fp8_dequantize(codes, scales, block_rows, out_dtype, out)
+    if y is not None:
+        return y
     shape, e, n, k, _, dev = _f8_matrix(codes, "codes", (_F8, _U8))
     _f8_codes(codes, "codes", shape, dev)
     _mx_need(scales, "scales", torch.float32, _f8_scales(shape, block_rows), dev)
@@ -652,6 +661,9 @@ def aq_fp8_gemm(X_codes, X_scales, codes, scales, out_dtype=None, out=None):
 
     codes [N, K], scales [ceil(N / 128), ceil(K / 128)] (as aq_fp8_quantize with block_rows=128 returns them).
     """
+    y = _mx.fp8_gemm(X_codes, X_scales, codes, scales, out_dtype, out)
+    if y is not None:
+        return y
     m, k, dev = _f8_rows(X_codes, X_scales)
     n, = _f8_weights(codes, scales, k, dev, 2)
     out, code = _mx_out(out, m, n, out_dtype, X_codes, dev)
@@ -659,6 +671,23 @@ def aq_fp8_gemm(X_codes, X_scales, codes, scales, out_dtype=None, out=None):
         _mx_call("aq_fp8_gemm", dev, X_codes.data_ptr(), X_scales.data_ptr(), m, k, codes.data_ptr(), scales.data_ptr(), n,
                  out.data_ptr(), code)
     return out
+
+
+def _f8_values(X):
+    """(rows, columns, row stride, device) of the activations X [M, K]."""
+    if getattr(X, "ndim", 2) != 2:
+        raise ValueError("X must have 2 dimensions")
+    (m, k), _, _, _, ld, dev = _f8_matrix(X, "X", _MX_OUT)
+    return m, k, ld, dev
+
+
+def _f8_workspace(workspace, need: int, like, dev: int):
+    if workspace is None:
+        return like.new_empty(need, dtype=_U8)
+    _need(workspace, "workspace", _U8, 1)
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on cuda:{dev} (got {workspace.device})")
+    return workspace
 
 
 def aq_fp8_linear_workspace(M: int, K: int) -> int:
@@ -671,18 +700,15 @@ def aq_fp8_linear(X, codes, scales, out_dtype=None, out=None, workspace=None):
 
     workspace: None allocates it; a uint8 device tensor is used as given.
     """
-    if getattr(X, "ndim", 2) != 2:
-        raise ValueError("X must have 2 dimensions")
-    (m, k), _, _, _, ld, dev = _f8_matrix(X, "X", _MX_OUT)
+    if workspace is None:
+        y = _mx.fp8_linear(X, codes, scales, out_dtype, out)
+        if y is not None:
+            return y
+    m, k, ld, dev = _f8_values(X)
     n, = _f8_weights(codes, scales, k, dev, 2)
     out, code = _mx_out(out, m, n, out_dtype, X, dev)
     if m and n:
-        if workspace is None:
-            workspace = X.new_empty(aq_fp8_linear_workspace(m, k), dtype=_U8)
-        else:
-            _need(workspace, "workspace", _U8, 1)
-            if workspace.get_device() != dev:
-                raise ValueError(f"workspace must be on cuda:{dev} (got {workspace.device})")
+        workspace = _f8_workspace(workspace, aq_fp8_linear_workspace(m, k), X, dev)
         _mx_call("aq_fp8_linear", dev, X.data_ptr(), _MX_OUT[X.dtype], m, k, ld, codes.data_ptr(), scales.data_ptr(), n,
                  out.data_ptr(), code, workspace.data_ptr(), workspace.numel())
     return out
@@ -695,6 +721,9 @@ def aq_fp8_grouped_gemm(X_codes, X_scales, codes, scales, offsets, rows=None, ou
     X_codes [T, K], X_scales [T, ceil(K / 128)], codes [E, N, K], scales [E, ceil(N / 128), ceil(K / 128)], offsets
     [E + 1] int32 and rows int32 on the device.  Rows of Y outside the offsets are not written.
     """
+    y = _mx.fp8_grouped_gemm(X_codes, X_scales, codes, scales, offsets, rows, out_dtype, out)
+    if y is not None:
+        return y
     t, k, dev = _f8_rows(X_codes, X_scales)
     e, n = _f8_weights(codes, scales, k, dev, 3)
     m = _mx_lists(offsets, rows, e, t, dev)
@@ -730,6 +759,44 @@ def aq_fp8_swiglu_quantize(H, end=None, *, codes=None, scales=None):
         _mx_call("aq_fp8_swiglu_quantize", dev, H.data_ptr(), _MX_OUT[H.dtype], m, k // 2, _ptr(end), codes.data_ptr(),
                  scales.data_ptr())
     return codes, scales
+
+
+def aq_fp8_experts_workspace(T: int, top: int, K: int, E: int, I: int, out_dtype=torch.float32) -> int:
+    return int(_lib.load().aq_fp8_experts_workspace(T, top, K, E, I, _MX_OUT[out_dtype]))
+
+
+def aq_fp8_experts(X, gate_up_codes, gate_up_scales, down_codes, down_scales, ids, weights, out_dtype=None, workspace=None):
+    """(out [T, K], products [T * top, K] f32, slots [T, top] int32): a mixture's gated experts with FP8 weights.
+
+    out[t] = sum_j weights[t, j] D_e Q(silu(G_e Q(x[t])) * U_e Q(x[t])) for the experts e = ids[t, j] (int32; others than
+    0 .. E - 1 add nothing), Q the rounding to FP8 rows.  gate_up [E, 2I, K] and down [E, K, I] as codes and scales in
+    128 x 128 blocks; X f32 or bf16, its rows may be strided; weights f32; out float32, or bfloat16 with the products
+    on the FP8 matrix instructions.  products holds a choice's result in row slots[t, j] (not written for a choice
+    without an expert), as aq_moe_combine and its gradient take them.
+    workspace: None allocates it; a uint8 device tensor is used as given.
+    """
+    if workspace is None:
+        got = _mx.fp8_experts(X, gate_up_codes, gate_up_scales, down_codes, down_scales, ids, weights, out_dtype)
+        if got is not None:
+            return got
+    t, k, ld, dev = _f8_values(X)
+    e, n = _f8_weights(gate_up_codes, gate_up_scales, k, dev, 3)
+    if n % 2:
+        raise ValueError(f"gate_up must be [E, 2I, K] (got {[e, n, k]})")
+    if tuple(_f8_weights(down_codes, down_scales, n // 2, dev, 3)) != (e, k):
+        raise ValueError(f"down must be {[e, k, n // 2]} (got {list(down_codes.shape)})")
+    _need(ids, "ids", torch.int32, 2)
+    top = ids.shape[1]
+    _mx_need(ids, "ids", torch.int32, (t, top), dev)
+    _mx_need(weights, "weights", torch.float32, (t, top), dev)
+    out, code = _mx_out(None, t, k, out_dtype, X, dev)
+    products, slots = X.new_empty((t * top, k), dtype=torch.float32), torch.empty_like(ids)
+    workspace = _f8_workspace(workspace, aq_fp8_experts_workspace(t, top, k, e, n // 2, out.dtype), X, dev)
+    _mx_call("aq_fp8_experts", dev, X.data_ptr(), _MX_OUT[X.dtype], t, k, ld, gate_up_codes.data_ptr(),
+             gate_up_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), e, n // 2, ids.data_ptr(),
+             weights.data_ptr(), top, products.data_ptr(), slots.data_ptr(), out.data_ptr(), code, workspace.data_ptr(),
+             workspace.numel())
+    return out, products, slots
 
 
 # ---- routing to experts --------------------------------------------------------------------
@@ -768,6 +835,9 @@ def aq_moe_route(logits, top: int, *, score: str = "softmax", bias=None, groups:
     experts of the top_groups best runs of E / groups neighbours; renormalize divides a token's weights by their sum.
     An expert whose logit is -inf is never chosen; slots left over get id -1 and weight 0.
     """
+    pair = _mx.route(logits, top, score, bias, groups, top_groups, renormalize, scale)
+    if pair is not None:
+        return pair
     t, e, ld, dev = _logits(logits)
     if bias is not None:
         _mx_need(bias, "bias", torch.float32, (e,), dev)
@@ -784,6 +854,9 @@ def aq_moe_route(logits, top: int, *, score: str = "softmax", bias=None, groups:
 def aq_moe_route_backward(logits, ids, weights, dweights, *, score: str = "softmax", renormalize: bool = True,
                           scale: float = 1.0):
     """dlogits [T, E] (the logits' type): the gradient of sum(dweights * weights) at the choices that aq_moe_route made."""
+    y = _mx.route_backward(logits, ids, weights, dweights, score, renormalize, scale)
+    if y is not None:
+        return y
     t, e, ld, dev = _logits(logits)
     if getattr(ids, "ndim", 0) != 2:
         raise ValueError("ids must be [T, top]")

@@ -740,7 +740,7 @@ aq_status aq_fp8_gemm(const uint8_t* x_codes, const float* x_scales, int64_t M, 
   if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
   if (M == 0 || N == 0) return ok();
   return runtime_status(aq::launch_fp8_gemm(x_codes, x_scales, (int)M, (int)K, codes, scales, 1, (int)N, nullptr, nullptr,
-                                            (int)M, Y, y_dtype == AQ_BF16, (hipStream_t)stream),
+                                            (int)M, Y, y_dtype == AQ_BF16, false, (hipStream_t)stream),
                         fn);
 }
 
@@ -771,7 +771,7 @@ aq_status aq_fp8_linear(const void* X, int32_t x_dtype, int64_t M, int64_t K, in
   hipError_t e = aq::launch_fp8_quantize(X, x_dtype == AQ_BF16, 1, M, K, ldx, false, x_codes, x_scales, (hipStream_t)stream);
   if (e == hipSuccess)
     e = aq::launch_fp8_gemm(x_codes, x_scales, (int)M, (int)K, codes, scales, 1, (int)N, nullptr, nullptr, (int)M, Y,
-                            y_dtype == AQ_BF16, (hipStream_t)stream);
+                            y_dtype == AQ_BF16, false, (hipStream_t)stream);
   return runtime_status(e, fn);
 }
 
@@ -790,7 +790,7 @@ aq_status aq_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, int
   if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
   if (M == 0 || N == 0) return ok();
   return runtime_status(aq::launch_fp8_gemm(x_codes, x_scales, (int)T, (int)K, codes, scales, (int)E, (int)N, offsets, rows,
-                                            (int)M, Y, y_dtype == AQ_BF16, (hipStream_t)stream),
+                                            (int)M, Y, y_dtype == AQ_BF16, false, (hipStream_t)stream),
                         fn);
 }
 
@@ -935,6 +935,113 @@ aq_status aq_moe_combine_backward(const void* Y, int32_t y_dtype, int64_t R, int
   return runtime_status(aq::launch_moe_combine_backward(Y, y_dtype == AQ_BF16, R, K, slots, T, (int)top, dout,
                                                         dout_dtype == AQ_BF16, dweights, (hipStream_t)stream),
                         fn);
+}
+
+// The parts of the workspace of aq_fp8_experts, each on a boundary of 256 bytes.
+namespace {
+
+struct ExpertsParts {
+  bool fused;
+  size_t offsets, rows, group, x_codes, x_scales, h_codes, h_scales, h, bytes;
+  ExpertsParts(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I, bool fast) {
+    const int64_t C = T * top;
+    fused = aq::fp8_gated_fused(fast, (int)C, (int)K, (int)I, (int)E);
+    size_t at = 0;
+    auto part = [&at](size_t n) {
+      const size_t here = at;
+      at += (n + 255) / 256 * 256;
+      return here;
+    };
+    offsets = part(sizeof(int32_t) * (E + 1));
+    rows = part(sizeof(int32_t) * C);
+    group = part(aq_moe_group_workspace(T, top, E));
+    x_codes = part(T * K);
+    x_scales = part(sizeof(float) * T * ((K + 127) / 128));
+    h_codes = part(C * I);
+    h_scales = part(sizeof(float) * C * ((I + 127) / 128));
+    h = part(fused ? 0 : sizeof(float) * C * 2 * I);
+    bytes = at;
+  }
+};
+
+// the sizes' limits, in the order of their checks in aq_fp8_experts
+bool experts_sizes(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I) {
+  return T > 0 && T < kDimLimit && E > 0 && E <= 1024 && top > 0 && T * top < kDimLimit && K > 0 && K < kGemmDimLimit &&
+         K % 16 == 0 && I > 0 && 2 * I < kGemmDimLimit && I % 16 == 0 && E * K < (int64_t(1) << 27) &&
+         E * 2 * I < (int64_t(1) << 27) && T * K < (int64_t(1) << 36) && T * top * I < (int64_t(1) << 36) &&
+         T * top * K < (int64_t(1) << 37);
+}
+
+}  // namespace
+
+size_t aq_fp8_experts_workspace(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I, int32_t out_dtype) {
+  return experts_sizes(T, top, K, E, I) ? ExpertsParts(T, top, K, E, I, out_dtype == AQ_BF16).bytes : 0;
+}
+
+aq_status aq_fp8_experts(const void* X, int32_t x_dtype, int64_t T, int64_t K, int64_t ldx, const uint8_t* gate_up,
+                         const float* gate_up_scales, const uint8_t* down, const float* down_scales, int64_t E, int64_t I,
+                         const int32_t* ids, const float* weights, int64_t top, float* products, int32_t* slots, void* out,
+                         int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "aq_fp8_experts";
+  AQ_REQUIRE(x_dtype == AQ_F32 || x_dtype == AQ_BF16, "%s: x_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, x_dtype);
+  AQ_REQUIRE(out_dtype == AQ_F32 || out_dtype == AQ_BF16, "%s: out_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, out_dtype);
+  aq_status st = check_choices(fn, T, E, top);
+  if (st != AQ_OK) return st;
+  AQ_REQUIRE(K > 0 && K < kGemmDimLimit && K % 16 == 0, "%s: K must be a positive multiple of 16 below 2^22 (got %lld)", fn,
+             (long long)K);
+  AQ_REQUIRE(I > 0 && 2 * I < kGemmDimLimit && I % 16 == 0, "%s: I must be a positive multiple of 16 below 2^21 (got %lld)",
+             fn, (long long)I);
+  AQ_REQUIRE(T == 0 || experts_sizes(T, top, K, E, I), "%s: T %lld, top %lld, K %lld, E %lld, I %lld are too large together",
+             fn, (long long)T, (long long)top, (long long)K, (long long)E, (long long)I);
+  AQ_REQUIRE(ldx >= K && ldx < kDimLimit * 2 && ldx % (x_dtype == AQ_BF16 ? 8 : 4) == 0,
+             "%s: ldx (%lld) must be at least K and a multiple of 16 bytes", fn, (long long)ldx);
+  AQ_PTR(gate_up, 16, "gate_up");
+  AQ_PTR(gate_up_scales, 4, "gate_up_scales");
+  AQ_PTR(down, 16, "down");
+  AQ_PTR(down_scales, 4, "down_scales");
+  if (T > 0) {
+    AQ_PTR(X, 16, "X");
+    AQ_PTR(ids, 4, "ids");
+    AQ_PTR(weights, 4, "weights");
+    AQ_PTR(products, 16, "products");
+    AQ_PTR(slots, 4, "slots");
+    AQ_PTR(out, 16, "out");
+    AQ_PTR(workspace, 16, "workspace");
+    const size_t need = aq_fp8_experts_workspace(T, top, K, E, I, out_dtype);
+    AQ_REQUIRE(workspace_bytes >= need, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+  }
+  if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
+  if (T == 0) return ok();
+  const bool fast = out_dtype == AQ_BF16;
+  const ExpertsParts at(T, top, K, E, I, fast);
+  auto* const base = static_cast<uint8_t*>(workspace);
+  auto* const offsets = reinterpret_cast<int32_t*>(base + at.offsets);
+  auto* const rows = reinterpret_cast<int32_t*>(base + at.rows);
+  uint8_t* const x_codes = base + at.x_codes;
+  auto* const x_scales = reinterpret_cast<float*>(base + at.x_scales);
+  uint8_t* const h_codes = base + at.h_codes;
+  auto* const h_scales = reinterpret_cast<float*>(base + at.h_scales);
+  auto* const h = reinterpret_cast<float*>(base + at.h);
+  const hipStream_t on = (hipStream_t)stream;
+  const int C = (int)(T * top);
+  hipError_t e = aq::launch_moe_group(ids, C, (int)top, (int)E, offsets, rows, slots,
+                                      reinterpret_cast<uint32_t*>(base + at.group), on);
+  if (e == hipSuccess) e = aq::launch_fp8_quantize(X, x_dtype == AQ_BF16, 1, T, K, ldx, false, x_codes, x_scales, on);
+  if (at.fused) {
+    if (e == hipSuccess)
+      e = aq::launch_fp8_gated(x_codes, x_scales, (int)T, (int)K, gate_up, gate_up_scales, (int)E, (int)I, offsets, rows, C,
+                               h_codes, h_scales, fast, on);
+  } else {
+    if (e == hipSuccess)
+      e = aq::launch_fp8_gemm(x_codes, x_scales, (int)T, (int)K, gate_up, gate_up_scales, (int)E, (int)(2 * I), offsets,
+                              rows, C, h, false, fast, on);
+    if (e == hipSuccess) e = aq::launch_fp8_swiglu_quantize(h, false, C, (int)I, offsets + E, h_codes, h_scales, on);
+  }
+  if (e == hipSuccess)
+    e = aq::launch_fp8_gemm(h_codes, h_scales, C, (int)I, down, down_scales, (int)E, (int)K, offsets, nullptr, C, products,
+                            false, fast, on);
+  if (e == hipSuccess) e = aq::launch_moe_combine(products, false, C, K, slots, weights, T, (int)top, out, fast, on);
+  return runtime_status(e, fn);
 }
 
 }  // extern "C"

@@ -81,14 +81,23 @@ hipError_t launch_fp8_quantize(const void* X, bool x_bf16, int64_t E, int64_t N,
 hipError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t E, int64_t N, int64_t K, bool blocks,
                                  void* Y, bool y_bf16, hipStream_t stream);
 // Products of FP8 rows X [T, K] with scales XS [T, ceil(K / 128)] and weights in 128 x 128 blocks.  offsets NULL: dense
-// (E = 1, T = M); else grouped by expert, rows NULL or [M]
+// (E = 1, T = M); else grouped by expert, rows NULL or [M].  bf16 Y is computed by the FP8 matrix instructions, fp32 Y by
+// the bf16 ones, or grouped with `fast` by the FP8 ones too
 hipError_t launch_fp8_gemm(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
-                           int N, const int32_t* offsets, const int32_t* rows, int M, void* Y, bool y_bf16,
+                           int N, const int32_t* offsets, const int32_t* rows, int M, void* Y, bool y_bf16, bool fast,
                            hipStream_t stream);
 // The kernel form that such a product takes on a device of `cus` compute units (E = 1: dense), and a form's
 // description (negative past the last): the tests hold that every form is run.
 extern "C" int fp8_form(bool y_bf16, bool grouped, int M, int K, int N, int E, int cus);
 extern "C" int fp8_form_name(bool y_bf16, int form, char* to, size_t n);
+// (of the product with the gated activation: negative where the activation is a kernel of its own)
+extern "C" int fp8_gated_form(bool fast, int M, int K, int I, int E, int cus);
+// The first product of an expert's gated MLP with its activation: h = silu(g) u of [g | u] = X times weights [E, 2 I, K]
+// by expert, rounded to FP8 rows (codes [M, I], scales [M, I / 128]); where fp8_gated_fused holds.
+bool fp8_gated_fused(bool fast, int M, int K, int I, int E);
+hipError_t launch_fp8_gated(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
+                            int I, const int32_t* offsets, const int32_t* rows, int M, uint8_t* h_codes, float* h_scales,
+                            bool fast, hipStream_t stream);
 // Routing: T tokens, rows of logits ld elements apart
 struct RouteArgs {
   const void* logits;

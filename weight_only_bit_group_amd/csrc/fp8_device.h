@@ -65,6 +65,12 @@ __device__ __forceinline__ uint32_t row_umax(uint32_t v) {
   return v;
 }
 
+// silu(g) u; silu(g) is g times the reciprocal of 1 + 2^(-g log2 e), each of the two within 1 ulp: far below the
+// rounding to E4M3 that follows
+__device__ __forceinline__ float gated(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
+}
+
 // eight consecutive values of a row
 template <bool BF16>
 struct Eight {

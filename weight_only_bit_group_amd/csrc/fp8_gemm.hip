@@ -52,8 +52,12 @@ struct F8Args {
   const int32_t* offsets;  // grouped: [E + 1]
   const int32_t* rows;     // grouped: [M] activation rows, or NULL
   int E, T;                // experts; rows of X
-  void* Y;
+  void* Y;                 // [M, N], or the codes [M, N / 2] of the gated activation
+  float* YS;               // the codes' scales [M, nnb / 2]
 };
+
+// what becomes of a tile's sums: fp32, rounded to bf16, or h = silu(g) u of the columns [g | u] in FP8
+enum class Out { F32, BF16, GATED };
 
 // 4 bytes per lane from the lane's own address; lane l lands at lds + 4 l
 __device__ __forceinline__ void dma4_at(const void* src, uint32_t lds) {
@@ -136,9 +140,9 @@ struct F8Split {
   static_assert((R - 1) * DMA < 64 && LDS <= 160 * 1024, "loads in flight are counted in six bits");
 };
 
-template <class C, bool GROUPED, bool BF16>
+template <class C, bool GROUPED, bool WIDE, Out OUT>
 __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
-  using Op = Operand<!BF16>;
+  using Op = Operand<WIDE>;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -265,7 +269,7 @@ __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[4 * j + c] = lost ? __builtin_nanf("") : v[j][c];
-    store_columns<BF16, 4 * C::FN>(a, r, t.n0 + 4 * C::FN * g, o);
+    store_columns<OUT == Out::BF16, 4 * C::FN>(a, r, t.n0 + 4 * C::FN * g, o);
   };
   if constexpr (C::NW == 1) {
 #pragma unroll
@@ -302,7 +306,8 @@ struct F8Cfg {
   static constexpr int A_DMA = BM / 8 / NW;   // loads per wave and stage, 1 KiB each
   static constexpr int B_DMA = BN / 8 / NW;
   static constexpr bool SPLIT = false;
-  static constexpr int S_ROWS = BM / NW;      // rows whose scales a wave loads per stage, by one load of a dword a lane
+  // rows whose scales a wave loads per stage, by one load of a dword a lane (fewer than 16 a wave: some are loaded twice)
+  static constexpr int S_ROWS = std::max(16, BM / NW);
   static constexpr int LDS = 2 * 128 * (BM + BN) + 512 * NW;
   // blocks that a compute unit holds; their registers leave room for 8 waves, or 12
   static constexpr int PER_CU = std::max(1, std::min(160 * 1024 / LDS, (FM * FN >= 16 ? 8 : 12) / NW));
@@ -311,9 +316,12 @@ struct F8Cfg {
   static_assert(S_ROWS % 16 == 0 && S_ROWS <= 64, "the scales of 16 rows lie together");
 };
 
-template <class C, bool GROUPED, bool BF16>
+template <class C, bool GROUPED, bool WIDE, Out OUT>
 __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
-  using Op = Operand<!BF16>;
+  using Op = Operand<WIDE>;
+  constexpr bool GATED = OUT == Out::GATED;
+  static_assert(!GATED || (GROUPED && C::BN == 256 && C::FN == 4), "a block of 128 columns of h, 8 of them a lane");
+  constexpr int COLS = GATED ? 128 : C::BN;   // columns of the output that a tile has
   __shared__ __attribute__((aligned(1024))) uint8_t Xs[2][C::BM * 128];
   __shared__ __attribute__((aligned(1024))) uint8_t Ws[2][C::BN * 128];
   __shared__ __attribute__((aligned(256))) float Ss[2][C::NW * 64];
@@ -322,10 +330,11 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wid / C::WN, wn = wid % C::WN;
   const int l16 = lane & 15, g = lane >> 4;
-  const int tiles_n = (a.N + C::BN - 1) / C::BN;
+  const int inner = a.N / 2;                  // gated: columns of g and of u
+  const int tiles_n = GATED ? inner / 128 : (a.N + C::BN - 1) / C::BN;
   Tile t;
   if constexpr (GROUPED) {
-    if (!grouped_tile<C::BM>(a, tiles_n, C::BN, blockIdx.x, t)) return;   // the whole block
+    if (!grouped_tile<C::BM>(a, tiles_n, COLS, blockIdx.x, t)) return;   // the whole block
   } else {
     // groups of four row tiles walked column by column: the 32 tiles that an XCD runs together are four rows of
     // eight (an eighth of the row tiles, two rows of 16, costs 3% at 4096 rows)
@@ -340,10 +349,14 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
     t.r1 = min(t.r0 + C::BM, a.M);
     t.n0 = __builtin_amdgcn_readfirstlane((within / gm) * C::BN);
   }
-  // LDS row i of the weights: row i's wave region, operand j = (i / 16) % FN, operand row i % 16 = 4 g + v
+  // LDS row i of the weights: row i's wave region, operand j = (i / 16) % FN, operand row i % 16 = 4 g + v.  Gated: a
+  // wave's first FN / 2 operands are rows of G, the others the same rows of U, so a lane has both of 2 FN columns of h.
   auto wrow = [&](int i) {
-    const int n = (i / (16 * C::FN)) * (16 * C::FN) + ((i & 15) >> 2) * (4 * C::FN) + 4 * ((i / 16) % C::FN) + (i & 3);
-    return min(n, a.N - 1 - t.n0);
+    const int j = (i / 16) % C::FN;
+    if constexpr (GATED)
+      return (i / (16 * C::FN)) * (8 * C::FN) + ((i & 15) >> 2) * (2 * C::FN) + 4 * (j % (C::FN / 2)) + (i & 3) +
+             (j < C::FN / 2 ? 0 : inner);
+    return min((i / (16 * C::FN)) * (16 * C::FN) + ((i & 15) >> 2) * (4 * C::FN) + 4 * j + (i & 3), a.N - 1 - t.n0);
   };
   auto xrow = [&](int i) -> int64_t {
     const int r = min(t.r0 + i, t.r1 - 1);
@@ -354,13 +367,13 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
   // load j of wave w covers 8 rows from 8 (j NW + w) on; the unit that a lane fetches is the same in all of them
   static_assert(C::NW % 2 == 0, "the permutation's period is 16 rows");
   const int unit = swizzle(8 * wid + (lane >> 3), lane & 7);
-  uint32_t xsrc[C::A_DMA], wsrc[C::B_DMA];   // units from X (X is below 2^36 bytes), bytes from wtile (below 2^31)
+  uint32_t xsrc[C::A_DMA], wsrc[C::B_DMA];   // units from X (X is below 2^36 bytes), bytes from wtile (below 2^32)
 #pragma unroll
   for (int j = 0; j < C::A_DMA; ++j)
     xsrc[j] = (uint32_t)((xrow(8 * (j * C::NW + wid) + (lane >> 3)) * a.K) >> 4) + unit;
 #pragma unroll
   for (int j = 0; j < C::B_DMA; ++j) wsrc[j] = (uint32_t)wrow(8 * (j * C::NW + wid) + (lane >> 3)) * (uint32_t)a.K + 16u * unit;
-  const float* ssrc = a.XS + xrow(C::S_ROWS * wid + lane % C::S_ROWS) * a.nkb;
+  const float* ssrc = a.XS + xrow((C::S_ROWS * wid + lane % C::S_ROWS) % C::BM) * a.nkb;
   const int left = (a.K - last * 128) >> 4;   // units of the last block
   const uint32_t back = max(unit - left + 1, 0);
   auto issue = [&](int s, int buf) {
@@ -377,7 +390,8 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
   // (uniform over the wave: the constant address space makes it a scalar load; a wave whose columns are all past N reads
   // the last block's)
   const auto* wscale = (const __attribute__((address_space(4))) float*)(uint64_t)uniform(reinterpret_cast<const uint8_t*>(
-      a.WS + ((int64_t)t.e * a.nnb + min((t.n0 + wn * 16 * C::FN) >> 7, a.nnb - 1)) * a.nkb));
+      a.WS + ((int64_t)t.e * a.nnb + (GATED ? t.n0 >> 7 : min((t.n0 + wn * 16 * C::FN) >> 7, a.nnb - 1))) * a.nkb));
+  const auto* uscale = wscale + (GATED ? (int64_t)(a.nnb / 2) * a.nkb : 0);   // gated: the scales of U
 
   f32x4 acc[C::FM][C::FN];
 #pragma unroll
@@ -397,7 +411,7 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
   static_assert(C::FM % 2 == 0, "row blocks alternate between two sets of registers");
   u32x4 wr[C::FN][2], xr[2][2];
   f32x4 p[C::FN];
-  float fr[2], sw, swnext, before = 0.0f;
+  float fr[2], sw, swnext, uw = 0.0f, uwnext = 0.0f, before = 0.0f, ubefore = 0.0f;
 #pragma unroll
   for (int j = 0; j < C::FN; ++j) p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   auto load_w = [&](const uint8_t* tile, int j) {
@@ -413,7 +427,8 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
   };
   auto add = [&](int i, int j) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[j][v], before, acc[i][j][v]);
+    for (int v = 0; v < 4; ++v)
+      acc[i][j][v] = __builtin_fmaf(p[j][v], GATED && j >= C::FN / 2 ? ubefore : before, acc[i][j][v]);
   };
   auto stage = [&](int s, auto last_) {
     constexpr bool LAST = decltype(last_)::value;
@@ -422,16 +437,17 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
     Op w[C::FN];
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) w[j] = Op(wr[j][0], wr[j][1]);
-    const float by = sw;
+    const float by = sw, uby = uw;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
       const bool hand = !LAST && i + 1 == C::FM;
       if (hand) {
         drain_barrier();
         swnext = wscale[s + 1];
+        if (GATED) uwnext = uscale[s + 1];
       }
       const Op x = LAST ? Op(xr[i & 1][0] & keep0, xr[i & 1][1] & keep1) : Op(xr[i & 1][0], xr[i & 1][1]);
-      const float f = fr[i & 1] * by;
+      const float f = fr[i & 1] * by, uf = fr[i & 1] * uby;
       if (hand) load_x(buf ^ 1, 0);
       else if (i + 1 < C::FM) load_x(buf, i + 1);
       __builtin_amdgcn_sched_barrier(0);
@@ -444,9 +460,11 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
       }
       if (hand) issue(min(s + 2, last), buf);
       before = f;
+      ubefore = uf;
       __builtin_amdgcn_sched_barrier(0);
     }
     if (!LAST) sw = swnext;
+    if (!LAST) uw = uwnext;
   };
   issue(0, 0);
   drain_barrier();
@@ -455,6 +473,7 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
   for (int j = 0; j < C::FN; ++j) load_w(&Ws[0][0], j);
   load_x(0, 0);
   sw = wscale[0];
+  if (GATED) uw = uscale[0];
   for (int s = 0; s < last; ++s) stage(s, std::false_type{});
   stage(last, std::true_type{});
 #pragma unroll
@@ -462,17 +481,58 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_tile_kernel(F8Args a) {
   // no load may land in LDS that the next block owns by then
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
+  if constexpr (GATED) {
+    // a block of h: 8 columns a lane, 32 a wave, its largest magnitude over the WN waves of the row through LDS
+    uint32_t* top = reinterpret_cast<uint32_t*>(&Xs[0][0]);   // [BM][WN]
+    __syncthreads();                                          // (every wave's loads have landed)
 #pragma unroll
-  for (int i = 0; i < C::FM; ++i) {
-    const int r = t.r0 + wm * 16 * C::FM + 16 * i + l16;
-    if (r >= t.r1) continue;
-    const bool lost = GROUPED && source_row(a, r) < 0;
-    float o[4 * C::FN];
+    for (int i = 0; i < C::FM; ++i) {
+      const int r = t.r0 + wm * 16 * C::FM + 16 * i + l16;
+      const bool lost = r < t.r1 && source_row(a, r) < 0;
+      uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j)
+      for (int j = 0; j < C::FN / 2; ++j)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) o[4 * j + v] = lost ? __builtin_nanf("") : acc[i][j][v];
-    store_columns<BF16, 4 * C::FN>(a, r, t.n0 + wn * 16 * C::FN + 4 * C::FN * g, o);
+        for (int v = 0; v < 4; ++v) {
+          const float h = lost ? __builtin_nanf("") : fp8::gated(acc[i][j][v], acc[i][j + C::FN / 2][v]);
+          acc[i][j][v] = h;
+          m = max(m, fp8::abs_bits(h));
+        }
+      m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+      if (g == 0) top[(wm * 16 * C::FM + 16 * i + l16) * C::WN + wn] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+      const int at = wm * 16 * C::FM + 16 * i + l16, r = t.r0 + at;
+      if (r >= t.r1) continue;
+      uint32_t m = 0;
+#pragma unroll
+      for (int w = 0; w < C::WN; ++w) m = max(m, top[at * C::WN + w]);
+      const float scale = fp8::scale_of(m);
+      float h[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) h[c] = acc[i][c / 4][c % 4];
+      uint32_t w[2];
+      fp8::codes_of<2>(h, scale, w);
+      *reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(a.Y) + (int64_t)r * inner + t.n0 + 8 * C::FN * wn + 8 * g) =
+          w[0] | ((uint64_t)w[1] << 32);
+      if (wn == 0 && g == 0) a.YS[(int64_t)r * (a.nnb / 2) + (t.n0 >> 7)] = scale;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+      const int r = t.r0 + wm * 16 * C::FM + 16 * i + l16;
+      if (r >= t.r1) continue;
+      const bool lost = GROUPED && source_row(a, r) < 0;
+      float o[4 * C::FN];
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[4 * j + v] = lost ? __builtin_nanf("") : acc[i][j][v];
+      store_columns<OUT == Out::BF16, 4 * C::FN>(a, r, t.n0 + wn * 16 * C::FN + 4 * C::FN * g, o);
+    }
   }
 }
 
@@ -482,12 +542,12 @@ int64_t row_tiles(const F8Args& a) {
   return GROUPED ? std::min<int64_t>(a.M, a.M / C::BM + a.E) : (a.M + C::BM - 1) / C::BM;
 }
 
-template <class C, bool GROUPED, bool BF16>
+template <class C, bool GROUPED, bool WIDE, Out OUT>
 hipError_t launch(const F8Args& a, hipStream_t stream) {
-  const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;
+  const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;   // (gated: BN / 2 columns of each half of N)
   const dim3 grid((unsigned)(row_tiles<C, GROUPED>(a) * tiles_n)), block(C::NT);
   if constexpr (C::SPLIT) {
-    const auto kernel = fp8_split_kernel<C, GROUPED, BF16>;
+    const auto kernel = fp8_split_kernel<C, GROUPED, WIDE, OUT>;
     if (C::LDS > 64 * 1024) {
       // the kernel's limit of dynamic LDS, raised once per device (bit d of done)
       static std::atomic<uint64_t> done{0};
@@ -503,7 +563,7 @@ hipError_t launch(const F8Args& a, hipStream_t stream) {
     }
     hipLaunchKernelGGL(kernel, grid, block, C::LDS, stream, a);
   } else {
-    hipLaunchKernelGGL((fp8_tile_kernel<C, GROUPED, BF16>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((fp8_tile_kernel<C, GROUPED, WIDE, OUT>), grid, block, 0, stream, a);
   }
   return hipGetLastError();
 }
@@ -545,45 +605,78 @@ struct F8Form {
 };
 
 // f(the forms of a product)
-template <bool BF16, class F>
+template <bool WIDE, Out OUT, class F>
 auto with_forms(F f) {
-  if constexpr (BF16)
-    return f(F8Form<F8Split<1, 1, 16, 1>>{{0.000f, 2.616f, 0.605f, 0.055f}}, F8Form<F8Split<1, 1, 4, 4>>{{0.735f, 2.076f, 0.251f, 0.052f}},
-             F8Form<F8Split<1, 4, 8, 1>>{{0.989f, 2.705f, 0.614f, 0.040f}}, F8Form<F8Split<1, 4, 2, 3>>{{0.931f, 2.521f, 0.461f, 0.060f}},
-             F8Form<F8Split<2, 4, 4, 1>>{{0.281f, 3.417f, 0.656f, 0.050f}}, F8Form<F8Cfg<2, 2, 2, 4>>{{2.990f, 0.875f, 0.490f, 0.070f}},
-             F8Form<F8Cfg<2, 2, 4, 4>>{{1.234f, 3.150f, 0.743f, 0.056f}}, F8Form<F8Cfg<2, 4, 8, 4>>{{0.000f, 9.719f, 1.253f, 0.086f}});
+  if constexpr (OUT == Out::GATED && !WIDE)
+    return f(F8Form<F8Cfg<1, 4, 2, 4>>{{2.966f, 1.859f, 0.594f, 0.099f}}, F8Form<F8Cfg<2, 4, 4, 4>>{{0.000f, 5.582f, 1.952f, 0.020f}});
+  else if constexpr (OUT == Out::GATED)
+    return f(F8Form<F8Cfg<1, 4, 2, 4>>{{3.092f, 2.256f, 0.952f, 0.063f}}, F8Form<F8Cfg<2, 4, 4, 4>>{{0.250f, 5.595f, 2.177f, 0.037f}});
+  else if constexpr (!WIDE)
+    return f(F8Form<F8Split<1, 1, 16, 1>>{{0.036f, 3.309f, 0.383f, 0.070f}}, F8Form<F8Split<1, 1, 4, 4>>{{1.588f, 1.234f, 0.274f, 0.062f}},
+             F8Form<F8Split<1, 4, 8, 1>>{{1.326f, 2.788f, 0.783f, 0.037f}}, F8Form<F8Split<2, 4, 4, 1>>{{1.616f, 2.945f, 0.555f, 0.055f}},
+             F8Form<F8Cfg<1, 4, 2, 2>>{{0.620f, 3.186f, 0.428f, 0.052f}}, F8Form<F8Cfg<2, 2, 4, 4>>{{0.000f, 4.839f, 0.826f, 0.043f}},
+             F8Form<F8Cfg<2, 4, 8, 4>>{{2.859f, 14.527f, 1.371f, 0.072f}});
   else
-    return f(F8Form<F8Split<1, 1, 16, 1>>{{3.012f, 0.000f, 0.562f, 0.047f}}, F8Form<F8Split<1, 1, 4, 4>>{{2.203f, 0.750f, 0.344f, 0.057f}},
-             F8Form<F8Split<1, 4, 8, 1>>{{2.190f, 1.209f, 1.005f, 0.029f}}, F8Form<F8Split<1, 4, 2, 3>>{{2.108f, 1.458f, 0.502f, 0.054f}},
-             F8Form<F8Split<2, 4, 4, 1>>{{0.286f, 3.508f, 0.802f, 0.048f}}, F8Form<F8Cfg<1, 4, 4, 2>>{{0.000f, 4.378f, 0.535f, 0.088f}},
-             F8Form<F8Cfg<2, 2, 4, 4>>{{0.000f, 5.215f, 0.705f, 0.116f}});
+    return f(F8Form<F8Split<1, 1, 16, 1>>{{3.764f, 0.561f, 0.491f, 0.063f}}, F8Form<F8Split<1, 1, 4, 4>>{{2.022f, 1.443f, 0.305f, 0.085f}},
+             F8Form<F8Split<1, 4, 8, 1>>{{1.674f, 2.108f, 1.077f, 0.047f}}, F8Form<F8Split<2, 4, 4, 1>>{{1.152f, 2.372f, 0.817f, 0.058f}},
+             F8Form<F8Cfg<1, 4, 2, 2>>{{0.591f, 3.396f, 0.506f, 0.049f}}, F8Form<F8Cfg<2, 2, 4, 4>>{{2.378f, 3.801f, 0.886f, 0.079f}});
 }
 
-// the index of the form that the product takes on a device of `cus` compute units
-template <bool GROUPED, bool BF16>
-int least(const F8Args& a, int cus) {
-  return with_forms<BF16>([&](auto... form) {
+// the index of the form that the product takes on a device of `cus` compute units, and its estimated time
+struct Choice {
+  int form;
+  float us;
+};
+template <bool GROUPED, bool WIDE, Out OUT>
+Choice least(const F8Args& a, int cus) {
+  return with_forms<WIDE, OUT>([&](auto... form) {
     const float t[] = {estimate<typename decltype(form)::C, GROUPED>(a, form.cost, cus)...};
-    return (int)(std::min_element(std::begin(t), std::end(t)) - std::begin(t));
+    const auto* best = std::min_element(std::begin(t), std::end(t));
+    return Choice{(int)(best - std::begin(t)), *best};
   });
 }
 
-template <bool GROUPED, bool BF16>
+template <bool GROUPED, bool WIDE, Out OUT>
 hipError_t launch_any(const F8Args& a, hipStream_t stream) {
-  return with_forms<BF16>([&](auto... form) {
+  return with_forms<WIDE, OUT>([&](auto... form) {
     using Fn = hipError_t (*)(const F8Args&, hipStream_t);
-    const Fn fn[] = {launch<typename decltype(form)::C, GROUPED, BF16>...};
-    return fn[least<GROUPED, BF16>(a, device_cu_count())](a, stream);
+    const Fn fn[] = {launch<typename decltype(form)::C, GROUPED, WIDE, OUT>...};
+    return fn[least<GROUPED, WIDE, OUT>(a, device_cu_count()).form](a, stream);
   });
 }
 
 }  // namespace
 
-int fp8_form(bool y_bf16, bool grouped, int M, int K, int N, int E, int cus) {
+namespace {
+
+F8Args sizes(int M, int K, int N, int E) {
   F8Args a = {};
   a.M = M, a.N = N, a.K = K, a.E = E, a.nkb = (K + 127) / 128, a.nnb = (N + 127) / 128;
-  return y_bf16 ? grouped ? least<true, true>(a, cus) : least<false, true>(a, cus)
-                : grouped ? least<true, false>(a, cus) : least<false, false>(a, cus);
+  return a;
+}
+
+}  // namespace
+
+int fp8_form(bool y_bf16, bool grouped, int M, int K, int N, int E, int cus) {
+  const F8Args a = sizes(M, K, N, E);
+  return (y_bf16 ? grouped ? least<true, false, Out::BF16>(a, cus) : least<false, false, Out::BF16>(a, cus)
+                 : grouped ? least<true, true, Out::F32>(a, cus) : least<false, true, Out::F32>(a, cus)).form;
+}
+
+// Whether h = silu(g) u is rounded to FP8 by the product that makes g and u (whole blocks of h, an expert's weights within
+// 32 bits of offset), or written in fp32 and rounded by a kernel of its own: the least estimated time, with figures fitted
+// like the products' to 58 sizes for both.  By sizes alone, so that a workspace can be told from them.  Both sides, us, on
+// 64 experts of [2 x 1408, 2048], bf16 out: 16 tokens of 8 choices 67 fused, 59 apart; 2048 tokens 210 and 218.
+bool fp8_gated_fused(bool fast, int M, int K, int I, int E) { return fp8_gated_form(fast, M, K, I, E, 256) >= 0; }
+
+int fp8_gated_form(bool fast, int M, int K, int I, int E, int cus) {
+  if (I % 128 || (int64_t)2 * I * K >= (int64_t(1) << 32)) return -1;
+  const F8Args a = sizes(M, K, 2 * I, E);
+  const Choice one = fast ? least<true, false, Out::GATED>(a, cus) : least<true, true, Out::GATED>(a, cus);
+  const Choice two = fast ? least<true, false, Out::F32>(a, cus) : least<true, true, Out::F32>(a, cus);
+  const float rows = 9e-6f * (float)M * (float)I;   // MB of [g | u] and h
+  const float apart = fast ? 1.32f * two.us + 1.84f + 0.06f * rows : 1.14f * two.us + 1.99f + 0.14f * rows;
+  return one.us < apart ? one.form : -1;
 }
 
 int fp8_form_name(bool y_bf16, int i, char* to, size_t n) {
@@ -592,15 +685,23 @@ int fp8_form_name(bool y_bf16, int i, char* to, size_t n) {
     const Fn fn[] = {decltype(form)::C::describe...};
     return i < 0 || i >= (int)std::size(fn) ? -1 : fn[i](to, n);
   };
-  return y_bf16 ? with_forms<true>(describe) : with_forms<false>(describe);
+  return y_bf16 ? with_forms<false, Out::BF16>(describe) : with_forms<true, Out::F32>(describe);
 }
 
 hipError_t launch_fp8_gemm(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
-                           int N, const int32_t* offsets, const int32_t* rows, int M, void* Y, bool y_bf16,
+                           int N, const int32_t* offsets, const int32_t* rows, int M, void* Y, bool y_bf16, bool fast,
                            hipStream_t stream) {
-  const F8Args a = {X, XS, codes, scales, M, N, K, (K + 127) / 128, (N + 127) / 128, offsets, rows, E, T, Y};
-  if (offsets) return y_bf16 ? launch_any<true, true>(a, stream) : launch_any<true, false>(a, stream);
-  return y_bf16 ? launch_any<false, true>(a, stream) : launch_any<false, false>(a, stream);
+  const F8Args a = {X, XS, codes, scales, M, N, K, (K + 127) / 128, (N + 127) / 128, offsets, rows, E, T, Y, nullptr};
+  if (!offsets) return y_bf16 ? launch_any<false, false, Out::BF16>(a, stream) : launch_any<false, true, Out::F32>(a, stream);
+  if (fast && !y_bf16) return launch_any<true, false, Out::F32>(a, stream);
+  return y_bf16 ? launch_any<true, false, Out::BF16>(a, stream) : launch_any<true, true, Out::F32>(a, stream);
+}
+
+hipError_t launch_fp8_gated(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
+                            int I, const int32_t* offsets, const int32_t* rows, int M, uint8_t* h_codes, float* h_scales,
+                            bool fast, hipStream_t stream) {
+  const F8Args a = {X, XS, codes, scales, M, 2 * I, K, (K + 127) / 128, I / 64, offsets, rows, E, T, h_codes, h_scales};
+  return fast ? launch_any<true, false, Out::GATED>(a, stream) : launch_any<true, true, Out::GATED>(a, stream);
 }
 
 }  // namespace aq

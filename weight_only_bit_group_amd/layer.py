@@ -449,6 +449,7 @@ class FP8Linear(torch.nn.Module):
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top, bias, how):
+        ctx.set_materialize_grads(False)
         ids, weights = B.aq_moe_route(logits, top, bias=bias, **how)
         ctx.save_for_backward(logits, ids, weights)
         ctx.how = {k: how[k] for k in ("score", "renormalize", "scale")}
@@ -458,6 +459,8 @@ class _Route(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, _, dweights):
+        if dweights is None:
+            return None, None, None, None
         logits, ids, weights = ctx.saved_tensors
         return B.aq_moe_route_backward(logits, ids, weights, dweights.float().contiguous(), **ctx.how), None, None, None
 
@@ -482,24 +485,28 @@ def route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, scor
     return ids.view(*lead, top), weights.view(*lead, top)
 
 
-class _Combine(torch.autograd.Function):
-    """The weighted sum over a token's choices, differentiable in the weights."""
+class _Experts(torch.autograd.Function):
+    """FP8Experts' call as a part of the graph: differentiable in the weights."""
 
     @staticmethod
-    def forward(ctx, name, y, slots, weights, out_dtype):
-        ctx.name = name
-        ctx.save_for_backward(y, slots)
-        return B.aq_moe_combine(y, slots, weights, out_dtype)
+    def forward(ctx, x, weights, ids, module):
+        ctx.set_materialize_grads(False)
+        ctx.name = "FP8Experts"
+        out, products, slots = module._call(x, ids, weights)
+        ctx.save_for_backward(products, slots)
+        return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        if ctx.needs_input_grad[1]:
+        if ctx.needs_input_grad[0]:
             _NoBackward.backward(ctx, grad)
-        y, slots = ctx.saved_tensors
+        if grad is None:
+            return None, None, None, None
+        products, slots = ctx.saved_tensors
         if grad.dtype not in (torch.float32, torch.bfloat16):
             grad = grad.float()
-        return None, None, None, B.aq_moe_combine_backward(y, slots, grad.contiguous()), None
+        return None, B.aq_moe_combine_backward(products, slots, grad.contiguous()), None, None
 
 
 class FP8Experts(torch.nn.Module):
@@ -513,8 +520,8 @@ class FP8Experts(torch.nn.Module):
     type) and weights [.., top], as ``route`` gives them; a choice outside 0 .. E - 1 (the filling of a padded batch, an
     expert of another rank) adds nothing.  Both layers run as one product grouped by expert each, without reading a
     count back to the host, so a call may be captured into a graph whose replays follow x, ids and weights.  A token's
-    products are added in the order of its choices, in fp32.  The output is out_dtype; with bfloat16 the products of
-    a choice are rounded to bfloat16 before they are added.  weights are differentiable, the experts are not: an error
+    products are added in the order of its choices, in fp32.  The output is out_dtype: float32 with sums in fp32
+    throughout, or bfloat16 on the FP8 matrix instructions.  weights are differentiable, the experts are not: an error
     when x's gradient is asked for.
     """
 
@@ -556,22 +563,19 @@ class FP8Experts(torch.nn.Module):
         top = ids.shape[-1]
         if ids.dtype != torch.int32:   # (numbers that 32 bits do not hold are outside the experts too)
             ids = ids.long().clamp(-1, self.num_experts).int()
-        offsets, rows, slots = B.aq_moe_group(ids.reshape(-1, top).contiguous(), self.num_experts)
-
-        def experts(x2):
-            if rows.shape[0] == 0:
-                return x2.new_empty(0, self.features, dtype=self.out_dtype)
-            h = B.aq_fp8_grouped_gemm(*B.aq_fp8_quantize(x2), self.gate_up_codes, self.gate_up_scales, offsets, rows)
-            h = B.aq_fp8_swiglu_quantize(h, offsets[-1:])
-            return B.aq_fp8_grouped_gemm(*h, self.down_codes, self.down_scales, offsets, out_dtype=self.out_dtype)
-
-        y = _forward_only("FP8Experts", experts, x2)
+        ids = ids.reshape(-1, top).contiguous()
         w = weights.reshape(-1, top).float().contiguous()
-        if torch.is_grad_enabled() and (w.requires_grad or y.requires_grad):
-            out = _Combine.apply("FP8Experts", y, slots, w, self.out_dtype)
+        if torch.is_grad_enabled() and (w.requires_grad or x2.requires_grad):
+            out = _Experts.apply(x2, w, ids, self)
         else:
-            out = B.aq_moe_combine(y, slots, w, self.out_dtype)
+            out = self._call(x2, ids, w)[0]
         return out.reshape(*x.shape[:-1], self.features)
+
+    def _call(self, x, ids, weights):
+        if ids.shape[0] == 0:
+            return x.new_empty(0, self.features, dtype=self.out_dtype), x.new_empty(0, self.features, dtype=torch.float32), ids
+        return B.aq_fp8_experts(x, self.gate_up_codes, self.gate_up_scales, self.down_codes, self.down_scales, ids, weights,
+                                self.out_dtype)
 
     def extra_repr(self) -> str:
         return f"experts={self.num_experts}, features={self.features}, inner={self.inner}, weights=fp8"

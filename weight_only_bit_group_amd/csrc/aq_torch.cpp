@@ -9,12 +9,17 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/saved_variable.h>
 
 #include <algorithm>
 
@@ -439,34 +444,111 @@ bool logits_of(PyObject* o, int device, Rows& r) {
   return r.m > 0 && r.k > 0 && (r.k == 1 || r.x->stride(1) == 1) && r.ld >= r.k;
 }
 
-// logits, top, score, bias, groups, top_groups, renormalize, scale -> (ids, weights)
+// logits [T, E], top, score, bias, groups, top_groups, renormalize, scale, as the binding takes them
+struct Routing {
+  Rows l;
+  int64_t top = 0, groups = 0, top_groups = 0;
+  int32_t score = 0;
+  bool renormalize = false;
+  float scale = 0;
+  const at::Tensor* bias = nullptr;
+  at::Tensor ids, weights;
+
+  bool read(PyObject* const* args, int device) {
+    if (!logits_of(args[0], device, l) || !integer(args[1], top) || !score_of(args[2], score) || !integer(args[4], groups) ||
+        !(args[5] == Py_None || integer(args[5], top_groups)) || !PyBool_Check(args[6]) || !number(args[7], scale))
+      return false;
+    if (args[5] == Py_None) top_groups = groups;
+    renormalize = args[6] == Py_True;
+    if (top <= 0 || top > std::min<int64_t>(l.k, 64) || groups <= 0 || groups > 64 || top_groups <= 0 || top_groups > 64)
+      return false;
+    return args[3] == Py_None || (bias = dense_of(args[3], device, F32, {l.k}));
+  }
+  bool run(int device) {
+    ids = fresh({l.m, top}, I32, device);
+    weights = fresh({l.m, top}, F32, device);
+    void* const stream = stream_of(device);
+    auto* i = static_cast<int32_t*>(ids.data_ptr());
+    auto* w = static_cast<float*>(weights.data_ptr());
+    return succeeds([&] {
+      return aq_moe_route(l.x->const_data_ptr(), code_of(l.x), l.m, l.k, l.ld, top, score, bias ? floats(bias) : nullptr,
+                          (int32_t)groups, (int32_t)top_groups, renormalize, scale, i, w, stream);
+    });
+  }
+};
+
+// -> (ids, weights)
 PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
   if (nargs != 8) Py_RETURN_NONE;
   const int device = device_for(args[0]);
   if (device < 0) Py_RETURN_NONE;
-  Rows l;
-  int64_t top = 0, groups = 0, top_groups = 0;
+  Routing r;
+  if (!r.read(args, device) || !r.run(device)) Py_RETURN_NONE;
+  return tuple_of(r.ids, r.weights);
+  END_HANDLE_TH_ERRORS
+}
+
+// The gradient of route's weights with respect to the logits, as a node of torch's graph (from Python, applying the
+// function and going back through it take 30 us of the host more).
+struct RouteBackward : public torch::autograd::Node {
+  torch::autograd::SavedVariable logits, ids, weights;
   int32_t score = 0;
+  bool renormalize = false;
   float scale = 0;
-  if (!logits_of(args[0], device, l) || !integer(args[1], top) || !score_of(args[2], score) || !integer(args[4], groups) ||
-      !(args[5] == Py_None || integer(args[5], top_groups)) || !PyBool_Check(args[6]) || !number(args[7], scale))
-    Py_RETURN_NONE;
-  if (args[5] == Py_None) top_groups = groups;
-  if (top <= 0 || top > std::min<int64_t>(l.k, 64) || groups <= 0 || groups > 64 || top_groups <= 0 || top_groups > 64)
-    Py_RETURN_NONE;
-  const at::Tensor* bias = nullptr;
-  if (args[3] != Py_None && !(bias = dense_of(args[3], device, F32, {l.k}))) Py_RETURN_NONE;
-  at::Tensor ids = fresh({l.m, top}, I32, device), weights = fresh({l.m, top}, F32, device);
-  void* const stream = stream_of(device);
-  auto* i = static_cast<int32_t*>(ids.data_ptr());
-  auto* w = static_cast<float*>(weights.data_ptr());
-  if (!succeeds([&] {
-        return aq_moe_route(l.x->const_data_ptr(), code_of(l.x), l.m, l.k, l.ld, top, score, bias ? floats(bias) : nullptr,
-                            (int32_t)groups, (int32_t)top_groups, args[6] == Py_True, scale, i, w, stream);
-      }))
-    Py_RETURN_NONE;
-  return tuple_of(ids, weights);
+
+  torch::autograd::variable_list apply(torch::autograd::variable_list&& grads) override {
+    std::lock_guard<std::mutex> lock(mutex_);
+    torch::autograd::variable_list out(1);
+    if (!grads[0].defined() || !task_should_compute_output(0)) return out;
+    const bool again = at::GradMode::is_enabled() && grads[0].requires_grad();
+    {
+      at::NoGradGuard no_grad;
+      const at::Tensor l = logits.unpack(), i = ids.unpack(), w = weights.unpack(shared_from_this());
+      const at::Tensor d = grads[0].to(F32).contiguous();
+      const c10::OptionalDeviceGuard guard(l.device());
+      out[0] = fresh({l.size(0), l.size(1)}, l.scalar_type(), l.get_device());
+      const int64_t ld = l.size(0) > 1 ? l.stride(0) : l.size(1);
+      const aq_status st = aq_moe_route_backward(l.const_data_ptr(), code_of(&l), l.size(0), l.size(1), ld, i.size(1), score,
+                                                 renormalize, scale, ints(&i), floats(&w), floats(&d), out[0].data_ptr(),
+                                                 stream_of(l.get_device()));
+      TORCH_CHECK(st == AQ_OK, "aq_moe_route_backward: ", aq_last_error());
+    }
+    if (again) {   // the gradient is not differentiable itself: asking for its gradient is an error
+      torch::autograd::DelayedError error("trying to differentiate the gradient of route", 1);
+      out = error.apply({out[0].requires_grad_(true)});
+    }
+    return out;
+  }
+  void release_variables() override {
+    std::lock_guard<std::mutex> lock(mutex_);
+    logits.reset_data();
+    ids.reset_data();
+    weights.reset_data();
+  }
+  std::string name() const override { return "RouteBackward"; }
+};
+
+// -> (ids, weights), weights part of the graph where the logits are
+PyObject* route_graph(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  if (nargs != 8) Py_RETURN_NONE;
+  const int device = device_for(args[0]);
+  if (device < 0) Py_RETURN_NONE;
+  Routing r;
+  if (!r.read(args, device) || !r.run(device)) Py_RETURN_NONE;
+  if (at::GradMode::is_enabled() && r.l.x->requires_grad()) {
+    auto node = std::shared_ptr<RouteBackward>(new RouteBackward(), torch::autograd::deleteNode);
+    node->set_next_edges(torch::autograd::collect_next_edges(*r.l.x));
+    node->score = r.score;
+    node->renormalize = r.renormalize;
+    node->scale = r.scale;
+    torch::autograd::set_history(r.weights, node);
+    node->logits = torch::autograd::SavedVariable(*r.l.x, false);
+    node->ids = torch::autograd::SavedVariable(r.ids, false);
+    node->weights = torch::autograd::SavedVariable(r.weights, true);
+  }
+  return tuple_of(r.ids, r.weights);
   END_HANDLE_TH_ERRORS
 }
 
@@ -549,6 +631,7 @@ PyMethodDef methods[] = {{"quantize", AQ_FAST(quantize)},
                          {"fp8_linear", AQ_FAST(f8_linear)},
                          {"fp8_experts", AQ_FAST(experts)},
                          {"route", AQ_FAST(route)},
+                         {"route_graph", AQ_FAST(route_graph)},
                          {"route_backward", AQ_FAST(route_backward)},
                          {nullptr, nullptr, 0, nullptr}};
 

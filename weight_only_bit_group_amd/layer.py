@@ -470,6 +470,10 @@ def route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, scor
     """(ids [.., top] int32, weights [.., top] float32) of a router's logits [.., E], as FP8Experts and MXFP4Experts take
     them; see ``binding.aq_moe_route`` for the arguments.  weights are differentiable with respect to the logits, the
     choice is not, and the bias (which only balances the choice) gets no gradient."""
+    if logits.is_cuda:
+        pair = B.moe_route_graph(logits, top, bias, score, groups, top_groups, renormalize, scale)
+        if pair is not None:
+            return pair
     lead, e = logits.shape[:-1], logits.shape[-1]
     l2 = logits.reshape(-1, e)
     if l2.dtype not in (torch.float32, torch.bfloat16):

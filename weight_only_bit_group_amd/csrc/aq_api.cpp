@@ -850,7 +850,7 @@ aq_status aq_moe_route(const void* logits, int32_t l_dtype, int64_t T, int64_t E
   AQ_REQUIRE(aligned(bias, 4), "%s: bias must be 4-byte aligned", fn);
   if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
   if (T == 0) return ok();
-  const aq::RouteArgs a = {logits, bias, T, ld, (int)E, (int)top, groups, top_groups, 0, score == AQ_SIGMOID,
+  const aq::RouteArgs a = {logits, bias, T, ld, (int)E, (int)top, groups, top_groups, 0, 0, score == AQ_SIGMOID,
                            renormalize != 0, scale, ids, weights};
   return runtime_status(aq::launch_moe_route(a, l_dtype == AQ_BF16, (hipStream_t)stream), fn);
 }
@@ -866,7 +866,7 @@ aq_status aq_moe_route_backward(const void* logits, int32_t l_dtype, int64_t T, 
   AQ_PTR(dlogits, l_dtype == AQ_BF16 ? 2 : 4, "dlogits");
   if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
   if (T == 0) return ok();
-  const aq::RouteArgs a = {logits, nullptr, T, ld, (int)E, (int)top, 1, 1, 0, score == AQ_SIGMOID, renormalize != 0, scale,
+  const aq::RouteArgs a = {logits, nullptr, T, ld, (int)E, (int)top, 1, 1, 0, 0, score == AQ_SIGMOID, renormalize != 0, scale,
                            const_cast<int32_t*>(ids), const_cast<float*>(weights)};
   return runtime_status(aq::launch_moe_route_backward(a, l_dtype == AQ_BF16, dweights, dlogits, (hipStream_t)stream), fn);
 }

@@ -106,6 +106,7 @@ struct RouteArgs {
   int E, top;
   int groups, top_groups;
   int lanes;           // of a wave for each group (set by the launch)
+  uint32_t magic;      // 2^20 over the experts of a group, rounded up (set by the launch)
   bool sigmoid, renormalize;
   float scale;
   int32_t* ids;        // [T, top]

@@ -36,8 +36,7 @@ __device__ __forceinline__ void count_run(const int32_t* ids, int64_t lo, int64_
 }
 
 // places 64 choices from i0 on, id the lane's (or -1); cnt holds the next free place of each expert
-template <class Row>
-__device__ __forceinline__ void place_64(int64_t i, int64_t end, int id, int bits, int top, uint32_t* cnt, Row* rows,
+__device__ __forceinline__ void place_64(int64_t i, int64_t end, int id, int bits, int top, uint32_t* cnt, int32_t* rows,
                                          int32_t* slots) {
   const int lane = threadIdx.x & 63;
   const uint64_t below = ((uint64_t)1 << lane) - 1;
@@ -52,7 +51,7 @@ __device__ __forceinline__ void place_64(int64_t i, int64_t end, int id, int bit
     const uint32_t at = cnt[id];
     slot = (int)(at + __popcll(same & below));
     if ((same & ~below) == ((uint64_t)1 << lane)) cnt[id] = slot + 1;   // the last of its equals
-    rows[slot] = (Row)((uint32_t)i / (uint32_t)top);
+    rows[slot] = (int)((uint32_t)i / (uint32_t)top);
   }
   if (i < end) slots[i] = slot;
 }
@@ -87,8 +86,8 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint3
   return before + incl - v;
 }
 
-// starts [E] of the experts from this workgroup's totals; offsets [E + 1] as well; returns the last, the choices that count
-__device__ __forceinline__ int starts_of(int E, uint32_t* start, uint32_t* part, int32_t* offsets) {
+// starts [E] of the experts from this workgroup's totals; offsets [E + 1] as well
+__device__ __forceinline__ void starts_of(int E, uint32_t* start, uint32_t* part, int32_t* offsets) {
   uint32_t base = 0, total = 0;
   for (int e0 = 0; e0 < E; e0 += blockDim.x) {
     const int e = e0 + threadIdx.x;
@@ -100,21 +99,18 @@ __device__ __forceinline__ int starts_of(int E, uint32_t* start, uint32_t* part,
     base += total;
   }
   if (threadIdx.x == 0) offsets[E] = (int)base;
-  return (int)base;
 }
 
-// Each wave's run, at most PER choices a lane, stays in registers between the counting and the placing.  The tokens of the
-// slots, which 16 bits hold, are gathered in LDS first: 16384 scattered stores of one compute unit take 15 us, 64 a
-// request 9.  (STAGED: up to 512 experts, whose counters leave LDS for them.)
-template <int PER, bool STAGED>
+// Each wave's run, at most PER choices a lane, stays in registers between the counting and the placing (loaded twice:
+// 25 us for 16384 choices of 64 experts, so 15).
+template <int PER>
 __global__ __launch_bounds__(1024) void group_single_kernel(const int32_t* __restrict__ ids, int C, int E, int bits, int top,
                                                            int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
                                                            int32_t* __restrict__ slots) {
-  extern __shared__ uint32_t lds[];   // counters [waves][E], starts [E], tokens [C]
+  extern __shared__ uint32_t lds[];   // counters [waves][E], starts [E]
   __shared__ uint32_t part[16];
   const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   uint32_t* start = lds + waves * E;
-  uint16_t* tokens = reinterpret_cast<uint16_t*>(start + E);
   uint32_t* cnt = lds + wave * E;
   const int run = (C + waves - 1) / waves, lo = min(wave * run, C), hi = min(lo + run, C);
   int id[PER];
@@ -136,19 +132,12 @@ __global__ __launch_bounds__(1024) void group_single_kernel(const int32_t* __res
     start[e] = sum;
   }
   __syncthreads();
-  const int count = starts_of(E, start, part, offsets);
+  starts_of(E, start, part, offsets);
   __syncthreads();
   for (int e = lane; e < E; e += 64) cnt[e] += start[e];
 #pragma unroll
   for (int j = 0; j < PER; ++j)
-    if (lo + 64 * j < hi) {
-      if constexpr (STAGED) place_64(lo + 64 * j + lane, hi, id[j], bits, top, cnt, tokens, slots);
-      else place_64(lo + 64 * j + lane, hi, id[j], bits, top, cnt, rows, slots);
-    }
-  if constexpr (STAGED) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < count; i += blockDim.x) rows[i] = tokens[i];
-  }
+    if (lo + 64 * j < hi) place_64(lo + 64 * j + lane, hi, id[j], bits, top, cnt, rows, slots);
 }
 
 // chunk b's counts of every expert: counts[b E + e]
@@ -330,20 +319,18 @@ size_t moe_group_workspace_bytes(int64_t C, int E) {
 
 hipError_t launch_moe_group(const int32_t* ids, int64_t C, int top, int E, int32_t* offsets, int32_t* rows, int32_t* slots,
                             uint32_t* work, hipStream_t stream) {
+  const int waves = group_waves(E);
+  const dim3 block(64 * waves);
   int bits = 0;
   while (1 << bits < E) ++bits;
   if (C <= kSingle) {
-    const int waves = E <= 256 ? 16 : 8;
-    const int per = (int)((C + 64 * waves - 1) / (64 * waves));   // choices of a lane
-    auto* kernel = E > 512    ? per <= 2 ? group_single_kernel<2, false> : group_single_kernel<32, false>
-                   : per <= 2 ? group_single_kernel<2, true>
-                   : per <= 16 ? group_single_kernel<16, true> : group_single_kernel<32, true>;
-    const size_t lds = sizeof(uint32_t) * (waves + 1) * E + (E > 512 ? 0 : sizeof(uint16_t) * C);   // 50 KiB at most
-    hipLaunchKernelGGL(kernel, dim3(1), dim3(64 * waves), lds, stream, ids, (int)C, E, bits, top, offsets, rows, slots);
+    const int per = (int)((C + 64 * waves - 1) / (64 * waves));   // choices of a lane: at most 16, or 32 with 8 waves
+    auto* kernel = per <= 2 ? group_single_kernel<2> : per <= 8 ? group_single_kernel<8>
+                   : per <= 16 ? group_single_kernel<16> : group_single_kernel<32>;
+    hipLaunchKernelGGL(kernel, dim3(1), block, sizeof(uint32_t) * (waves + 1) * E, stream, ids, (int)C, E, bits, top, offsets,
+                       rows, slots);
     return hipGetLastError();
   }
-  const int waves = group_waves(E);
-  const dim3 block(64 * waves);
   const int chunks = (int)((C + kChunk - 1) / kChunk);
   hipLaunchKernelGGL(group_count_kernel, dim3(chunks), block, sizeof(uint32_t) * E, stream, ids, C, E, work);
   hipLaunchKernelGGL(group_starts_kernel, dim3(1), dim3(1024), sizeof(uint32_t) * E, stream, chunks, E, work, offsets);

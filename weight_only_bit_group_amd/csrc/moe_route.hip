@@ -13,6 +13,10 @@
 // As unsigned integers that order as the keys do, their upper halves alone nearly always single out one lane:
 // an arg max is a 32-bit maximum by DPP and a ballot, the lower halves and the index only decide where more than
 // one lane has it.
+//   Few tokens are bound by the chain of dependent steps: 16 tokens of 256 experts with a bias and 8 groups take 6.2 us (8.4
+// with exchanges through LDS and keys searched again for every choice), 2.2 of them an empty launch.  Many are bound by
+// the vector instructions of the choices: 16384 tokens of 128 experts, bf16, 12.4 us and 10.1 for the gradient, where
+// their 4 and 8 MB would take 1 and 2.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -28,29 +32,55 @@ constexpr int kTokens = 4;   // waves of a workgroup, a token each
 
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 63; }
 
+// Exchanges within the wave by DPP and lane swaps (a fifth of the time of exchanges through LDS).  A value that is the
+// same in all lanes of a quad, half row, row or half wave meets its partner's there, so that after the steps up to
+// `lanes` all of them hold f over the lanes, from operands that only change places: the same bits in every lane.
 template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false));
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 | dpp<CTRL>((uint32_t)u));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;   // quad_perm [1,0,3,2], [2,3,0,1]
+
+// f(value of the lane's half, of the other half) where the halves are rows (32 lanes) or half waves
+template <bool ROWS, class F>
+__device__ __forceinline__ double across(double v, F f) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t h = (uint32_t)(u >> 32), l = (uint32_t)u;
+  const auto a = ROWS ? __builtin_amdgcn_permlane16_swap(h, h, false, false) : __builtin_amdgcn_permlane32_swap(h, h, false, false);
+  const auto b = ROWS ? __builtin_amdgcn_permlane16_swap(l, l, false, false) : __builtin_amdgcn_permlane32_swap(l, l, false, false);
+  return f(__builtin_bit_cast(double, (uint64_t)a[0] << 32 | b[0]), __builtin_bit_cast(double, (uint64_t)a[1] << 32 | b[1]));
 }
 
 // max over the wave, in every lane
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-  v = dpp_umax<0xB1>(v);    // quad_perm [1, 0, 3, 2]
-  v = dpp_umax<0x4E>(v);    // quad_perm [2, 3, 0, 1]
-  v = dpp_umax<0x124>(v);   // row_ror:4
-  v = dpp_umax<0x128>(v);   // row_ror:8
+  v = max(v, dpp<kXor1>(v));
+  v = max(v, dpp<kXor2>(v));
+  v = max(v, dpp<kHalfMirror>(v));
+  v = max(v, dpp<kMirror>(v));
   const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
   v = max(a[0], a[1]);
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return max(b[0], b[1]);
 }
 
-__device__ __forceinline__ double shfl_xor(double v, int m) { return __shfl_xor(v, m, 64); }
-
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v += shfl_xor(v, m);
-  return v;
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  v += dpp<kHalfMirror>(v);
+  v += dpp<kMirror>(v);
+  const auto plus = [](double a, double b) { return a + b; };
+  return across<false>(across<true>(v, plus), plus);
+}
+
+__device__ __forceinline__ double readlane64(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t h = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane), l = __builtin_amdgcn_readlane((uint32_t)u, lane);
+  return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
 }
 
 // integers that order as the numbers do, above 0 (0: never chosen; -inf gives 0x000F.. in 64 bits, above 0 too)
@@ -61,6 +91,11 @@ __device__ __forceinline__ uint64_t order(double v) {
 __device__ __forceinline__ uint32_t order(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
   return u >> 31 ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float wave_max(float v) {   // (not NaN)
+  const uint32_t h = wave_umax(order(v));
+  return __uint_as_float(h >> 31 ? h & 0x7FFFFFFFu : ~h);
 }
 
 template <bool BF16>
@@ -123,8 +158,7 @@ __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteArgs a) {
   double total = 1.0, top_l = 0.0;
   double s[P];
   if (whole) {
-    const uint32_t h = wave_umax(order(high));
-    const float hf = __uint_as_float(h >> 31 ? h & 0x7FFFFFFFu : ~h);
+    const float hf = wave_max(high);
     top_l = hf == -INFINITY ? 0.0 : hf;
     total = 0.0;
 #pragma unroll
@@ -178,64 +212,103 @@ __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteArgs a) {
         two = fmax(two, fmin(one, k));
         one = fmax(one, k);
       }
-    for (int m = 1; m < q; m <<= 1) {
-      const double x = shfl_xor(one, m), y = shfl_xor(two, m);
+    // the two highest of this lane's and its partner's two
+    auto meet = [&](double x, double y) {
       two = fmax(fmax(two, y), fmin(one, x));
       one = fmax(one, x);
+    };
+    if (q > 1) meet(dpp<kXor1>(one), dpp<kXor1>(two));
+    if (q > 2) meet(dpp<kXor2>(one), dpp<kXor2>(two));
+    if (q > 4) meet(dpp<kHalfMirror>(one), dpp<kHalfMirror>(two));
+    if (q > 8) meet(dpp<kMirror>(one), dpp<kMirror>(two));
+    if (q > 16) {   // (two groups: 32 lanes each)
+      const bool odd = lane >> 4 & 1;
+      double x[2], y[2];
+      across<true>(one, [&](double a, double b) { return x[0] = a, x[1] = b, a; });
+      across<true>(two, [&](double a, double b) { return y[0] = a, y[1] = b, a; });
+      meet(odd ? x[0] : x[1], odd ? y[0] : y[1]);
     }
     const double score = two == -INFINITY ? one : one + two;
     int rank = 0;   // groups ahead of this lane's
     for (int j = 0; j < a.groups; ++j) {
-      const double other = __shfl(score, j * q, 64);
+      const double other = readlane64(score, j * q);
       rank += other > score || (other == score && j < g);
     }
     const uint64_t stay = __ballot(g < a.groups && lane % q == 0 && rank < a.top_groups);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int e = lane + 64 * i;
-      if (e < a.E && !(stay >> (e / size * q) & 1)) hi[i] = lo[i] = 0;
+      const int e = lane + 64 * i, group = (int)((uint32_t)e * a.magic >> 20);   // e / size
+      if (e < a.E && !(stay >> (group * q) & 1)) hi[i] = lo[i] = 0;
     }
   }
 
   // the choices, one after the other; lane j keeps the j-th
   int id = -1;
-  uint32_t bh = 0, bl = 0, bi = 0;
-  auto local = [&]() {
-    bh = bl = 0;
-    bi = lane;
+  if constexpr (P <= 4) {
+    // a lane's keys in order, the winner's move up
+    uint32_t at[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const bool more = BIAS ? hi[i] > bh || (hi[i] == bh && lo[i] > bl) : hi[i] > bh;
-      if (more) {
-        bh = hi[i];
-        bl = lo[i];
-        bi = lane + 64 * i;
+    for (int i = 0; i < P; ++i) at[i] = lane + 64 * i;
+    auto sort2 = [&](int i, int j) {
+      const bool swap = hi[j] > hi[i] || (hi[j] == hi[i] && (lo[j] > lo[i] || (lo[j] == lo[i] && at[j] < at[i])));
+      const uint32_t h = hi[i], l = lo[i], x = at[i];
+      hi[i] = swap ? hi[j] : h, lo[i] = swap ? lo[j] : l, at[i] = swap ? at[j] : x;
+      hi[j] = swap ? h : hi[j], lo[j] = swap ? l : lo[j], at[j] = swap ? x : at[j];
+    };
+    if constexpr (P == 2) sort2(0, 1);
+    if constexpr (P == 4) sort2(0, 1), sort2(2, 3), sort2(0, 2), sort2(1, 3), sort2(1, 2);
+    for (int j = 0; j < a.top; ++j) {
+      Winner w;
+      if (!wave_best<BIAS>(hi[0], lo[0], at[0], w)) break;
+      if (lane == j) id = (int)w.index;
+      const bool mine = lane == w.lane;
+#pragma unroll
+      for (int i = 0; i + 1 < P; ++i) {
+        hi[i] = mine ? hi[i + 1] : hi[i];
+        lo[i] = mine ? lo[i + 1] : lo[i];
+        at[i] = mine ? at[i + 1] : at[i];
       }
+      hi[P - 1] = mine ? 0 : hi[P - 1];
     }
-  };
-  local();
-  for (int j = 0; j < a.top; ++j) {
-    Winner w;
-    if (!wave_best<BIAS>(bh, bl, bi, w)) break;
-    if (lane == j) id = (int)w.index;
-    if (lane == w.lane) {
+  } else {
+    // the winner's lane looks through its keys again (8 or 16: ordering them all would cost more than eight choices)
+    uint32_t bh = 0, bl = 0, bi = 0;
+    auto local = [&]() {
+      bh = bl = 0;
+      bi = lane;
 #pragma unroll
-      for (int i = 0; i < P; ++i)
-        if ((int)w.index == lane + 64 * i) hi[i] = lo[i] = 0;
-      local();
+      for (int i = 0; i < P; ++i) {
+        const bool more = BIAS ? hi[i] > bh || (hi[i] == bh && lo[i] > bl) : hi[i] > bh;
+        if (more) {
+          bh = hi[i];
+          bl = lo[i];
+          bi = lane + 64 * i;
+        }
+      }
+    };
+    local();
+    for (int j = 0; j < a.top; ++j) {
+      Winner w;
+      if (!wave_best<BIAS>(bh, bl, bi, w)) break;
+      if (lane == j) id = (int)w.index;
+      if (lane == w.lane) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          if ((int)w.index == lane + 64 * i) hi[i] = lo[i] = 0;
+        local();
+      }
     }
   }
 
   // their scores again, from the logits
   double share = 0.0;
-  const double mine = id >= 0 ? (double)logit<BF16>(a.logits, row + id) : -INFINITY;
+  const float chosen = id >= 0 ? logit<BF16>(a.logits, row + id) : -INFINITY;
+  const double mine = chosen;
   if (a.sigmoid) {
     if (id >= 0) share = sigmoid64(mine);
   } else if (a.renormalize) {
     // relative to the chosen ones' highest: their sum is at least 1
-    double h = mine;
-#pragma unroll
-    for (int m = 32; m; m >>= 1) h = fmax(h, shfl_xor(h, m));
+    const float h = wave_max(chosen);
     if (id >= 0) share = exp(mine - h);
   } else if (id >= 0) {
     share = exp(mine - top_l) / total;
@@ -285,8 +358,7 @@ __global__ __launch_bounds__(64 * kTokens) void route_backward_kernel(RouteArgs 
       l[i] = e < a.E ? logit<BF16>(a.logits, row + e) : -INFINITY;
       high = fmaxf(high, l[i]);
     }
-    const uint32_t h = wave_umax(order(high));
-    const float hf = __uint_as_float(h >> 31 ? h & 0x7FFFFFFFu : ~h);
+    const float hf = wave_max(high);
     const double top_l = hf == -INFINITY ? 0.0 : hf;
     double total = 0.0;
 #pragma unroll
@@ -301,9 +373,7 @@ __global__ __launch_bounds__(64 * kTokens) void route_backward_kernel(RouteArgs 
     v = id >= 0 ? exp(mine - top_l) / total * d : 0.0;   // p_j d_j, added to the chosen expert's
     m = wave_sum64(v);
   } else if (!a.sigmoid) {
-    double h = mine;
-#pragma unroll
-    for (int k = 32; k; k >>= 1) h = fmax(h, shfl_xor(h, k));
+    const float h = wave_max((float)mine);
     const double s = id >= 0 ? exp(mine - h) : 0.0;
     const double sum = wave_sum64(s);
     const double share = sum > 0.0 ? s / sum : 0.0;
@@ -325,7 +395,7 @@ __global__ __launch_bounds__(64 * kTokens) void route_backward_kernel(RouteArgs 
   for (int i = 0; i < P; ++i) out[i] = whole ? -p[i] * m : 0.0;
   for (int j = 0; j < a.top; ++j) {
     const int e = __builtin_amdgcn_readlane(id, j);
-    const double x = __shfl(v, j, 64);
+    const double x = readlane64(v, j);
     if (e >= 0 && (e & 63) == lane) {
 #pragma unroll
       for (int i = 0; i < P; ++i)
@@ -357,6 +427,9 @@ hipError_t with_experts(int E, F f) {
 hipError_t launch_moe_route(RouteArgs a, bool l_bf16, hipStream_t stream) {
   a.lanes = 1;
   while (2 * a.lanes * a.groups <= 64) a.lanes *= 2;
+  // e / size for e <= 1023: the multiplier is off by less than size, e times that by less than 2^20
+  const int size = a.E / a.groups;
+  a.magic = ((1u << 20) + size - 1) / size;
   const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(64 * kTokens);
   const size_t lds = a.groups > 1 ? sizeof(double) * kTokens * a.E : 0;
   return with_experts(a.E, [&](auto p) {

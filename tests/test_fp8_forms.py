@@ -1,7 +1,7 @@
 """Every form of the FP8 products is compiled for some size that the tests run (no GPU: the choice is the host's)."""
 import pytest
 
-from tests.fp8_forms import CUS, GATED, SIZES, form_of, forms
+from tests.fp8_forms import CUS, GATED, ROUNDED, SIZES, form_of, forms
 
 
 @pytest.mark.parametrize("bf16", [False, True])
@@ -33,3 +33,9 @@ def test_gated_activation_alone_where_it_has_to_be(lib):
     for fast in (False, True):
         assert lib.fp8_gated_form(fast, 16384, 2048, 1408, 64, CUS) >= 0 > lib.fp8_gated_form(fast, 16384, 2048, 1424, 64, CUS)
         assert all(lib.fp8_gated_form(fast, 1 << i, 1 << 15, 1 << 16, 2, CUS) < 0 for i in range(20))
+
+
+def test_rounded_sizes_select_their_form(lib):
+    assert {name for _, name in ROUNDED} == {name for name in forms(lib, True) if name.startswith("split 1 ")}
+    for (bf16, name), sizes in ROUNDED.items():
+        assert len(sizes) >= 3 and all(m <= 16 and m * k <= 8192 and form_of(lib, bf16, m, n, k) == name for m, n, k in sizes)

@@ -768,10 +768,8 @@ aq_status aq_fp8_linear(const void* X, int32_t x_dtype, int64_t M, int64_t K, in
   if (M == 0 || N == 0) return ok();
   auto* x_codes = static_cast<uint8_t*>(workspace);
   auto* x_scales = reinterpret_cast<float*>(x_codes + M * K);
-  hipError_t e = aq::launch_fp8_quantize(X, x_dtype == AQ_BF16, 1, M, K, ldx, false, x_codes, x_scales, (hipStream_t)stream);
-  if (e == hipSuccess)
-    e = aq::launch_fp8_gemm(x_codes, x_scales, (int)M, (int)K, codes, scales, 1, (int)N, nullptr, nullptr, (int)M, Y,
-                            y_dtype == AQ_BF16, false, (hipStream_t)stream);
+  const hipError_t e = aq::launch_fp8_linear(X, x_dtype == AQ_BF16, ldx, (int)M, (int)K, codes, scales, (int)N, Y,
+                                             y_dtype == AQ_BF16, x_codes, x_scales, (hipStream_t)stream);
   return runtime_status(e, fn);
 }
 

@@ -86,6 +86,9 @@ hipError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int6
 hipError_t launch_fp8_gemm(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
                            int N, const int32_t* offsets, const int32_t* rows, int M, void* Y, bool y_bf16, bool fast,
                            hipStream_t stream);
+// The dense product with rows of fp32 or bf16, ldx elements apart, rounded on the way in; room for their codes and scales
+hipError_t launch_fp8_linear(const void* X, bool x_bf16, int64_t ldx, int M, int K, const uint8_t* codes, const float* scales,
+                             int N, void* Y, bool y_bf16, uint8_t* x_codes, float* x_scales, hipStream_t stream);
 // The kernel form that such a product takes on a device of `cus` compute units (E = 1: dense), and a form's
 // description (negative past the last): the tests hold that every form is run.
 extern "C" int fp8_form(bool y_bf16, bool grouped, int M, int K, int N, int E, int cus);

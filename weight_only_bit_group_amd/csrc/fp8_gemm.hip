@@ -54,7 +54,11 @@ struct F8Args {
   int E, T;                // experts; rows of X
   void* Y;                 // [M, N], or the codes [M, N / 2] of the gated activation
   float* YS;               // the codes' scales [M, nnb / 2]
+  int64_t ldx;             // rows that are rounded on the way in: elements between them
 };
+
+// the activations: FP8 codes, or fp32 or bf16 rows that are rounded on the way in
+enum class In { CODES, F32, BF16 };
 
 // what becomes of a tile's sums: fp32, rounded to bf16, or h = silu(g) u of the columns [g | u] in FP8
 enum class Out { F32, BF16, GATED };
@@ -125,6 +129,10 @@ __device__ __forceinline__ void store_columns(const F8Args& a, int r, int col, c
 // the requests, 23 us against 13 for 16 rows on [4096, 14336].)
 //   Activation rows past the tile's are not fetched: their LDS bytes are whatever was there, in columns of the result
 // that are not stored.
+//   Up to 16 short rows are rounded by every block for itself, while its first weights are under way: one token on
+// [11008, 2048] takes 7.6 us, with a rounding kernel in front 9.4; 8 rows of 1024 on [11008, 1024] 6.4 and 7.6, on
+// [4096, 1024] 6.2 and 6.0 (graph-replayed; from the host a launch less).
+constexpr int kRounded = 8192;   // their values at most (32 KiB of fp32 a block)
 template <int FM_, int FN_, int NW_, int R_>
 struct F8Split {
   static constexpr int FM = FM_, FN = FN_, NW = NW_, R = R_;
@@ -140,9 +148,23 @@ struct F8Split {
   static_assert((R - 1) * DMA < 64 && LDS <= 160 * 1024, "loads in flight are counted in six bits");
 };
 
-template <class C, bool GROUPED, bool WIDE, Out OUT>
+template <class C, In IN>
+struct SplitStage {
+  static constexpr bool ROUND = IN != In::CODES;
+  static constexpr int X = ROUND ? 0 : 2048 * C::FM;
+  static constexpr int BYTES = ROUND ? 2048 * C::FN : C::STAGE, DMA = ROUND ? 2 * C::FN : C::DMA;
+  static constexpr int LDS = C::NW * std::max(C::R * BYTES, C::PART);
+  static constexpr int SIZE = IN == In::F32 ? 4 : 2;   // of a value
+  // behind the waves' buffers: codes, rows of `row` bytes (16 more than whole blocks: other banks); scales; values
+  static constexpr int row(int nkb) { return 128 * nkb + 16; }
+  static constexpr int lds(int M, int K, int nkb) { return LDS + (ROUND ? M * row(nkb) + (4 * M * nkb + 15) / 16 * 16 + SIZE * M * K : 0); }
+};
+
+template <class C, bool GROUPED, bool WIDE, Out OUT, In IN = In::CODES>
 __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
   using Op = Operand<WIDE>;
+  using S = SplitStage<C, IN>;
+  static_assert(!S::ROUND || (!GROUPED && C::FM == 1), "rows that are rounded are one tile's");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -161,7 +183,7 @@ __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
     t.n0 = (i / tiles_m) * C::BN;
   }
   const int count = (a.nkb - wid + C::NW - 1) / C::NW;   // this wave's stages: wid, wid + NW, ..
-  uint8_t* mine = lds + wid * C::R * C::STAGE;
+  uint8_t* mine = lds + wid * C::R * S::BYTES;
   auto xrow = [&](int i) -> int64_t {
     const int r = min(t.r0 + i, t.r1 - 1);
     return GROUPED ? max(source_row(a, r), 0) : r;
@@ -173,7 +195,8 @@ __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
   const uint8_t* wtile = a.W + ((int64_t)t.e * a.N + t.n0) * a.K;
   uint32_t xsrc[2 * C::FM], wsrc[2 * C::FN];   // units from X (X is below 2^36 bytes), bytes from wtile
 #pragma unroll
-  for (int j = 0; j < 2 * C::FM; ++j) xsrc[j] = (uint32_t)((xrow(8 * j + (lane >> 3)) * a.K) >> 4) + (unit ^ (4 * (j & 1)));
+  for (int j = 0; j < 2 * C::FM; ++j)
+    if (!S::ROUND) xsrc[j] = (uint32_t)((xrow(8 * j + (lane >> 3)) * a.K) >> 4) + (unit ^ (4 * (j & 1)));
 #pragma unroll
   for (int j = 0; j < 2 * C::FN; ++j)
     wsrc[j] = (uint32_t)wrow(8 * j + (lane >> 3)) * (uint32_t)a.K + 16u * (unit ^ (4 * (j & 1)));
@@ -184,10 +207,10 @@ __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
     const int s = wid + i * C::NW;
     const uint8_t* x = a.X + (int64_t)s * 128;
     const uint8_t* w = uniform(wtile + (int64_t)s * 128);
-    const uint32_t base = lds_addr(mine + slot * C::STAGE);
+    const uint32_t base = lds_addr(mine + slot * S::BYTES);
     const bool tail = s == last;
 #pragma unroll
-    for (int j = 0; j < 2 * C::FM; ++j) {
+    for (int j = 0; j < (S::ROUND ? 0 : 2 * C::FM); ++j) {
       const int back = tail ? max((unit ^ (4 * (j & 1))) - left + 1, 0) : 0;
       // (eight lanes at least, so that the load is counted)
       if (lane < 8 || 8 * j + (lane >> 3) < rows)
@@ -196,9 +219,9 @@ __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
 #pragma unroll
     for (int j = 0; j < 2 * C::FN; ++j) {
       const int back = tail ? max((unit ^ (4 * (j & 1))) - left + 1, 0) : 0;
-      dma16_from(w, wsrc[j] - 16 * back, __builtin_amdgcn_readfirstlane(base + 1024 * (2 * C::FM + j)));
+      dma16_from(w, wsrc[j] - 16 * back, __builtin_amdgcn_readfirstlane(base + S::X + 1024 * j));
     }
-    dma4_at(ssrc + s, __builtin_amdgcn_readfirstlane(base + 2048 * (C::FM + C::FN)));
+    if constexpr (!S::ROUND) dma4_at(ssrc + s, __builtin_amdgcn_readfirstlane(base + 2048 * (C::FM + C::FN)));
   };
   f32x4 acc[C::FM][C::FN];
 #pragma unroll
@@ -208,18 +231,49 @@ __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
 
   const float* wscale = a.WS + ((int64_t)t.e * a.nnb + (t.n0 >> 7)) * a.nkb;
   float scales = 0.0f;   // lane l: the weights' scale of the wave's stage i0 + l
+  uint8_t* const codes = lds + S::LDS;
+  float* const xscales = reinterpret_cast<float*>(codes + rows * S::row(a.nkb));
+  if constexpr (S::ROUND) {
+    uint8_t* const values = codes + rows * S::row(a.nkb) + (4 * rows * a.nkb + 15) / 16 * 16;
+    const int units = a.K * S::SIZE / 16;   // of a row
+    for (int i0 = 64 * wid; i0 < rows * units; i0 += C::NT) {
+      const int i = i0 + lane, r = i / units;
+      if (i < rows * units)
+        dma16_at(a.X + (r * a.ldx * S::SIZE + 16 * (i - r * units)), __builtin_amdgcn_readfirstlane(lds_addr(values) + 16 * i0));
+    }
+  }
 #pragma unroll
   for (int i = 0; i < C::R; ++i)
     if (i < count) issue(i, i);
+  if constexpr (S::ROUND) {
+    const uint8_t* const values = codes + rows * S::row(a.nkb) + (4 * rows * a.nkb + 15) / 16 * 16;
+    // every wave's values have landed, the weights behind them need not
+    if (count >= C::R) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(C::R * S::DMA) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    for (int item = threadIdx.x >> 4; item < rows * a.nkb; item += C::NT / 16) {
+      const int r = item / a.nkb, kb = item - r * a.nkb, k = 128 * kb + 8 * l16;
+      fp8::Eight<IN == In::BF16> in;
+      in.clear();
+      if (k < a.K) in.load(values, (int64_t)r * a.K + k);
+      const float s = fp8::scale_of(fp8::row_umax(in.amax()));
+      float v[8];
+      in.values(v);
+      uint32_t w[2];
+      fp8::codes_of<2>(v, s, w);
+      *reinterpret_cast<uint64_t*>(codes + r * S::row(a.nkb) + k) = w[0] | ((uint64_t)w[1] << 32);
+      if (l16 == 0) xscales[item] = s;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
   for (int i0 = 0; i0 < count; i0 += 64) {
     scales = wscale[min(wid + (i0 + lane) * C::NW, last)];
     const int stop = min(i0 + 64, count);
     for (int n = i0; n < stop; ++n) {
       const int s = wid + n * C::NW, slot = n % C::R;
-      if (n + C::R < count) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((C::R - 1) * C::DMA) : "memory");
+      if (n + C::R < count) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((C::R - 1) * S::DMA) : "memory");
       else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      const uint8_t* xt = mine + slot * C::STAGE;
-      const uint8_t* wt = xt + 2048 * C::FM;
+      const uint8_t* xt = mine + slot * S::BYTES;
+      const uint8_t* wt = xt + S::X;
       const float* st = reinterpret_cast<const float*>(xt + 2048 * (C::FM + C::FN));
       auto half = [](const uint8_t* tile, int r, int u) {
         return *reinterpret_cast<const u32x4*>(tile + 128 * r + 16 * swizzle(r, u));
@@ -228,9 +282,17 @@ __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
       float f[C::FM];
 #pragma unroll
       for (int i = 0; i < C::FM; ++i) {
-        x[i][0] = half(xt, 16 * i + l16, g);
-        x[i][1] = half(xt, 16 * i + l16, 4 + g);
-        f[i] = st[16 * i + l16];
+        if constexpr (S::ROUND) {
+          const int r = min(l16, rows - 1);
+          const uint8_t* at = codes + r * S::row(a.nkb) + 128 * s + 16 * g;
+          x[i][0] = *reinterpret_cast<const u32x4*>(at);
+          x[i][1] = *reinterpret_cast<const u32x4*>(at + 64);
+          f[i] = xscales[r * a.nkb + s];
+        } else {
+          x[i][0] = half(xt, 16 * i + l16, g);
+          x[i][1] = half(xt, 16 * i + l16, 4 + g);
+          f[i] = st[16 * i + l16];
+        }
       }
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) {
@@ -542,13 +604,17 @@ int64_t row_tiles(const F8Args& a) {
   return GROUPED ? std::min<int64_t>(a.M, a.M / C::BM + a.E) : (a.M + C::BM - 1) / C::BM;
 }
 
-template <class C, bool GROUPED, bool WIDE, Out OUT>
+template <class C, bool GROUPED, bool WIDE, Out OUT, In IN = In::CODES>
 hipError_t launch(const F8Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + C::BN - 1) / C::BN;   // (gated: BN / 2 columns of each half of N)
   const dim3 grid((unsigned)(row_tiles<C, GROUPED>(a) * tiles_n)), block(C::NT);
   if constexpr (C::SPLIT) {
-    const auto kernel = fp8_split_kernel<C, GROUPED, WIDE, OUT>;
-    if (C::LDS > 64 * 1024) {
+    const auto kernel = fp8_split_kernel<C, GROUPED, WIDE, OUT, IN>;
+    using S = SplitStage<C, IN>;
+    const int lds = S::lds(a.M, a.K, a.nkb);
+    constexpr int most = S::LDS + (S::ROUND ? kRounded * (1 + S::SIZE) + 16 * (128 + 16 + 8) : 0);
+    static_assert(most <= 160 * 1024, "of a compute unit");
+    if (most > 64 * 1024) {
       // the kernel's limit of dynamic LDS, raised once per device (bit d of done)
       static std::atomic<uint64_t> done{0};
       int dev = 0;
@@ -556,12 +622,12 @@ hipError_t launch(const F8Args& a, hipStream_t stream) {
       if (e != hipSuccess) return e;
       const uint64_t bit = uint64_t(1) << (dev & 63);
       if (!(done.load(std::memory_order_acquire) & bit)) {
-        e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+        e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != hipSuccess) return e;
         done.fetch_or(bit, std::memory_order_acq_rel);
       }
     }
-    hipLaunchKernelGGL(kernel, grid, block, C::LDS, stream, a);
+    hipLaunchKernelGGL(kernel, grid, block, lds, stream, a);
   } else {
     hipLaunchKernelGGL((fp8_tile_kernel<C, GROUPED, WIDE, OUT>), grid, block, 0, stream, a);
   }
@@ -645,9 +711,22 @@ hipError_t launch_any(const F8Args& a, hipStream_t stream) {
   });
 }
 
-}  // namespace
-
-namespace {
+// rows of fp32 or bf16 that the chosen form rounds itself
+template <bool WIDE, Out OUT, In IN>
+bool launch_rounded(const F8Args& a, hipStream_t stream, hipError_t& e) {
+  return with_forms<WIDE, OUT>([&](auto... form) {
+    using Fn = hipError_t (*)(const F8Args&, hipStream_t);
+    constexpr auto one = [](auto f) -> Fn {
+      using C = typename decltype(f)::C;
+      if constexpr (C::SPLIT && C::BM == 16) return launch<C, false, WIDE, OUT, IN>;
+      else return nullptr;
+    };
+    const Fn fn[] = {one(form)...};
+    const Fn f = fn[least<false, WIDE, OUT>(a, device_cu_count()).form];
+    if (f) e = f(a, stream);
+    return f != nullptr;
+  });
+}
 
 F8Args sizes(int M, int K, int N, int E) {
   F8Args a = {};
@@ -691,16 +770,31 @@ int fp8_form_name(bool y_bf16, int i, char* to, size_t n) {
 hipError_t launch_fp8_gemm(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
                            int N, const int32_t* offsets, const int32_t* rows, int M, void* Y, bool y_bf16, bool fast,
                            hipStream_t stream) {
-  const F8Args a = {X, XS, codes, scales, M, N, K, (K + 127) / 128, (N + 127) / 128, offsets, rows, E, T, Y, nullptr};
+  const F8Args a = {X, XS, codes, scales, M, N, K, (K + 127) / 128, (N + 127) / 128, offsets, rows, E, T, Y, nullptr, 0};
   if (!offsets) return y_bf16 ? launch_any<false, false, Out::BF16>(a, stream) : launch_any<false, true, Out::F32>(a, stream);
   if (fast && !y_bf16) return launch_any<true, false, Out::F32>(a, stream);
   return y_bf16 ? launch_any<true, false, Out::BF16>(a, stream) : launch_any<true, true, Out::F32>(a, stream);
 }
 
+hipError_t launch_fp8_linear(const void* X, bool x_bf16, int64_t ldx, int M, int K, const uint8_t* codes, const float* scales,
+                             int N, void* Y, bool y_bf16, uint8_t* x_codes, float* x_scales, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (M <= 16 && M * (int64_t)K <= kRounded) {
+    F8Args a = {static_cast<const uint8_t*>(X), nullptr, codes, scales, M, N, K, (K + 127) / 128, (N + 127) / 128, nullptr,
+                nullptr, 1, M, Y, nullptr, ldx};
+    if (y_bf16 ? x_bf16 ? launch_rounded<false, Out::BF16, In::BF16>(a, stream, e) : launch_rounded<false, Out::BF16, In::F32>(a, stream, e)
+               : x_bf16 ? launch_rounded<true, Out::F32, In::BF16>(a, stream, e) : launch_rounded<true, Out::F32, In::F32>(a, stream, e))
+      return e;
+  }
+  e = launch_fp8_quantize(X, x_bf16, 1, M, K, ldx, false, x_codes, x_scales, stream);
+  if (e != hipSuccess) return e;
+  return launch_fp8_gemm(x_codes, x_scales, M, K, codes, scales, 1, N, nullptr, nullptr, M, Y, y_bf16, false, stream);
+}
+
 hipError_t launch_fp8_gated(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
                             int I, const int32_t* offsets, const int32_t* rows, int M, uint8_t* h_codes, float* h_scales,
                             bool fast, hipStream_t stream) {
-  const F8Args a = {X, XS, codes, scales, M, 2 * I, K, (K + 127) / 128, I / 64, offsets, rows, E, T, h_codes, h_scales};
+  const F8Args a = {X, XS, codes, scales, M, 2 * I, K, (K + 127) / 128, I / 64, offsets, rows, E, T, h_codes, h_scales, 0};
   return fast ? launch_any<true, false, Out::GATED>(a, stream) : launch_any<true, true, Out::GATED>(a, stream);
 }
 

@@ -527,16 +527,16 @@ aq_status aq_moe_combine_backward(const void* Y, int32_t y_dtype, int64_t R, int
  * with Q the rounding to FP8 rows: aq_moe_group, aq_fp8_quantize, the product with [G_e; U_e] (gate_up [E, 2 I, K]) whose
  * result becomes FP8 rows as aq_fp8_swiglu_quantize makes them, the product with down [E, K, I], aq_moe_combine.  A
  * choice outside 0 .. E - 1 adds nothing.
- * fp32 out: both products as aq_fp8_grouped_gemm with fp32 Y.  bf16 out: both on the FP8 matrix instructions; their
+ * Both products as aq_fp8_grouped_gemm with fp32 Y; with bf16 out the second is on the FP8 matrix instructions.  Their
  * results stay fp32, and out is rounded once.
  * products [T top, K]: D_e's results, a choice's in row slots[t, j] (rows of choices outside the experts: not written),
  * which aq_moe_combine_backward takes for the weights' gradient.
  * X [T, K] fp32 or bf16, rows ldx elements apart; ids [T, top] int32, weights [T, top] fp32, slots [T, top] int32, out
- * [T, K].  workspace: aq_fp8_experts_workspace(T, top, K, E, I, out_dtype) bytes of device memory, 16-byte aligned, used
+ * [T, K].  workspace: aq_fp8_experts_workspace(T, top, K, E, I) bytes of device memory, 16-byte aligned, used
  * only during the call (0 for sizes that the call refuses).
  * Errors: as the calls that it is made of; 2 I below 2^22; T * top below 2^30.
  */
-size_t aq_fp8_experts_workspace(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I, int32_t out_dtype);
+size_t aq_fp8_experts_workspace(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I);
 aq_status aq_fp8_experts(const void* X, int32_t x_dtype, int64_t T, int64_t K, int64_t ldx, const uint8_t* gate_up,
                          const float* gate_up_scales, const uint8_t* down, const float* down_scales, int64_t E, int64_t I,
                          const int32_t* ids, const float* weights, int64_t top, float* products, int32_t* slots, void* out,

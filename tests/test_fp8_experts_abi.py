@@ -43,11 +43,11 @@ def test_workspace(lib):
     up = lambda n: -(-n // 256) * 256
     t, top, k, e, i = 5, 3, 272, 9, 144
     base = up(4 * (e + 1)) + up(4 * t * top) + up(t * k) + up(4 * t * 3) + up(t * top * i) + up(4 * t * top * 2)
-    assert f(t, top, k, e, i, 0) == f(t, top, k, e, i, 1) == base + up(8 * t * top * i)
-    assert f(2048, 8, 2048, 64, 1408, 1) < f(2048, 8, 2048, 64, 1424, 1) - 16384 * 2 * 1408 * 4
+    assert f(t, top, k, e, i) == base + up(8 * t * top * i)
+    assert f(2048, 8, 2048, 64, 1408) < f(2048, 8, 2048, 64, 1424) - 16384 * 2 * 1408 * 4
     for bad in ((0, 2, 64, 8, 64), (-1, 2, 64, 8, 64), (4, 0, 64, 8, 64), (4, 2, 60, 8, 64), (4, 2, 64, 0, 64), (4, 2, 64, 2000, 64), (4, 2, 64, 8, 8)):
-        assert f(*bad, 0) == 0
-    assert f(1 << 40, 1 << 40, 1 << 40, 1 << 40, 1 << 40, 0) == 0
+        assert f(*bad) == 0
+    assert f(1 << 40, 1 << 40, 1 << 40, 1 << 40, 1 << 40) == 0
 
 
 def test_binding_refusals():

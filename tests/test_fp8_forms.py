@@ -21,18 +21,17 @@ def test_sizes_select_their_form(lib, bf16, grouped, name):
 
 
 def test_gated_sizes_select_their_form(lib):
-    assert {form for _, form in GATED} == {-1, 0, 1}
-    for (fast, form), sizes in GATED.items():
+    assert set(GATED) == {-1, 0, 1}
+    for form, sizes in GATED.items():
         assert len(sizes) >= 2
         for t, top, e, k, inner in sizes:
-            assert lib.fp8_gated_form(fast, t * top, k, inner, e, CUS) == form, (t, top, e, k, inner)
+            assert lib.fp8_gated_form(t * top, k, inner, e, CUS) == form, (t, top, e, k, inner)
 
 
 def test_gated_activation_alone_where_it_has_to_be(lib):
     """A last block of h that is not whole, and an expert's weights past 32 bits of offset."""
-    for fast in (False, True):
-        assert lib.fp8_gated_form(fast, 16384, 2048, 1408, 64, CUS) >= 0 > lib.fp8_gated_form(fast, 16384, 2048, 1424, 64, CUS)
-        assert all(lib.fp8_gated_form(fast, 1 << i, 1 << 15, 1 << 16, 2, CUS) < 0 for i in range(20))
+    assert lib.fp8_gated_form(16384, 2048, 1408, 64, CUS) >= 0 > lib.fp8_gated_form(16384, 2048, 1424, 64, CUS)
+    assert all(lib.fp8_gated_form(1 << i, 1 << 15, 1 << 16, 2, CUS) < 0 for i in range(20))
 
 
 def test_rounded_sizes_select_their_form(lib):

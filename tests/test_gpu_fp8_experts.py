@@ -50,12 +50,12 @@ def _apart(x, gu, down, ids, weights, out):
     return B.aq_moe_combine(y, slots, weights, out), y, slots
 
 
-@pytest.mark.parametrize("fast,form", list(GATED))
-def test_forms(lib, fast, form):
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("form", list(GATED))
+def test_forms(lib, form, out):
     from weight_only_bit_group_amd import binding as B
-    out = BF16 if fast else F32
-    for t, top, e, k, inner in GATED[fast, form]:
-        step(f"experts {'bf16' if fast else 'fp32'} form {form}: t {t} top {top} e {e} k {k} inner {inner}")
+    for t, top, e, k, inner in GATED[form]:
+        step(f"experts {out} form {form}: t {t} top {top} e {e} k {k} inner {inner}")
         args = _inputs(t, top, e, k, inner)
         ref, ry, rslots = _apart(*args, out)
         x, gu, down, ids, weights = args
@@ -74,7 +74,7 @@ def test_fills_nothing_else(out, inner):
     t, top, e, k = 37, 3, 5, 272
     x, gu, down, ids, weights = _inputs(t, top, e, k, inner)
     ids[5:9] = -1
-    need = B.aq_fp8_experts_workspace(t, top, k, e, inner, out)
+    need = B.aq_fp8_experts_workspace(t, top, k, e, inner)
     work = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
     step(f"experts {out} with guards, inner {inner}")
     got, y, slots = B.aq_fp8_experts(x, *gu, *down, ids, weights, out, workspace=work[256:256 + need])

@@ -56,7 +56,7 @@ SIGNATURES = {
     "aq_moe_group_workspace": (_SZ, [_I64, _I64, _I64]),
     "aq_moe_group": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
     "aq_moe_combine": (_I32, [_P, _I32, _I64, _I64, _P, _P, _I64, _I64, _P, _I32, _P]),
-    "aq_fp8_experts_workspace": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I32]),
+    "aq_fp8_experts_workspace": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
     "aq_fp8_experts": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _I32, _P,
                               _SZ, _P]),
     "aq_moe_combine_backward": (_I32, [_P, _I32, _I64, _I64, _P, _I64, _I64, _P, _I32, _P, _P]),

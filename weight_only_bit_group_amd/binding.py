@@ -761,8 +761,8 @@ def aq_fp8_swiglu_quantize(H, end=None, *, codes=None, scales=None):
     return codes, scales
 
 
-def aq_fp8_experts_workspace(T: int, top: int, K: int, E: int, I: int, out_dtype=torch.float32) -> int:
-    return int(_lib.load().aq_fp8_experts_workspace(T, top, K, E, I, _MX_OUT[out_dtype]))
+def aq_fp8_experts_workspace(T: int, top: int, K: int, E: int, I: int) -> int:
+    return int(_lib.load().aq_fp8_experts_workspace(T, top, K, E, I))
 
 
 def aq_fp8_experts(X, gate_up_codes, gate_up_scales, down_codes, down_scales, ids, weights, out_dtype=None, workspace=None):
@@ -770,8 +770,8 @@ def aq_fp8_experts(X, gate_up_codes, gate_up_scales, down_codes, down_scales, id
 
     out[t] = sum_j weights[t, j] D_e Q(silu(G_e Q(x[t])) * U_e Q(x[t])) for the experts e = ids[t, j] (int32; others than
     0 .. E - 1 add nothing), Q the rounding to FP8 rows.  gate_up [E, 2I, K] and down [E, K, I] as codes and scales in
-    128 x 128 blocks; X f32 or bf16, its rows may be strided; weights f32; out float32, or bfloat16 with the products
-    on the FP8 matrix instructions.  products holds a choice's result in row slots[t, j] (not written for a choice
+    128 x 128 blocks; X f32 or bf16, its rows may be strided; weights f32; out float32, or bfloat16 with the second
+    product on the FP8 matrix instructions.  products holds a choice's result in row slots[t, j] (not written for a choice
     without an expert), as aq_moe_combine and its gradient take them.
     workspace: None allocates it; a uint8 device tensor is used as given.
     """
@@ -791,7 +791,7 @@ def aq_fp8_experts(X, gate_up_codes, gate_up_scales, down_codes, down_scales, id
     _mx_need(weights, "weights", torch.float32, (t, top), dev)
     out, code = _mx_out(None, t, k, out_dtype, X, dev)
     products, slots = X.new_empty((t * top, k), dtype=torch.float32), torch.empty_like(ids)
-    workspace = _f8_workspace(workspace, aq_fp8_experts_workspace(t, top, k, e, n // 2, out.dtype), X, dev)
+    workspace = _f8_workspace(workspace, aq_fp8_experts_workspace(t, top, k, e, n // 2), X, dev)
     _mx_call("aq_fp8_experts", dev, X.data_ptr(), _MX_OUT[X.dtype], t, k, ld, gate_up_codes.data_ptr(),
              gate_up_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), e, n // 2, ids.data_ptr(),
              weights.data_ptr(), top, products.data_ptr(), slots.data_ptr(), out.data_ptr(), code, workspace.data_ptr(),

@@ -941,9 +941,9 @@ namespace {
 struct ExpertsParts {
   bool fused;
   size_t offsets, rows, group, x_codes, x_scales, h_codes, h_scales, h, bytes;
-  ExpertsParts(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I, bool fast) {
+  ExpertsParts(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I) {
     const int64_t C = T * top;
-    fused = aq::fp8_gated_fused(fast, (int)C, (int)K, (int)I, (int)E);
+    fused = aq::fp8_gated_fused((int)C, (int)K, (int)I, (int)E);
     size_t at = 0;
     auto part = [&at](size_t n) {
       const size_t here = at;
@@ -972,8 +972,8 @@ bool experts_sizes(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I) {
 
 }  // namespace
 
-size_t aq_fp8_experts_workspace(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I, int32_t out_dtype) {
-  return experts_sizes(T, top, K, E, I) ? ExpertsParts(T, top, K, E, I, out_dtype == AQ_BF16).bytes : 0;
+size_t aq_fp8_experts_workspace(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I) {
+  return experts_sizes(T, top, K, E, I) ? ExpertsParts(T, top, K, E, I).bytes : 0;
 }
 
 aq_status aq_fp8_experts(const void* X, int32_t x_dtype, int64_t T, int64_t K, int64_t ldx, const uint8_t* gate_up,
@@ -1005,13 +1005,13 @@ aq_status aq_fp8_experts(const void* X, int32_t x_dtype, int64_t T, int64_t K, i
     AQ_PTR(slots, 4, "slots");
     AQ_PTR(out, 16, "out");
     AQ_PTR(workspace, 16, "workspace");
-    const size_t need = aq_fp8_experts_workspace(T, top, K, E, I, out_dtype);
+    const size_t need = aq_fp8_experts_workspace(T, top, K, E, I);
     AQ_REQUIRE(workspace_bytes >= need, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
   }
   if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
   if (T == 0) return ok();
   const bool fast = out_dtype == AQ_BF16;
-  const ExpertsParts at(T, top, K, E, I, fast);
+  const ExpertsParts at(T, top, K, E, I);
   auto* const base = static_cast<uint8_t*>(workspace);
   auto* const offsets = reinterpret_cast<int32_t*>(base + at.offsets);
   auto* const rows = reinterpret_cast<int32_t*>(base + at.rows);
@@ -1028,11 +1028,11 @@ aq_status aq_fp8_experts(const void* X, int32_t x_dtype, int64_t T, int64_t K, i
   if (at.fused) {
     if (e == hipSuccess)
       e = aq::launch_fp8_gated(x_codes, x_scales, (int)T, (int)K, gate_up, gate_up_scales, (int)E, (int)I, offsets, rows, C,
-                               h_codes, h_scales, fast, on);
+                               h_codes, h_scales, on);
   } else {
     if (e == hipSuccess)
       e = aq::launch_fp8_gemm(x_codes, x_scales, (int)T, (int)K, gate_up, gate_up_scales, (int)E, (int)(2 * I), offsets,
-                              rows, C, h, false, fast, on);
+                              rows, C, h, false, false, on);
     if (e == hipSuccess) e = aq::launch_fp8_swiglu_quantize(h, false, C, (int)I, offsets + E, h_codes, h_scales, on);
   }
   if (e == hipSuccess)

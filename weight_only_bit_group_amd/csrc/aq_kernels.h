@@ -94,13 +94,13 @@ hipError_t launch_fp8_linear(const void* X, bool x_bf16, int64_t ldx, int M, int
 extern "C" int fp8_form(bool y_bf16, bool grouped, int M, int K, int N, int E, int cus);
 extern "C" int fp8_form_name(bool y_bf16, int form, char* to, size_t n);
 // (of the product with the gated activation: negative where the activation is a kernel of its own)
-extern "C" int fp8_gated_form(bool fast, int M, int K, int I, int E, int cus);
+extern "C" int fp8_gated_form(int M, int K, int I, int E, int cus);
 // The first product of an expert's gated MLP with its activation: h = silu(g) u of [g | u] = X times weights [E, 2 I, K]
-// by expert, rounded to FP8 rows (codes [M, I], scales [M, I / 128]); where fp8_gated_fused holds.
-bool fp8_gated_fused(bool fast, int M, int K, int I, int E);
+// by expert with fp32 sums, rounded to FP8 rows (codes [M, I], scales [M, I / 128]); where fp8_gated_fused holds.
+bool fp8_gated_fused(int M, int K, int I, int E);
 hipError_t launch_fp8_gated(const uint8_t* X, const float* XS, int T, int K, const uint8_t* codes, const float* scales, int E,
                             int I, const int32_t* offsets, const int32_t* rows, int M, uint8_t* h_codes, float* h_scales,
-                            bool fast, hipStream_t stream);
+                            hipStream_t stream);
 // Routing: T tokens, rows of logits ld elements apart
 struct RouteArgs {
   const void* logits;

@@ -597,7 +597,7 @@ PyObject* experts(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   if (!weights) Py_RETURN_NONE;
   Output y;
   if (!y.make(args[7], Py_None, x.m, x.k, device)) Py_RETURN_NONE;
-  const size_t need = aq_fp8_experts_workspace(x.m, top, x.k, up.e, inner, y.dtype);
+  const size_t need = aq_fp8_experts_workspace(x.m, top, x.k, up.e, inner);
   if (need == 0) Py_RETURN_NONE;
   at::Tensor products = fresh({x.m * top, x.k}, F32, device), slots = fresh({x.m, top}, I32, device);
   at::Tensor workspace = fresh({(int64_t)need}, U8, device);

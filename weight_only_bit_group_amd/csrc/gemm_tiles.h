@@ -46,13 +46,13 @@ struct Tile {
   int n0;
 };
 
-// Tile t of a grouped launch: the experts' rows cut into pieces of BM, each times the
-// column tiles, the columns fastest.  The launch has at least as many blocks as tiles;
-// blocks past them get false.  Every wave scans the offsets by itself, 64 experts at a
+// Tile `block` of a grouped product: the experts' rows cut into pieces of BM, each times the
+// column tiles, the columns fastest.  `most` is the host's bound of their number, ntiles becomes the number;
+// tiles past it get false.  Every wave scans the offsets by itself, 64 experts at a
 // time.  Offsets are clamped to the rows of Y and an expert's end to its start, so no value of
 // theirs leads outside the buffers.
 template <int BM, class Args>
-__device__ __forceinline__ bool grouped_tile(const Args& a, int tiles_n, int bn, int block, Tile& out) {
+__device__ __forceinline__ bool grouped_tile(const Args& a, int tiles_n, int bn, int block, Tile& out, int64_t most, int& ntiles) {
   const int lane = threadIdx.x & 63;
   auto span = [&](int e, int& lo, int& hi) {
     lo = hi = 0;
@@ -75,8 +75,8 @@ __device__ __forceinline__ bool grouped_tile(const Args& a, int tiles_n, int bn,
     incl = scan((hi - lo + BM - 1) / BM);
     total += __shfl(incl, 63, 64);
   }
-  // (no more than the launch has blocks, unless overlapping offsets count rows twice)
-  const int ntiles = (int)min((int64_t)total * tiles_n, (int64_t)gridDim.x);
+  // (no more than `most`, unless overlapping offsets count rows twice)
+  ntiles = __builtin_amdgcn_readfirstlane((int)min((int64_t)total * tiles_n, most));
   if (block >= ntiles) return false;
   const int t = tile_of_block(block, ntiles);
   const int mt = t / tiles_n;
@@ -100,6 +100,13 @@ __device__ __forceinline__ bool grouped_tile(const Args& a, int tiles_n, int bn,
     base += __shfl(incl, 63, 64);
   }
   return false;
+}
+
+// the tile of this block, in a launch with a block for every tile
+template <int BM, class Args>
+__device__ __forceinline__ bool grouped_tile(const Args& a, int tiles_n, int bn, int block, Tile& out) {
+  int ntiles;
+  return grouped_tile<BM>(a, tiles_n, bn, block, out, (int64_t)gridDim.x, ntiles);
 }
 
 // The activation row that row r of Y reads; -1 (and the address of row 0) for a listed row

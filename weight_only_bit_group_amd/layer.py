@@ -525,8 +525,8 @@ class FP8Experts(torch.nn.Module):
     expert of another rank) adds nothing.  Both layers run as one product grouped by expert each, without reading a
     count back to the host, so a call may be captured into a graph whose replays follow x, ids and weights.  A token's
     products are added in the order of its choices, in fp32.  The output is out_dtype: float32 with sums in fp32
-    throughout, or bfloat16 on the FP8 matrix instructions.  weights are differentiable, the experts are not: an error
-    when x's gradient is asked for.
+    throughout, or bfloat16 with the second product on the FP8 matrix instructions.  weights are differentiable, the
+    experts are not: an error when x's gradient is asked for.
     """
 
     def __init__(self, gate_up_codes: torch.Tensor, gate_up_scales: torch.Tensor, down_codes: torch.Tensor,

@@ -361,6 +361,11 @@ __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
 // ---- tiles ----------------------------------------------------------------------------------
 // WM x WN waves, each (16 FM) activation rows x (16 FN) weight rows.  K advances in stages of one block, 128 bytes of
 // a row, through two LDS buffers filled by LDS-DMA.
+//   M = 4096 on [11008, 2048], bf16 out: 103 to 115 us, 1.6 to 1.8 PFLOP/s (a library product of FP8 with one scale a
+// tensor 101); K = 14336 on 4096 columns 230 us, 2.1.  There the matrix cores work 48% of the loop's cycles: a stage of a
+// 256 x 256 tile has 2048 cycles of matrix instructions on a SIMD and takes 4290, a third of them waiting for the
+// hand-over; four fused multiply-adds follow every instruction, and 64 KB of a stage come from the L2 and LDS alike.
+// fp32 out: 0.9 PFLOP/s, the codes' conversion (16 instructions an operand) beside four matrix instructions a product.
 template <int WM_, int WN_, int FM_, int FN_>
 struct F8Cfg {
   static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_;
@@ -729,15 +734,17 @@ hipError_t launch(const F8Args& a, hipStream_t stream) {
 // The form of a product: the one whose estimated time is the least,
 //   fixed + r (round + stage * stages of a wave) + mb * (MB through LDS-DMA)     [us]
 // with r = the tiles over those that the device holds at once, at least 1: a block takes its run of stages whether or
-// not others run beside it, and every tile adds its traffic.  The four figures of a form are least-squares fits of the
-// relative error, its best cases weighted most, to graph-replayed times of 193 products (M = 1 to 4096 on weights of
-// 512 to 14336 rows and columns, drawn ones of M to 4096, N to 14336 and K to 14336, to 128 experts with 1 to 32768
-// rows) of 14 forms.  The forms kept lose 1% of geometric-mean time against the best of all, the estimates' choice of
-// them 3% (bf16 out) and 5% (fp32 out), 1.4 times at worst.  Both sides, graph-replayed, us:
-//   M = 1 on [11008, 2048], fp32 out: 16 x 64 over 8 waves 7.2, 16 x 16 over 4 waves 8.6, tiles of 64 x 128 16.3
-//   M = 16 on [4096, 14336], fp32 out: 16 x 16 over 16 waves 16.2, 16 x 64 over 8 waves 28.8, tiles of 64 x 128 98.9
-//   M = 128 on [11008, 2048], bf16 out: tiles of 64 x 128 18, of 128 x 128 20, 32 x 64 over 4 waves 22
-//   M = 4096 there: tiles of 256 x 256 136, of 128 x 128 142
+// not others run beside it, and every tile adds its traffic.  The four figures of a form are fitted to graph-replayed
+// times of 423 products (1 to 16384 rows on weights of 512 to 14336 rows and columns, drawn ones of 64 to 14336, up to
+// 128 experts with 1 to 32768 rows): least squares of the relative error, then the choice's loss against the best form
+// in the geometric mean, which is 1.1% (bf16 out) and 1.3% (fp32 out) and at worst 1.28 times.  Forms without which that
+// mean would be 0.5% higher at most were left out.  Both sides, us:
+//   M = 1 on [11008, 2048], fp32 out: 16 x 64 over 8 waves 7.3, 16 x 16 over 4 waves 8.6, tiles of 32 x 128 17.8
+//   M = 16 on [4096, 14336], fp32 out: 16 x 16 over 16 waves 16.5, 16 x 32 over 8 waves 20.8, 16 x 64 over 8 waves 28.7
+//   M = 32 there, bf16 out: 16 x 32 over 8 waves 20.0, 16 x 16 over 16 waves 25.2, 16 x 64 over 8 waves 26.9
+//   M = 128 on [11008, 2048], bf16 out: 32 x 64 over 4 waves 14.5, tiles of 32 x 128 19.2, of 128 x 128 22.1
+//   M = 4096 there: tiles of 256 x 256 114.8, of 128 x 128 142.7, of 32 x 128 232.1; fp32 out 265.7, 215.4, 296.9
+//   64 x 8 rows of 128 experts [2048, 1024]: tiles of 32 x 128 52.6, 32 x 64 over 4 waves 54.9, tiles of 128 x 128 63.2
 struct F8Cost {
   float fixed, round, stage, mb;
 };
@@ -768,14 +775,16 @@ auto with_forms(F f) {
   if constexpr (OUT == Out::GATED)
     return f(F8Form<F8Cfg<1, 4, 2, 4>>{{3.531f, 2.168f, 0.933f, 0.053f}}, F8Form<F8Cfg<2, 4, 4, 4>>{{2.818f, 7.496f, 1.926f, 0.024f}});
   else if constexpr (!WIDE)
-    return f(F8Form<F8Split<1, 1, 16, 1>>{{1.144f, 2.701f, 0.310f, 0.082f}}, F8Form<F8Split<1, 1, 4, 4>>{{2.185f, 1.201f, 0.275f, 0.070f}},
-             F8Form<F8Split<1, 4, 8, 1>>{{1.447f, 2.494f, 0.756f, 0.042f}}, F8Form<F8Split<2, 4, 4, 1>>{{1.948f, 1.763f, 0.705f, 0.060f}},
-             F8Form<F8Cfg<1, 4, 2, 2>>{{1.714f, 2.462f, 0.405f, 0.056f}}, F8Form<F8Cfg<2, 2, 4, 4>>{{0.142f, 4.853f, 0.839f, 0.046f}},
-             F8Form<F8Cfg<2, 4, 8, 4>>{{1.263f, 9.229f, 1.291f, 0.056f}});
+    return f(F8Form<F8Split<1, 1, 16, 1>>{{0.569f, 2.548f, 0.336f, 0.070f}}, F8Form<F8Split<1, 1, 4, 4>>{{1.913f, 0.985f, 0.194f, 0.085f}},
+             F8Form<F8Split<1, 2, 8, 2>>{{0.998f, 1.896f, 0.628f, 0.036f}}, F8Form<F8Split<1, 4, 8, 1>>{{0.416f, 2.539f, 0.968f, 0.031f}},
+             F8Form<F8Split<2, 2, 8, 2>>{{1.051f, 2.018f, 0.814f, 0.038f}}, F8Form<F8Split<2, 4, 4, 1>>{{1.640f, 1.548f, 0.786f, 0.056f}},
+             F8Form<F8Cfg<1, 4, 2, 2>>{{1.509f, 1.923f, 0.578f, 0.039f}}, F8Form<F8Cfg<2, 2, 4, 4>>{{0.923f, 3.869f, 0.739f, 0.065f}},
+             F8Form<F8Cfg<2, 4, 8, 4>>{{0.907f, 6.838f, 1.538f, 0.046f}});
   else
-    return f(F8Form<F8Split<1, 1, 16, 1>>{{3.323f, 0.238f, 0.778f, 0.051f}}, F8Form<F8Split<1, 1, 4, 4>>{{2.142f, 1.259f, 0.286f, 0.068f}},
-             F8Form<F8Split<1, 4, 8, 1>>{{1.772f, 1.231f, 0.832f, 0.065f}}, F8Form<F8Split<2, 4, 4, 1>>{{1.012f, 2.623f, 0.772f, 0.052f}},
-             F8Form<F8Cfg<1, 4, 2, 2>>{{0.107f, 3.327f, 0.529f, 0.059f}}, F8Form<F8Cfg<2, 2, 4, 4>>{{4.368f, 4.886f, 0.632f, 0.105f}});
+    return f(F8Form<F8Split<1, 1, 16, 1>>{{3.406f, 0.455f, 0.459f, 0.053f}}, F8Form<F8Split<1, 1, 4, 4>>{{1.993f, 1.124f, 0.361f, 0.054f}},
+             F8Form<F8Split<1, 2, 8, 2>>{{1.874f, 1.704f, 0.592f, 0.041f}}, F8Form<F8Split<1, 4, 8, 1>>{{1.992f, 1.572f, 0.974f, 0.040f}},
+             F8Form<F8Split<2, 2, 8, 2>>{{2.013f, 1.914f, 0.749f, 0.046f}}, F8Form<F8Split<2, 4, 4, 1>>{{1.122f, 2.074f, 0.786f, 0.050f}},
+             F8Form<F8Cfg<1, 4, 2, 2>>{{0.056f, 2.847f, 0.659f, 0.045f}}, F8Form<F8Cfg<2, 2, 4, 4>>{{3.308f, 2.320f, 0.961f, 0.086f}});
 }
 
 // the index of the form that the product takes on a device of `cus` compute units, and its estimated time

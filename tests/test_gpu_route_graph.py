@@ -1,4 +1,6 @@
 """route's gradient as a part of torch's graph: the native node and the Python function give the same, and both keep its rules."""
+import gc
+
 import pytest
 import torch
 
@@ -14,7 +16,12 @@ def _gpu(lib):
 
 
 class _Refuses:
+    """Stands for the native module: calls go through Python; it still tells what a capture meets."""
+
     def __getattr__(self, name):
+        if name == "capture_conflict":
+            from weight_only_bit_group_amd import _aq_torch
+            return _aq_torch.capture_conflict
         return lambda *a: None
 
 
@@ -158,6 +165,38 @@ def test_backward_captured_and_replayed(route):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, call()))
+
+
+def test_capture_beside_a_living_graph_is_refused(route):
+    """Leaves whose earlier graph lives on another stream: refused when the call is made, before anything is recorded."""
+    from weight_only_bit_group_amd import layer
+    l = _logits(20, 32).requires_grad_()
+    m = layer.FP8Experts.from_weights(torch.randn(4, 64, 32, device="cuda"), torch.randn(4, 32, 32, device="cuda"))
+    x, ids, w = torch.randn(20, 32, device="cuda"), torch.randint(0, 4, (20, 2), device="cuda"), torch.rand(20, 2, device="cuda").requires_grad_()
+    alive = [route(l, 2)[1], route(l * 2.0, 2)[1], m(x, ids, w)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda: route(l, 2), lambda: route(l * 2.0, 2), lambda: m(x, ids, w), lambda: m(x, ids, w * 0.5)):
+        g = torch.cuda.CUDAGraph()
+        with pytest.raises(RuntimeError, match="earlier call"):
+            with torch.cuda.graph(g, stream=side):
+                x.add_(0.0)   # (a graph of something)
+                call()
+    alive[0].sum().backward()
+    del alive, call
+    l.grad = w.grad = None
+    gc.collect()   # (the refused calls' exceptions hold their frames, and these the graphs)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):   # (let go: captured)
+        out = torch.autograd.grad(route(l, 2)[1].square().sum(), l)[0], torch.autograd.grad(m(x, ids, w).square().sum(), w)[0]
+    ref = torch.autograd.grad(route(l, 2)[1].square().sum(), l)[0], torch.autograd.grad(m(x, ids, w).square().sum(), w)[0]
+    for _ in range(3):
+        for o in out:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
 
 
 def test_backward_of_threads_at_once(route):

@@ -348,7 +348,7 @@ class _MxNative:
     def __getattr__(self, name):
         if name not in ("quantize", "dequantize", "gemm", "gemm_a4", "grouped_gemm", "grouped_gemm_a4", "fp8_quantize",
                         "fp8_dequantize", "fp8_gemm", "fp8_grouped_gemm", "fp8_linear", "fp8_experts", "route",
-                        "route_graph", "route_backward"):
+                        "route_graph", "capture_conflict", "route_backward"):
             raise AttributeError(name)
         _lib.load()
         from . import _aq_torch   # an ImportError here: the module has not been built
@@ -855,6 +855,12 @@ def moe_route_graph(logits, top: int, bias, score: str, groups: int, top_groups,
     """aq_moe_route's result, the weights part of the graph where the logits are, or None where the native module does
     not make the call."""
     return _mx.route_graph(logits, top, score, bias, groups, top_groups, renormalize, scale)
+
+
+def capture_conflict(t) -> bool:
+    """Whether the current stream is being captured and t's graph reaches a leaf that a graph of an earlier call, on another
+    stream, holds: the backward pass could not be captured."""
+    return bool(_mx.capture_conflict(t))
 
 
 def aq_moe_route_backward(logits, ids, weights, dweights, *, score: str = "softmax", renormalize: bool = True,

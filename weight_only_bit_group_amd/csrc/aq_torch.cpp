@@ -16,12 +16,17 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/saved_variable.h>
 
+#include <hip/hip_runtime_api.h>
+
 #include <algorithm>
+#include <unordered_set>
+#include <vector>
 
 #include "aq.h"
 
@@ -489,6 +494,39 @@ PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// Whether the current stream is being captured while a leaf that t was computed from belongs to a graph of an earlier
+// call on another stream.  Its node accumulates on that stream: a captured backward pass would send work there, which
+// breaks the capture in a thread of torch's engine.
+bool capture_conflict(const at::Tensor& t, int device) {
+  if (!at::GradMode::is_enabled() || !t.requires_grad()) return false;
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  const auto stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)device);
+  if (hipStreamIsCapturing(stream.stream(), &status) != hipSuccess || status == hipStreamCaptureStatusNone) return false;
+  std::vector<std::shared_ptr<torch::autograd::Node>> open;
+  if (auto leaf = t.grad_fn() ? t.grad_fn() : torch::autograd::impl::try_get_grad_accumulator(t)) open.push_back(leaf);
+  std::unordered_set<torch::autograd::Node*> seen;
+  while (!open.empty()) {
+    const auto node = open.back();
+    open.pop_back();
+    if (!seen.insert(node.get()).second) continue;
+    if (dynamic_cast<torch::autograd::AccumulateGrad*>(node.get())) {
+      const auto on = node->stream();
+      if (on && on->id() != stream.id()) return true;   // (the device type's name differs: only the numbers compare)
+    }
+    for (const auto& edge : node->next_edges())
+      if (edge.function) open.push_back(edge.function);
+  }
+  return false;
+}
+
+// tensor -> bool
+PyObject* conflict(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  const int device = nargs == 1 ? device_for(args[0]) : -1;
+  return PyBool_FromLong(device >= 0 && capture_conflict(THPVariable_Unpack(args[0]), device));
+  END_HANDLE_TH_ERRORS
+}
+
 // The gradient of route's weights with respect to the logits, as a node of torch's graph (from Python, applying the
 // function and going back through it take 30 us of the host more).
 struct RouteBackward : public torch::autograd::Node {
@@ -536,7 +574,8 @@ PyObject* route_graph(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   const int device = device_for(args[0]);
   if (device < 0) Py_RETURN_NONE;
   Routing r;
-  if (!r.read(args, device) || !r.run(device)) Py_RETURN_NONE;
+  // (a conflict is the caller's to report)
+  if (!r.read(args, device) || capture_conflict(*r.l.x, device) || !r.run(device)) Py_RETURN_NONE;
   if (at::GradMode::is_enabled() && r.l.x->requires_grad()) {
     auto node = std::shared_ptr<RouteBackward>(new RouteBackward(), torch::autograd::deleteNode);
     node->set_next_edges(torch::autograd::collect_next_edges(*r.l.x));
@@ -632,6 +671,7 @@ PyMethodDef methods[] = {{"quantize", AQ_FAST(quantize)},
                          {"fp8_experts", AQ_FAST(experts)},
                          {"route", AQ_FAST(route)},
                          {"route_graph", AQ_FAST(route_graph)},
+                         {"capture_conflict", AQ_FAST(conflict)},
                          {"route_backward", AQ_FAST(route_backward)},
                          {nullptr, nullptr, 0, nullptr}};
 

@@ -446,6 +446,12 @@ class FP8Linear(torch.nn.Module):
         return f"in_features={self.in_features}, out_features={self.out_features}, weights=fp8"
 
 
+def _capturable(name: str, t: torch.Tensor) -> None:
+    if B.capture_conflict(t):
+        raise RuntimeError(f"{name}: a graph of an earlier call with the same leaves is alive on another stream; let it go "
+                           "before its backward pass is captured, or run it on the capturing stream")
+
+
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top, bias, how):
@@ -469,7 +475,8 @@ def route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, scor
           top_groups: int | None = None, renormalize: bool = True, scale: float = 1.0):
     """(ids [.., top] int32, weights [.., top] float32) of a router's logits [.., E], as FP8Experts and MXFP4Experts take
     them; see ``binding.aq_moe_route`` for the arguments.  weights are differentiable with respect to the logits, the
-    choice is not, and the bias (which only balances the choice) gets no gradient."""
+    choice is not, and the bias (which only balances the choice) gets no gradient.  A call and its backward pass may be
+    captured; an error where a graph of an earlier call with the same leaves still lives on another stream."""
     if logits.is_cuda:
         pair = B.moe_route_graph(logits, top, bias, score, groups, top_groups, renormalize, scale)
         if pair is not None:
@@ -483,6 +490,7 @@ def route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, scor
     bias = None if bias is None else bias.detach().float().contiguous()
     how = dict(score=score, groups=groups, top_groups=top_groups, renormalize=renormalize, scale=scale)
     if torch.is_grad_enabled() and l2.requires_grad:
+        _capturable("route", l2)
         ids, weights = _Route.apply(l2, top, bias, how)
     else:
         ids, weights = B.aq_moe_route(l2, top, bias=bias, **how)
@@ -570,6 +578,7 @@ class FP8Experts(torch.nn.Module):
         ids = ids.reshape(-1, top).contiguous()
         w = weights.reshape(-1, top).float().contiguous()
         if torch.is_grad_enabled() and (w.requires_grad or x2.requires_grad):
+            _capturable("FP8Experts", w)
             out = _Experts.apply(x2, w, ids, self)
         else:
             out = self._call(x2, ids, w)[0]

@@ -1,6 +1,7 @@
 /*
  * libaq -- group-wise INT4 (W4A16) weight quantization, AWQ calibration, an FP4
- * decode path and MXFP4 products for AMD Instinct MI355X (gfx950).  C ABI.
+ * decode path, MXFP4 and FP8 products and routing to experts for AMD Instinct
+ * MI355X (gfx950).  C ABI.
  *
  * Conventions shared by every entry point
  *   - Tensor arguments are DEVICE pointers owned by the caller (the library

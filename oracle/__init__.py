@@ -17,6 +17,9 @@ Modules
   awq    candidate channel scales and the exhaustive alpha-grid MSE search
   fp4    E2M1 / E4M3 decoding, the FP4 forward reference, and an encoder used
          only to build realistic FP4 inputs
+  mxfp4  blocks of 32 E2M1 codes: quantiser, decoding, the forward references
+  fp8    E4M3 blocks of 128: quantiser, decoding, the forward references
+  moe    routing to experts and its gradient, choices grouped by expert
 
 Parity pins: every function is pinned in ``tests/test_oracle_*.py`` against
 closed forms, exhaustive or brute-force enumeration and the pages' own

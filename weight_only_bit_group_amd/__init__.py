@@ -1,4 +1,5 @@
-"""weight_only_bit_group_amd -- group-wise INT4 (W4A16), AWQ calibration, FP4 decode and MXFP4 products on MI355X.
+"""weight_only_bit_group_amd -- group-wise INT4 (W4A16), AWQ calibration, FP4 decode, MXFP4 and FP8 products and routing to
+experts on MI355X.
 
 The compute lives in libaq.so (hand-written HIP kernels for gfx950 behind the C
 ABI of include/aq.h).  ``binding`` exposes the entry points to torch under the

@@ -124,3 +124,18 @@ def test_large_activations_overflow_to_nan_alone():
     assert B.aq_fp8_experts(*args[:1], *args[1], *down, ids, weights, F32)[0].isnan().any(1).all()
     ref = _apart(*args, F32)[0]
     assert torch.equal(torch.nan_to_num(B.aq_fp8_experts(x, *args[1], *down, ids, weights, F32)[0], 5.0), torch.nan_to_num(ref, 5.0))
+
+
+@pytest.mark.parametrize("t,top,e", [(1, 1, 1), (3, 7, 1024), (40, 6, 600), (1024, 16, 700), (2048, 8, 300), (2049, 8, 5), (5000, 4, 1024)])
+def test_grouping_beside_the_rounding(t, top, e):
+    """Choices of one expert to 1024, with one workgroup (up to 16384 choices) and with three kernels behind it; fp32 rows apart."""
+    from weight_only_bit_group_amd import binding as B
+    k, inner = 144, 32
+    x, gu, down, ids, weights = _inputs(t, top, e, k, inner)
+    step(f"experts: {t} tokens of {top} choices of {e}")
+    ref, _, rslots = _apart(x, gu, down, ids, weights, F32)
+    wide = torch.full((t, k + 20), float("nan"), device="cuda")
+    wide[:, :k] = x.float()
+    for rows in (x, wide[:, :k]):
+        got, _, slots = B.aq_fp8_experts(rows, *gu, *down, ids, weights, F32)
+        assert torch.equal(slots, rslots) and torch.equal(got, ref)

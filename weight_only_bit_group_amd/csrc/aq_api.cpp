@@ -1022,9 +1022,9 @@ aq_status aq_fp8_experts(const void* X, int32_t x_dtype, int64_t T, int64_t K, i
   auto* const h = reinterpret_cast<float*>(base + at.h);
   const hipStream_t on = (hipStream_t)stream;
   const int C = (int)(T * top);
-  hipError_t e = aq::launch_moe_group(ids, C, (int)top, (int)E, offsets, rows, slots,
-                                      reinterpret_cast<uint32_t*>(base + at.group), on);
-  if (e == hipSuccess) e = aq::launch_fp8_quantize(X, x_dtype == AQ_BF16, 1, T, K, ldx, false, x_codes, x_scales, on);
+  hipError_t e = aq::launch_moe_group_quantize(ids, C, (int)top, (int)E, offsets, rows, slots,
+                                               reinterpret_cast<uint32_t*>(base + at.group), X, x_dtype == AQ_BF16, T, K, ldx,
+                                               x_codes, x_scales, on);
   if (at.fused) {
     if (e == hipSuccess)
       e = aq::launch_fp8_gated(x_codes, x_scales, (int)T, (int)K, gate_up, gate_up_scales, (int)E, (int)I, offsets, rows, C,

@@ -122,6 +122,10 @@ hipError_t launch_moe_route_backward(const RouteArgs& a, bool l_bf16, const floa
 size_t moe_group_workspace_bytes(int64_t C, int E);
 hipError_t launch_moe_group(const int32_t* ids, int64_t C, int top, int E, int32_t* offsets, int32_t* rows, int32_t* slots,
                             uint32_t* work, hipStream_t stream);
+// the same and, beside it, the T rows X [T, K] of the choices' tokens as FP8 rows
+hipError_t launch_moe_group_quantize(const int32_t* ids, int64_t C, int top, int E, int32_t* offsets, int32_t* rows,
+                                     int32_t* slots, uint32_t* work, const void* X, bool x_bf16, int64_t T, int64_t K,
+                                     int64_t ldx, uint8_t* codes, float* scales, hipStream_t stream);
 // rows [gate | up] of 2 I values -> FP8 rows of I; end NULL or the device's count of rows that matter
 hipError_t launch_fp8_swiglu_quantize(const void* H, bool h_bf16, int64_t M, int I, const int32_t* end, uint8_t* codes,
                                       float* scales, hipStream_t stream);

@@ -104,11 +104,9 @@ __device__ __forceinline__ void starts_of(int E, uint32_t* start, uint32_t* part
 // Each wave's run, at most PER choices a lane, stays in registers between the counting and the placing (loaded twice:
 // 25 us for 16384 choices of 64 experts, so 15).
 template <int PER>
-__global__ __launch_bounds__(1024) void group_single_kernel(const int32_t* __restrict__ ids, int C, int E, int bits, int top,
-                                                           int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
-                                                           int32_t* __restrict__ slots) {
-  extern __shared__ uint32_t lds[];   // counters [waves][E], starts [E]
-  __shared__ uint32_t part[16];
+__device__ __forceinline__ void group_single(const int32_t* ids, int C, int E, int bits, int top, int32_t* offsets,
+                                             int32_t* rows, int32_t* slots, uint32_t* lds, uint32_t* part) {
+  // lds: counters [waves][E], starts [E]
   const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   uint32_t* start = lds + waves * E;
   uint32_t* cnt = lds + wave * E;
@@ -138,6 +136,47 @@ __global__ __launch_bounds__(1024) void group_single_kernel(const int32_t* __res
 #pragma unroll
   for (int j = 0; j < PER; ++j)
     if (lo + 64 * j < hi) place_64(lo + 64 * j + lane, hi, id[j], bits, top, cnt, rows, slots);
+}
+
+template <int PER>
+__global__ __launch_bounds__(1024) void group_single_kernel(const int32_t* __restrict__ ids, int C, int E, int bits, int top,
+                                                           int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
+                                                           int32_t* __restrict__ slots) {
+  extern __shared__ uint32_t lds[];
+  __shared__ uint32_t part[16];
+  group_single<PER>(ids, C, E, bits, top, offsets, rows, slots, lds, part);
+}
+
+// The same by the first workgroup, the rounding of the tokens' rows to FP8 (16 lanes a block of 128) by the others: one
+// launch for two small ones (16 tokens of 2048 and 128 choices: 4.6 + 4.6 us one after the other).
+template <int PER, bool BF16>
+__global__ __launch_bounds__(1024) void group_quantize_kernel(const int32_t* __restrict__ ids, int C, int E, int bits, int top,
+                                                             int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
+                                                             int32_t* __restrict__ slots, const void* __restrict__ X,
+                                                             uint32_t items, int K, int64_t ldx, int nkb,
+                                                             uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  extern __shared__ uint32_t lds[];
+  __shared__ uint32_t part[16];
+  if (blockIdx.x == 0) {
+    group_single<PER>(ids, C, E, bits, top, offsets, rows, slots, lds, part);
+    return;
+  }
+  const uint32_t item = (blockIdx.x - 1) * (blockDim.x >> 4) + (threadIdx.x >> 4);
+  const uint32_t row = item / (uint32_t)nkb;
+  const int k = (int)(item - row * nkb) * fp8::kBlock + (threadIdx.x & 15) * 8;
+  const bool mine = item < items && k < K;
+  fp8::Eight<BF16> in;
+  in.clear();
+  if (mine) in.load(X, row * ldx + k);
+  const float s = fp8::scale_of(fp8::row_umax(in.amax()));
+  if (mine) {
+    float x[8];
+    in.values(x);
+    uint32_t w[2];
+    fp8::codes_of<2>(x, s, w);
+    *reinterpret_cast<uint64_t*>(codes + (int64_t)row * K + k) = w[0] | ((uint64_t)w[1] << 32);
+    if ((threadIdx.x & 15) == 0) scales[item] = s;
+  }
 }
 
 // chunk b's counts of every expert: counts[b E + e]
@@ -337,6 +376,31 @@ hipError_t launch_moe_group(const int32_t* ids, int64_t C, int top, int E, int32
   hipLaunchKernelGGL(group_place_kernel, dim3(chunks), block, sizeof(uint32_t) * waves * E, stream, ids, C, E, bits, top, work,
                      rows, slots);
   return hipGetLastError();
+}
+
+hipError_t launch_moe_group_quantize(const int32_t* ids, int64_t C, int top, int E, int32_t* offsets, int32_t* rows,
+                                     int32_t* slots, uint32_t* work, const void* X, bool x_bf16, int64_t T, int64_t K,
+                                     int64_t ldx, uint8_t* codes, float* scales, hipStream_t stream) {
+  if (C > kSingle) {
+    const hipError_t e = launch_moe_group(ids, C, top, E, offsets, rows, slots, work, stream);
+    return e != hipSuccess ? e : launch_fp8_quantize(X, x_bf16, 1, T, K, ldx, false, codes, scales, stream);
+  }
+  const int waves = group_waves(E), nkb = (int)((K + fp8::kBlock - 1) / fp8::kBlock);
+  int bits = 0;
+  while (1 << bits < E) ++bits;
+  const uint32_t items = (uint32_t)(T * nkb);
+  const int per = (int)((C + 64 * waves - 1) / (64 * waves));
+  auto run = [&](auto* kernel) {
+    hipLaunchKernelGGL(kernel, dim3(1 + (items + 4 * waves - 1) / (4 * waves)), dim3(64 * waves),
+                       sizeof(uint32_t) * (waves + 1) * E, stream, ids, (int)C, E, bits, top, offsets, rows, slots, X, items,
+                       (int)K, ldx, nkb, codes, scales);
+    return hipGetLastError();
+  };
+  if (x_bf16)
+    return run(per <= 2 ? group_quantize_kernel<2, true> : per <= 8 ? group_quantize_kernel<8, true>
+               : per <= 16 ? group_quantize_kernel<16, true> : group_quantize_kernel<32, true>);
+  return run(per <= 2 ? group_quantize_kernel<2, false> : per <= 8 ? group_quantize_kernel<8, false>
+             : per <= 16 ? group_quantize_kernel<16, false> : group_quantize_kernel<32, false>);
 }
 
 hipError_t launch_fp8_swiglu_quantize(const void* H, bool h_bf16, int64_t M, int I, const int32_t* end, uint8_t* codes,

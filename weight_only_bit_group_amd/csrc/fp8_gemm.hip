@@ -735,13 +735,14 @@ hipError_t launch(const F8Args& a, hipStream_t stream) {
 //   fixed + r (round + stage * stages of a wave) + mb * (MB through LDS-DMA)     [us]
 // with r = the tiles over those that the device holds at once, at least 1: a block takes its run of stages whether or
 // not others run beside it, and every tile adds its traffic.  The four figures of a form are fitted to graph-replayed
-// times of 423 products (1 to 16384 rows on weights of 512 to 14336 rows and columns, drawn ones of 64 to 14336, up to
+// times of 469 products (1 to 16384 rows on weights of 512 to 14336 rows and columns, drawn ones of 64 to 14336, up to
 // 128 experts with 1 to 32768 rows): least squares of the relative error, then the choice's loss against the best form
-// in the geometric mean, which is 1.1% (bf16 out) and 1.3% (fp32 out) and at worst 1.28 times.  Forms without which that
-// mean would be 0.5% higher at most were left out.  Both sides, us:
+// in the geometric mean, which is 1.1% (bf16 out) and 1.3% (fp32 out) and at worst 1.27 times.  Forms without which that
+// mean would be 0.6% higher at most were left out.  Both sides, us:
 //   M = 1 on [11008, 2048], fp32 out: 16 x 64 over 8 waves 7.3, 16 x 16 over 4 waves 8.6, tiles of 32 x 128 17.8
 //   M = 16 on [4096, 14336], fp32 out: 16 x 16 over 16 waves 16.5, 16 x 32 over 8 waves 20.8, 16 x 64 over 8 waves 28.7
 //   M = 32 there, bf16 out: 16 x 32 over 8 waves 20.0, 16 x 16 over 16 waves 25.2, 16 x 64 over 8 waves 26.9
+//   M = 333 on [1003, 2064], fp32 out: 32 x 32 over 8 waves 8.1, 32 x 64 over 4 waves 9.2, 16 x 64 over 8 waves 10.4
 //   M = 128 on [11008, 2048], bf16 out: 32 x 64 over 4 waves 14.5, tiles of 32 x 128 19.2, of 128 x 128 22.1
 //   M = 4096 there: tiles of 256 x 256 114.8, of 128 x 128 142.7, of 32 x 128 232.1; fp32 out 265.7, 215.4, 296.9
 //   64 x 8 rows of 128 experts [2048, 1024]: tiles of 32 x 128 52.6, 32 x 64 over 4 waves 54.9, tiles of 128 x 128 63.2
@@ -775,16 +776,16 @@ auto with_forms(F f) {
   if constexpr (OUT == Out::GATED)
     return f(F8Form<F8Cfg<1, 4, 2, 4>>{{3.531f, 2.168f, 0.933f, 0.053f}}, F8Form<F8Cfg<2, 4, 4, 4>>{{2.818f, 7.496f, 1.926f, 0.024f}});
   else if constexpr (!WIDE)
-    return f(F8Form<F8Split<1, 1, 16, 1>>{{0.569f, 2.548f, 0.336f, 0.070f}}, F8Form<F8Split<1, 1, 4, 4>>{{1.913f, 0.985f, 0.194f, 0.085f}},
-             F8Form<F8Split<1, 2, 8, 2>>{{0.998f, 1.896f, 0.628f, 0.036f}}, F8Form<F8Split<1, 4, 8, 1>>{{0.416f, 2.539f, 0.968f, 0.031f}},
-             F8Form<F8Split<2, 2, 8, 2>>{{1.051f, 2.018f, 0.814f, 0.038f}}, F8Form<F8Split<2, 4, 4, 1>>{{1.640f, 1.548f, 0.786f, 0.056f}},
-             F8Form<F8Cfg<1, 4, 2, 2>>{{1.509f, 1.923f, 0.578f, 0.039f}}, F8Form<F8Cfg<2, 2, 4, 4>>{{0.923f, 3.869f, 0.739f, 0.065f}},
-             F8Form<F8Cfg<2, 4, 8, 4>>{{0.907f, 6.838f, 1.538f, 0.046f}});
+    return f(F8Form<F8Split<1, 1, 16, 1>>{{0.626f, 2.525f, 0.349f, 0.067f}}, F8Form<F8Split<1, 1, 4, 4>>{{1.191f, 1.726f, 0.202f, 0.075f}},
+             F8Form<F8Split<1, 2, 8, 2>>{{0.987f, 1.871f, 0.692f, 0.028f}}, F8Form<F8Split<1, 4, 8, 1>>{{1.065f, 2.724f, 0.665f, 0.030f}},
+             F8Form<F8Split<2, 2, 8, 1>>{{1.195f, 1.698f, 0.658f, 0.051f}}, F8Form<F8Split<2, 4, 4, 1>>{{1.632f, 1.905f, 0.556f, 0.058f}},
+             F8Form<F8Cfg<1, 4, 2, 2>>{{1.019f, 2.687f, 0.520f, 0.038f}}, F8Form<F8Cfg<2, 2, 4, 4>>{{0.377f, 4.681f, 0.614f, 0.070f}},
+             F8Form<F8Cfg<2, 4, 8, 4>>{{0.637f, 7.304f, 1.551f, 0.044f}});
   else
-    return f(F8Form<F8Split<1, 1, 16, 1>>{{3.406f, 0.455f, 0.459f, 0.053f}}, F8Form<F8Split<1, 1, 4, 4>>{{1.993f, 1.124f, 0.361f, 0.054f}},
-             F8Form<F8Split<1, 2, 8, 2>>{{1.874f, 1.704f, 0.592f, 0.041f}}, F8Form<F8Split<1, 4, 8, 1>>{{1.992f, 1.572f, 0.974f, 0.040f}},
-             F8Form<F8Split<2, 2, 8, 2>>{{2.013f, 1.914f, 0.749f, 0.046f}}, F8Form<F8Split<2, 4, 4, 1>>{{1.122f, 2.074f, 0.786f, 0.050f}},
-             F8Form<F8Cfg<1, 4, 2, 2>>{{0.056f, 2.847f, 0.659f, 0.045f}}, F8Form<F8Cfg<2, 2, 4, 4>>{{3.308f, 2.320f, 0.961f, 0.086f}});
+    return f(F8Form<F8Split<1, 1, 16, 1>>{{3.237f, 0.434f, 0.454f, 0.049f}}, F8Form<F8Split<1, 1, 4, 4>>{{2.325f, 0.828f, 0.385f, 0.054f}},
+             F8Form<F8Split<1, 2, 8, 2>>{{1.768f, 1.542f, 0.623f, 0.035f}}, F8Form<F8Split<1, 4, 8, 1>>{{1.855f, 1.343f, 1.033f, 0.043f}},
+             F8Form<F8Split<2, 2, 8, 1>>{{2.363f, 1.040f, 0.775f, 0.049f}}, F8Form<F8Split<2, 4, 4, 1>>{{1.029f, 2.163f, 0.757f, 0.059f}},
+             F8Form<F8Cfg<1, 4, 2, 2>>{{0.121f, 3.236f, 0.645f, 0.044f}}, F8Form<F8Cfg<2, 2, 4, 4>>{{3.510f, 2.694f, 0.983f, 0.082f}});
 }
 
 // the index of the form that the product takes on a device of `cus` compute units, and its estimated time

@@ -410,13 +410,37 @@ def _f8_rows(x: torch.Tensor, k: int) -> torch.Tensor:
     return x2 if x2.dtype in (torch.bfloat16, torch.float32) else x2.float()
 
 
-class FP8Linear(torch.nn.Module):
+class _FP8Module(torch.nn.Module):
+    """A module whose FP8 codes and their fp32 scales keep their types.
+
+    Both count as floating point, so a cast of the model around the module (``.to(dtype)``, ``.half()``) would convert
+    them, and the weights with them; it moves them between devices alone.
+    """
+
+    _held: tuple = ()   # names of the buffers
+
+    def _apply(self, fn, recurse=True):
+        held = [self._buffers[name] for name in self._held]
+
+        def kept(t):
+            if not any(t is b for b in held):
+                return fn(t)
+            probe = fn(t.new_empty(1))   # (not t: its copy in a wider type may be several times the weights)
+            return fn(t) if probe.dtype == t.dtype else t.to(probe.device)
+
+        return super()._apply(kept, recurse)
+
+
+class FP8Linear(_FP8Module):
     """y = x W^T (+ bias) with W in FP8 (codes [N, K], scales [ceil(N / 128), ceil(K / 128)]).
 
     The input is rounded row by row to FP8 blocks of 128.  The output is out_dtype: float32 with sums in fp32
     throughout, or bfloat16 on the FP8 matrix instructions, twice as fast for many rows.  There is no backward pass: an
-    input that requires a gradient gets its output, and an error when the gradient is asked for.
+    input that requires a gradient gets its output, and an error when the gradient is asked for.  Codes and scales keep
+    their types when the module is cast.
     """
+
+    _held = ("codes", "scales")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None,
                  out_dtype: torch.dtype = torch.float32):
@@ -521,7 +545,7 @@ class _Experts(torch.autograd.Function):
         return None, B.aq_moe_combine_backward(products, slots, grad.contiguous()), None, None
 
 
-class FP8Experts(torch.nn.Module):
+class FP8Experts(_FP8Module):
     """The experts of a mixture, gated MLPs with FP8 weights:
 
         y[t] = sum_j w[t, j] D_e Q(silu(G_e Q(x[t])) * U_e Q(x[t])),   e = ids[t, j]
@@ -534,8 +558,10 @@ class FP8Experts(torch.nn.Module):
     count back to the host, so a call may be captured into a graph whose replays follow x, ids and weights.  A token's
     products are added in the order of its choices, in fp32.  The output is out_dtype: float32 with sums in fp32
     throughout, or bfloat16 with the second product on the FP8 matrix instructions.  weights are differentiable, the
-    experts are not: an error when x's gradient is asked for.
+    experts are not: an error when x's gradient is asked for.  Codes and scales keep their types when the module is cast.
     """
+
+    _held = ("gate_up_codes", "gate_up_scales", "down_codes", "down_scales")
 
     def __init__(self, gate_up_codes: torch.Tensor, gate_up_scales: torch.Tensor, down_codes: torch.Tensor,
                  down_scales: torch.Tensor, out_dtype: torch.dtype = torch.float32):

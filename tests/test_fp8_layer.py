@@ -62,3 +62,45 @@ def test_casts_move_codes_and_scales():
         for moved in (copy.deepcopy(m).to("meta", torch.bfloat16), copy.deepcopy(m).to("meta"), copy.deepcopy(m).to_empty(device="meta")):
             assert all(b.is_meta for b in moved.buffers()) and len(list(moved.buffers())) == len(types)
             assert [b.dtype for n, b in moved.named_buffers() if n != "bias"] == [b.dtype for n, b in m.named_buffers() if n != "bias"], name
+
+
+@pytest.mark.parametrize("assign", [False, True])
+@pytest.mark.parametrize("have", [F8, torch.uint8])
+@pytest.mark.parametrize("given", [F8, torch.uint8])
+def test_state_of_the_same_bytes_is_loaded_as_they_are(have, given, assign):
+    """A checkpoint that holds the codes as bytes, into a module that holds them as float8, and the other way round."""
+    whole = torch.nn.ModuleDict(_modules(given))
+    blank = torch.nn.ModuleDict(_modules(have))
+    before = {n: (dtype if dtype == torch.float32 else have, b) for n, (dtype, b) in _held(whole).items()}
+    for m in blank.modules():
+        for b in m.buffers(recurse=False):
+            b.zero_()
+    state = whole.state_dict()
+    types = {n: t.dtype for n, t in state.items()}
+    blank.load_state_dict(state, assign=assign)
+    assert {n: t.dtype for n, t in state.items()} == types   # (the caller's own dict is left as it was)
+    _unchanged(blank, before)
+    assert torch.equal(blank["linear"].bias, whole["linear"].bias)
+
+
+@pytest.mark.parametrize("assign", [False, True])
+def test_state_of_another_kind_is_refused(assign):
+    for name, m in _modules().items():
+        codes = m._held[0]
+        for dtype in (torch.bfloat16, torch.float32, torch.int8, torch.float8_e5m2, torch.float8_e4m3fnuz):
+            state = m.state_dict()
+            state[codes] = torch.zeros(state[codes].shape, dtype=dtype)
+            before = _held(m)
+            with pytest.raises(RuntimeError, match="float8_e4m3fn"):
+                copy.deepcopy(m).load_state_dict(state, assign=assign)
+            _unchanged(m, before)
+        for dtype in (torch.bfloat16, torch.float64):   # (values that fp32 holds)
+            state = m.state_dict()
+            state[m._held[1]] = torch.full_like(state[m._held[1]], 0.75, dtype=dtype)
+            other = copy.deepcopy(m)
+            other.load_state_dict(state, assign=assign)
+            scales = getattr(other, m._held[1])
+            assert scales.dtype == torch.float32 and (scales == 0.75).all()
+        state = m.state_dict()
+        del state[codes]
+        assert copy.deepcopy(m).load_state_dict(state, strict=False).missing_keys == [codes]

@@ -414,7 +414,8 @@ class _FP8Module(torch.nn.Module):
     """A module whose FP8 codes and their fp32 scales keep their types.
 
     Both count as floating point, so a cast of the model around the module (``.to(dtype)``, ``.half()``) would convert
-    them, and the weights with them; it moves them between devices alone.
+    them, and the weights with them; it moves them between devices alone.  A state may hold the codes as float8_e4m3fn
+    or as the same bytes in uint8, whichever the module holds.
     """
 
     _held: tuple = ()   # names of the buffers
@@ -429,6 +430,22 @@ class _FP8Module(torch.nn.Module):
             return fn(t) if probe.dtype == t.dtype else t.to(probe.device)
 
         return super()._apply(kept, recurse)
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs):
+        # (copying bytes into float8 or float8 into bytes would convert the numbers that they stand for)
+        for name in self._held:
+            given, have = state_dict.get(prefix + name), self._buffers[name]
+            if given is None or given.dtype == have.dtype:
+                continue
+            if have.dtype == torch.float32:
+                given = given.float()
+            elif given.dtype in (torch.float8_e4m3fn, torch.uint8):
+                given = given.view(have.dtype)
+            else:
+                error_msgs.append(f"{prefix + name} must be float8_e4m3fn (or uint8), got {given.dtype}")
+                given = have
+            state_dict[prefix + name] = given
+        super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs)
 
 
 class FP8Linear(_FP8Module):

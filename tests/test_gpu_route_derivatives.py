@@ -1,0 +1,50 @@
+"""What route's derivatives are and which are refused."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe as O
+from tests.gpu_util import dev, host, step
+from tests.test_gpu_route_graph import _gpu, _logits, route  # noqa: F401 (fixtures)
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("groups,top_groups,bias", [(1, 1, False), (1, 1, True), (4, 2, False), (4, 2, True), (8, 8, True)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradient_against_differences_in_64_bits(route, dtype, groups, top_groups, bias, renormalize, score):
+    """(f(l + h) - f(l - h)) / 2h of f = sum_j d_j w_j at the choices that were made, formed in 64 bits.  A weight as a
+    function of one logit has a third derivative below 2 scale (a logistic function's is below 1/8), so the difference is
+    off by h^2 / 3 scale sum |d|, and by the 64-bit weights' roundings over h; the gradient by its one rounding."""
+    t, e, top, scale, h = 7, 40, 5, 2.5, 2.0 ** -12
+    rng = np.random.default_rng(e + groups)
+    l = rng.standard_normal((t, e)) * 2
+    l[rng.random((t, e)) < 0.2] = -np.inf
+    l[3] = -np.inf          # nothing to choose
+    l[4, 2:] = -np.inf      # fewer than top
+    b = (rng.standard_normal(e) * 0.2).astype(np.float32) if bias else None
+    d = rng.standard_normal((t, top)).astype(np.float32)
+    x = dev(l.astype(np.float32)).to(dtype).requires_grad_()
+    l = host(x.detach().double())
+    kept = dict(score=score, renormalize=renormalize, scale=scale)
+    step(f"route against differences, {score} renormalize {renormalize} groups {groups} bias {bias} {dtype}")
+    ids, w = route(x, top, bias=None if b is None else dev(b), groups=groups, top_groups=top_groups, **kept)
+    assert (host(ids) == O.route(l, top, bias=b, groups=groups, top_groups=top_groups, **kept)[0]).all()
+    got, = torch.autograd.grad(w, x, dev(d))
+    got, ids = host(got.double()), host(ids)
+    diff = np.zeros((t, e))
+    for i in range(e):
+        side = []
+        for s in (h, -h):
+            moved = l.copy()
+            moved[:, i] += s
+            side.append((O.weights_at(moved, ids, **kept) * d).sum(1))
+        diff[:, i] = (side[0] - side[1]) / (2 * h)
+    size = scale * np.abs(d).sum(1, keepdims=True)
+    tol = size * (h * h / 3 * 2 + 2.0 ** -48 / h) + (2.0 ** -24 if dtype == F32 else 2.0 ** -8) * np.abs(diff) * 1.01
+    assert (np.abs(got - diff) <= tol).all()
+    assert (got[3] == 0).all() and np.abs(got).max() > 1e-3
+    assert (np.abs(got - O.route_backward(l, ids, d, **kept)) <= size * 2.0 ** -45 * (top + 1) + (2.0 ** -24 if dtype == F32 else 2.0 ** -8) * np.abs(got) * 1.01).all()

@@ -5,7 +5,7 @@ import torch
 
 from oracle import moe as O
 from tests.gpu_util import dev, host, step
-from tests.test_gpu_route_graph import _gpu, _logits, route  # noqa: F401 (fixtures)
+from tests.test_gpu_route_graph import HOWS, _gpu, _logits, route  # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -48,3 +48,30 @@ def test_gradient_against_differences_in_64_bits(route, dtype, groups, top_group
     assert (np.abs(got - diff) <= tol).all()
     assert (got[3] == 0).all() and np.abs(got).max() > 1e-3
     assert (np.abs(got - O.route_backward(l, ids, d, **kept)) <= size * 2.0 ** -45 * (top + 1) + (2.0 ** -24 if dtype == F32 else 2.0 ** -8) * np.abs(got) * 1.01).all()
+
+
+@pytest.mark.parametrize("how", HOWS)
+@pytest.mark.parametrize("needs", [True, False])
+def test_derivative_of_the_gradient_is_refused(route, how, needs):
+    """The gradient is a function of the logits whatever the gradient that comes in: with create_graph, asking for its
+    derivative is an error, never nothing."""
+    l = _logits().requires_grad_()
+    d = torch.randn(9, 3, device="cuda", requires_grad=needs)
+    step(f"route's second derivative, {how}")
+    plain, = torch.autograd.grad(route(l, 3, **how)[1], l, d)
+    assert not plain.requires_grad
+    _, w = route(l, 3, **how)
+    g, = torch.autograd.grad(w, l, d, create_graph=True)
+    assert torch.equal(g, plain)
+    with pytest.raises(RuntimeError, match="differentiate"):
+        torch.autograd.grad(g.square().sum(), l)
+    _, w = route(2 * l, 3, **how)
+    penalty = torch.autograd.grad(w.sum(), l, create_graph=True)[0].square().sum()
+    with pytest.raises(RuntimeError, match="differentiate"):
+        (w.square().sum() + penalty).backward()
+    other = _logits(seed=1).requires_grad_()
+    _, w = route(other, 3, **how)
+    w.square().sum().backward(create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate"):
+        other.grad.sum().backward()
+    other.grad = None

@@ -539,7 +539,7 @@ struct RouteBackward : public torch::autograd::Node {
     std::lock_guard<std::mutex> lock(mutex_);
     torch::autograd::variable_list out(1);
     if (!grads[0].defined() || !task_should_compute_output(0)) return out;
-    const bool again = at::GradMode::is_enabled() && grads[0].requires_grad();
+    const bool again = at::GradMode::is_enabled();   // (create_graph)
     {
       at::NoGradGuard no_grad;
       const at::Tensor l = logits.unpack(), i = ids.unpack(), w = weights.unpack(shared_from_this());
@@ -552,7 +552,9 @@ struct RouteBackward : public torch::autograd::Node {
                                                  stream_of(l.get_device()));
       TORCH_CHECK(st == AQ_OK, "aq_moe_route_backward: ", aq_last_error());
     }
-    if (again) {   // the gradient is not differentiable itself: asking for its gradient is an error
+    // The gradient is a function of the logits, whatever the gradient that came in, and not differentiable itself: asking
+    // for its gradient is an error.
+    if (again) {
       torch::autograd::DelayedError error("trying to differentiate the gradient of route", 1);
       out = error.apply({out[0].requires_grad_(true)});
     }

@@ -493,6 +493,18 @@ def _capturable(name: str, t: torch.Tensor) -> None:
                            "before its backward pass is captured, or run it on the capturing stream")
 
 
+class _NoSecond(torch.autograd.Function):
+    """route's gradient, whose own gradient is refused."""
+
+    @staticmethod
+    def forward(ctx, gradient):
+        return gradient.view_as(gradient)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError("trying to differentiate the gradient of route")
+
+
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top, bias, how):
@@ -504,19 +516,23 @@ class _Route(torch.autograd.Function):
         return ids, weights
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, _, dweights):
         if dweights is None:
             return None, None, None, None
         logits, ids, weights = ctx.saved_tensors
-        return B.aq_moe_route_backward(logits, ids, weights, dweights.float().contiguous(), **ctx.how), None, None, None
+        with torch.no_grad():
+            dlogits = B.aq_moe_route_backward(logits, ids, weights, dweights.float().contiguous(), **ctx.how)
+        if torch.is_grad_enabled():   # (create_graph: a function of the logits, whatever dweights is)
+            dlogits = _NoSecond.apply(dlogits.requires_grad_())
+        return dlogits, None, None, None
 
 
 def route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, score: str = "softmax", groups: int = 1,
           top_groups: int | None = None, renormalize: bool = True, scale: float = 1.0):
     """(ids [.., top] int32, weights [.., top] float32) of a router's logits [.., E], as FP8Experts and MXFP4Experts take
     them; see ``binding.aq_moe_route`` for the arguments.  weights are differentiable with respect to the logits, the
-    choice is not, and the bias (which only balances the choice) gets no gradient.  A call and its backward pass may be
+    choice is not, and the bias (which only balances the choice) gets no gradient.  The gradient has none of its own: an
+    error when it is asked for.  A call and its backward pass may be
     captured; an error where a graph of an earlier call with the same leaves still lives on another stream."""
     if logits.is_cuda:
         pair = B.moe_route_graph(logits, top, bias, score, groups, top_groups, renormalize, scale)

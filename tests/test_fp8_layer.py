@@ -3,6 +3,7 @@ import copy
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fw
 
 from weight_only_bit_group_amd import layer as L
 
@@ -104,3 +105,22 @@ def test_state_of_another_kind_is_refused(assign):
         state = m.state_dict()
         del state[codes]
         assert copy.deepcopy(m).load_state_dict(state, strict=False).missing_keys == [codes]
+
+
+def test_inputs_with_a_tangent_are_refused():
+    """A forward derivative is an error before anything else is looked at; without one the call goes on (to the binding, which
+    wants a GPU tensor)."""
+    m = _modules()
+    ids = torch.zeros(4, 2, dtype=torch.int64)
+    mx = L.MXFP4Linear(torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.uint8))
+    calls = {"FP8Linear": (m["linear"], torch.randn(4, 272)), "MXFP4Linear": (mx, torch.randn(4, 64)),
+             "FP8Experts": (lambda x: m["experts"](x, ids, ids.float()), torch.randn(4, 96)),
+             "FP8Experts weights": (lambda w: m["experts"](torch.zeros(4, 96), ids, w), torch.randn(4, 2)),
+             "route": (lambda l: L.route(l, 2), torch.randn(4, 8))}
+    with fw.dual_level():
+        for name, (call, x) in calls.items():
+            for y in (x, x.double(), x.clone().requires_grad_()):
+                with pytest.raises(RuntimeError, match=f"{name.split()[0]} has no forward derivative"):
+                    call(fw.make_dual(y, torch.ones_like(y)))
+            with pytest.raises(ValueError, match="GPU tensor"):
+                call(x)

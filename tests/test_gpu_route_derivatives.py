@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 import torch
+import torch.autograd.forward_ad as fw
 
 from oracle import moe as O
 from tests.gpu_util import dev, host, step
@@ -75,3 +76,39 @@ def test_derivative_of_the_gradient_is_refused(route, how, needs):
     with pytest.raises(RuntimeError, match="differentiate"):
         other.grad.sum().backward()
     other.grad = None
+
+
+def test_forward_derivatives_are_refused(route):
+    from weight_only_bit_group_amd import layer
+    l = _logits()
+    t = torch.randn_like(l)
+    ref = route(l, 3)
+    step("route of logits with a tangent")
+    with fw.dual_level():
+        for dual in (fw.make_dual(l, t), fw.make_dual(l.clone().requires_grad_(), t), fw.make_dual(l.double(), t.double()),
+                     fw.make_dual(l.view(3, 3, 24), t.view(3, 3, 24)), fw.make_dual(l, t) * 2.0):
+            with pytest.raises(RuntimeError, match="forward"):
+                route(dual, 3)
+            with torch.no_grad(), pytest.raises(RuntimeError, match="forward"):
+                route(dual, 3)
+        got = route(l, 3)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+        got = route(fw.unpack_dual(fw.make_dual(l, t)).primal, 3)
+        assert torch.equal(got[1], ref[1])
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(lambda x: route(x, 3)[1], (l,), (t,))
+    with pytest.raises(RuntimeError):
+        torch.func.grad(lambda x: route(x, 3)[1].sum())(l)
+
+    lin = layer.FP8Linear.from_weight(torch.randn(48, 64, device="cuda"))
+    m = layer.FP8Experts.from_weights(torch.randn(4, 64, 32, device="cuda"), torch.randn(4, 32, 32, device="cuda"))
+    x, ids, w = torch.randn(9, 32, device="cuda"), torch.randint(0, 4, (9, 2), device="cuda"), torch.rand(9, 2, device="cuda")
+    v = torch.randn(9, 64, device="cuda")
+    step("FP8 modules of inputs with a tangent")
+    with fw.dual_level():
+        for call in (lambda: lin(fw.make_dual(v, v)), lambda: lin(fw.make_dual(v.half(), v.half())), lambda: m(fw.make_dual(x, x), ids, w),
+                     lambda: m(x, ids, fw.make_dual(w, w)), lambda: m(x, ids, fw.make_dual(w.double(), w.double())),
+                     lambda: m(x, ids, fw.make_dual(w.clone().requires_grad_(), w))):
+            with pytest.raises(RuntimeError, match="forward"):
+                call()
+        assert torch.equal(m(x, ids, w), m(x.clone(), ids, w)) and lin(v).shape == (9, 48)

@@ -576,8 +576,8 @@ PyObject* route_graph(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   const int device = device_for(args[0]);
   if (device < 0) Py_RETURN_NONE;
   Routing r;
-  // (a conflict is the caller's to report)
-  if (!r.read(args, device) || capture_conflict(*r.l.x, device) || !r.run(device)) Py_RETURN_NONE;
+  // (a conflict, or a tangent, is the caller's to report)
+  if (!r.read(args, device) || r.l.x->_fw_grad(0).defined() || capture_conflict(*r.l.x, device) || !r.run(device)) Py_RETURN_NONE;
   if (at::GradMode::is_enabled() && r.l.x->requires_grad()) {
     auto node = std::shared_ptr<RouteBackward>(new RouteBackward(), torch::autograd::deleteNode);
     node->set_next_edges(torch::autograd::collect_next_edges(*r.l.x));

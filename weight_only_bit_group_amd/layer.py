@@ -37,6 +37,7 @@ from __future__ import annotations
 from dataclasses import dataclass
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
 
@@ -255,8 +256,16 @@ class _NoBackward(torch.autograd.Function):
                            "(run it under torch.no_grad(), or detach its input)")
 
 
+def _no_tangent(name: str, *tensors) -> None:
+    """Raises where one of the tensors carries a forward derivative: the kernels would lose it in silence."""
+    for t in tensors:
+        if forward_ad.unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{name} has no forward derivative: the tangent of its input would be lost")
+
+
 def _forward_only(name: str, compute, x: torch.Tensor) -> torch.Tensor:
     """compute(x), a fresh tensor; part of the graph where x is, so that no gradient is lost in silence."""
+    _no_tangent(name, x)
     if torch.is_grad_enabled() and x.requires_grad:
         return _NoBackward.apply(name, compute, x)
     return compute(x)
@@ -453,8 +462,8 @@ class FP8Linear(_FP8Module):
 
     The input is rounded row by row to FP8 blocks of 128.  The output is out_dtype: float32 with sums in fp32
     throughout, or bfloat16 on the FP8 matrix instructions, twice as fast for many rows.  There is no backward pass: an
-    input that requires a gradient gets its output, and an error when the gradient is asked for.  Codes and scales keep
-    their types when the module is cast.
+    input that requires a gradient gets its output, and an error when the gradient is asked for (an input with a forward
+    derivative: at once).  Codes and scales keep their types when the module is cast.
     """
 
     _held = ("codes", "scales")
@@ -531,13 +540,14 @@ def route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, scor
           top_groups: int | None = None, renormalize: bool = True, scale: float = 1.0):
     """(ids [.., top] int32, weights [.., top] float32) of a router's logits [.., E], as FP8Experts and MXFP4Experts take
     them; see ``binding.aq_moe_route`` for the arguments.  weights are differentiable with respect to the logits, the
-    choice is not, and the bias (which only balances the choice) gets no gradient.  The gradient has none of its own: an
-    error when it is asked for.  A call and its backward pass may be
-    captured; an error where a graph of an earlier call with the same leaves still lives on another stream."""
+    choice is not, and the bias (which only balances the choice) gets no gradient.  The gradient has none of its own, and
+    there is no forward derivative: an error when either is asked for.  A call and its backward pass may be captured; an
+    error where a graph of an earlier call with the same leaves still lives on another stream."""
     if logits.is_cuda:
         pair = B.moe_route_graph(logits, top, bias, score, groups, top_groups, renormalize, scale)
         if pair is not None:
             return pair
+    _no_tangent("route", logits)
     lead, e = logits.shape[:-1], logits.shape[-1]
     l2 = logits.reshape(-1, e)
     if l2.dtype not in (torch.float32, torch.bfloat16):
@@ -591,7 +601,7 @@ class FP8Experts(_FP8Module):
     count back to the host, so a call may be captured into a graph whose replays follow x, ids and weights.  A token's
     products are added in the order of its choices, in fp32.  The output is out_dtype: float32 with sums in fp32
     throughout, or bfloat16 with the second product on the FP8 matrix instructions.  weights are differentiable, the
-    experts are not: an error when x's gradient is asked for.  Codes and scales keep their types when the module is cast.
+    experts are not: an error when x's gradient is asked for, and where x or weights have a forward derivative.  Codes and scales keep their types when the module is cast.
     """
 
     _held = ("gate_up_codes", "gate_up_scales", "down_codes", "down_scales")
@@ -636,6 +646,7 @@ class FP8Experts(_FP8Module):
             ids = ids.long().clamp(-1, self.num_experts).int()
         ids = ids.reshape(-1, top).contiguous()
         w = weights.reshape(-1, top).float().contiguous()
+        _no_tangent("FP8Experts", x2, w)
         if torch.is_grad_enabled() and (w.requires_grad or x2.requires_grad):
             _capturable("FP8Experts", w)
             out = _Experts.apply(x2, w, ids, self)

@@ -1,4 +1,4 @@
-"""What route's derivatives are and which are refused."""
+"""What route's derivatives are and which are refused; one token's logits in any layout."""
 import numpy as np
 import pytest
 import torch
@@ -112,3 +112,22 @@ def test_forward_derivatives_are_refused(route):
             with pytest.raises(RuntimeError, match="forward"):
                 call()
         assert torch.equal(m(x, ids, w), m(x.clone(), ids, w)) and lin(v).shape == (9, 48)
+
+
+def test_one_token_of_any_layout(route):
+    """A single row, or logits of one dimension, whose experts are not neighbours in memory."""
+    wide = _logits(6, 80)
+    step("route of one token's strided logits")
+    for x in (wide[2:3, ::2], wide[2, ::2], wide[:, 5:6].t(), wide[:, 5], wide.view(2, 3, 80)[1:, 1:2, ::4], wide[:1, ::2].double(), wide[2, :1]):
+        top = min(3, x.shape[-1])
+        ids, w = route(x, top)
+        ref = route(x.contiguous(), top)
+        assert ids.shape == (*x.shape[:-1], top) and torch.equal(ids, ref[0]) and torch.equal(w, ref[1])
+        leaf = x.clone(memory_format=torch.contiguous_format).requires_grad_()
+        base = wide.double() if x.dtype == torch.float64 else wide.clone()
+        base.requires_grad_()
+        view = base.as_strided(x.shape, x.stride(), x.storage_offset()) if x.dtype == F32 else base[:1, ::2]
+        d = torch.randn_like(w)
+        want, = torch.autograd.grad(route(leaf, top)[1], leaf, d)
+        got, = torch.autograd.grad(route(view, top)[1], base, d)
+        assert torch.equal(got[got != 0].sort()[0], want.reshape(-1)[want.reshape(-1) != 0].sort()[0])

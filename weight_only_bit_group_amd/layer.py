@@ -552,7 +552,7 @@ def route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, scor
     l2 = logits.reshape(-1, e)
     if l2.dtype not in (torch.float32, torch.bfloat16):
         l2 = l2.float()
-    if l2.shape[0] > 1 and (l2.stride(1) != 1 or l2.stride(0) < e):
+    if l2.stride(1) != 1 or (l2.shape[0] > 1 and l2.stride(0) < e):
         l2 = l2.contiguous()
     bias = None if bias is None else bias.detach().float().contiguous()
     how = dict(score=score, groups=groups, top_groups=top_groups, renormalize=renormalize, scale=scale)
@@ -601,7 +601,8 @@ class FP8Experts(_FP8Module):
     count back to the host, so a call may be captured into a graph whose replays follow x, ids and weights.  A token's
     products are added in the order of its choices, in fp32.  The output is out_dtype: float32 with sums in fp32
     throughout, or bfloat16 with the second product on the FP8 matrix instructions.  weights are differentiable, the
-    experts are not: an error when x's gradient is asked for, and where x or weights have a forward derivative.  Codes and scales keep their types when the module is cast.
+    experts are not: an error when x's gradient is asked for, and where x or weights have a forward derivative.  Codes
+    and scales keep their types when the module is cast.
     """
 
     _held = ("gate_up_codes", "gate_up_scales", "down_codes", "down_scales")

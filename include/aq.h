@@ -481,8 +481,8 @@ aq_status aq_fp8_swiglu_quantize(const void* H, int32_t h_dtype, int64_t M, int6
  * aq_moe_route_backward: dlogits [T, E] (the logits' type, dense) = the gradient of sum(dweights * weights) at
  * those choices (ids and weights as aq_moe_route wrote them; a bias has no gradient).  NaN weights give the chosen
  * experts NaN.
- * Errors: EINVAL for a bad dtype or score, T < 0 or T >= 2^30, E <= 0 or E > 1024, top <= 0, top > E or top > 64,
- *         T * top >= 2^31, ld < E or ld >= 2^30, groups <= 0, groups > 64 or E % groups, top_groups <= 0,
+ * Errors: EINVAL for a bad dtype or score, T < 0 or T > 2^26 - 4 (a launch of a wave for each token), E <= 0 or
+ *         E > 1024, top <= 0, top > E or top > 64, T * top >= 2^31, ld < E or ld >= 2^30, groups <= 0, groups > 64 or E % groups, top_groups <= 0,
  *         top_groups > groups or fewer than top experts in them, a scale that is not finite, NULL / misaligned
  *         pointers (one element).
  */

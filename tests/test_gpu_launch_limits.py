@@ -1,0 +1,53 @@
+"""The largest sizes that the routing and FP8 entry points accept, launched: rows that repeat a few patterns, compared with
+the same rows in a small call."""
+import pytest
+import torch
+
+from tests.gpu_util import step
+
+pytestmark = pytest.mark.gpu
+BLOCKS = (1 << 24) - 1   # workgroups of 256 threads in a launch
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu(lib):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+    torch.cuda.empty_cache()
+
+
+def B():
+    from weight_only_bit_group_amd import binding
+    return binding
+
+
+PERIOD = 97
+
+
+def _rows(few, n):
+    """n rows that repeat the PERIOD rows of `few`."""
+    whole = n // PERIOD * PERIOD
+    return torch.cat([few.expand(n // PERIOD, *few.shape).reshape(whole, *few.shape[1:]), few[:n - whole]])
+
+
+def _repeats(got, few):
+    n = got.shape[0] // PERIOD
+    return bool((got[:n * PERIOD].view(n, PERIOD, *few.shape[1:]) == few).all()) and torch.equal(got[n * PERIOD:], few[:got.shape[0] - n * PERIOD])
+
+
+def test_most_tokens_of_route_and_its_gradient():
+    t, how = 4 * BLOCKS, dict(score="sigmoid", scale=1.5)
+    few, d = torch.randn(PERIOD, 4, device="cuda").to(BF16), torch.randn(PERIOD, 1, device="cuda")
+    ref = B().aq_moe_route(few, 1, **how)
+    l = _rows(few, t)
+    step(f"route {t} tokens")
+    ids, w = B().aq_moe_route(l, 1, **how)
+    assert ids.shape == (t, 1) and _repeats(ids, ref[0]) and _repeats(w, ref[1])
+    step(f"route's gradient, {t} tokens")
+    got = B().aq_moe_route_backward(l, ids, w, _rows(d, t), score="sigmoid", renormalize=False, scale=1.5)
+    assert _repeats(got, B().aq_moe_route_backward(few, *ref, d, score="sigmoid", renormalize=False, scale=1.5))
+    assert (got != 0).any()
+    with pytest.raises(ValueError, match="T must be"):
+        B().aq_moe_route(_rows(few, t + 1)[:, :1], 1)

@@ -67,6 +67,9 @@ constexpr int64_t kDimLimit = int64_t(1) << 30;
 // MFMA GEMMs: 32-bit offsets within a block's rows (loads) and within its output
 // tile (stores) need K < 2^22 and N < 2^22.
 constexpr int64_t kGemmDimLimit = int64_t(1) << 22;
+// A launch has fewer than 2^32 threads: workgroups of 256 that one can have.  (A wave a token or choice: four in each.)
+constexpr int64_t kLaunchBlocks = (int64_t(1) << 24) - 1;
+constexpr int64_t kLaunchWaves = 4 * kLaunchBlocks;
 // Smallest M for which the staged GEMM path (weights dequantized once into a bf16
 // staging matrix) is used when the caller provides the workspace.
 constexpr int64_t kStagedMinM = 2048;
@@ -826,6 +829,7 @@ static aq_status route_args(const char* fn, const void* logits, int32_t l_dtype,
   AQ_REQUIRE(score == AQ_SOFTMAX || score == AQ_SIGMOID, "%s: score must be AQ_SOFTMAX or AQ_SIGMOID (got %d)", fn, score);
   const aq_status st = check_choices(fn, T, E, top);
   if (st != AQ_OK) return st;
+  AQ_REQUIRE(T <= kLaunchWaves, "%s: T must be at most 2^26 - 4 (got %lld)", fn, (long long)T);
   AQ_REQUIRE(top <= E && top <= 64, "%s: top must be at most E and 64 (got %lld of %lld)", fn, (long long)top, (long long)E);
   AQ_REQUIRE(ld >= E && ld < kDimLimit, "%s: ld (%lld) must be at least E", fn, (long long)ld);
   AQ_PTR(logits, l_dtype == AQ_BF16 ? 2 : 4, "logits");

@@ -51,3 +51,35 @@ def test_most_tokens_of_route_and_its_gradient():
     assert (got != 0).any()
     with pytest.raises(ValueError, match="T must be"):
         B().aq_moe_route(_rows(few, t + 1)[:, :1], 1)
+
+
+def test_most_choices_of_the_weighted_sums_gradient():
+    t, top, r = 2 * BLOCKS, 2, 50
+    y, d = torch.randn(r, 8, device="cuda"), torch.randn(PERIOD, 8, device="cuda").to(BF16)
+    slots = torch.randint(-1, r + 1, (PERIOD, top), dtype=torch.int32, device="cuda")
+    step(f"combine's gradient, {t * top} choices")
+    got = B().aq_moe_combine_backward(y, _rows(slots, t), _rows(d, t))
+    assert got.shape == (t, top) and _repeats(got, B().aq_moe_combine_backward(y, slots, d)) and (got != 0).any()
+    step(f"combine, {t * top} choices")
+    w = torch.rand(PERIOD, top, device="cuda")
+    got = B().aq_moe_combine(y, _rows(slots, t), _rows(w, t), BF16)
+    assert _repeats(got, B().aq_moe_combine(y, slots, w, BF16))
+    with pytest.raises(ValueError, match="T \\* top"):
+        B().aq_moe_combine_backward(y, _rows(slots, t + 1), _rows(d, t + 1))
+
+
+def test_most_columns_of_combine():
+    """Rows as long as they may be, as many as a launch takes: 64 GiB of bf16, every row one of four."""
+    k = (1 << 22) - 8
+    t = 2048 * BLOCKS // k
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("not enough memory")
+    y = torch.randn(4, k, device="cuda").to(BF16)
+    slots = (torch.arange(t, device="cuda", dtype=torch.int32) % 4)[:, None].contiguous()
+    step(f"combine {t} x {k}")
+    out = B().aq_moe_combine(y, slots, torch.ones(t, 1, device="cuda"), BF16)
+    for i in range(4):
+        assert all(torch.equal(row, y[i]) for row in out[i::4][::97]) and torch.equal(out[t - 4 + i], y[(t - 4 + i) % 4])
+    assert torch.equal(out[:, 0], y[:, 0][slots[:, 0].long()]) and torch.equal(out[:, -1], y[:, -1][slots[:, 0].long()])
+    del out
+    torch.cuda.empty_cache()

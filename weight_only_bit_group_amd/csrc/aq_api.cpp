@@ -905,7 +905,6 @@ static aq_status check_combine(const char* fn, const void* Y, int32_t y_dtype, i
   AQ_REQUIRE(R >= 0 && R < (int64_t(1) << 31) && (R > 0 || T == 0), "%s: R out of range (%lld)", fn, (long long)R);
   AQ_REQUIRE(K > 0 && K < kGemmDimLimit && K % 8 == 0, "%s: K must be a positive multiple of 8 below 2^22 (got %lld)", fn,
              (long long)K);
-  AQ_REQUIRE(T * K < (int64_t(1) << 36) && T * top < (int64_t(1) << 31), "%s: T * K must be below 2^36", fn);
   AQ_PTR(Y, 16, "Y");
   AQ_PTR(slots, 4, "slots");
   return AQ_OK;
@@ -916,6 +915,8 @@ aq_status aq_moe_combine(const void* Y, int32_t y_dtype, int64_t R, int64_t K, c
   const char* fn = "aq_moe_combine";
   const aq_status st = check_combine(fn, Y, y_dtype, R, K, slots, T, top, out_dtype);
   if (st != AQ_OK) return st;
+  // (a thread for eight columns)
+  AQ_REQUIRE(T * K <= 8 * 256 * kLaunchBlocks, "%s: T * K must be at most 2^35 - 2048", fn);
   AQ_PTR(weights, 4, "weights");
   AQ_PTR(out, 16, "out");
   if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);
@@ -930,6 +931,8 @@ aq_status aq_moe_combine_backward(const void* Y, int32_t y_dtype, int64_t R, int
   const char* fn = "aq_moe_combine_backward";
   const aq_status st = check_combine(fn, Y, y_dtype, R, K, slots, T, top, dout_dtype);
   if (st != AQ_OK) return st;
+  AQ_REQUIRE(T * K < (int64_t(1) << 36), "%s: T * K must be below 2^36", fn);
+  AQ_REQUIRE(T * top <= kLaunchWaves, "%s: T * top must be at most 2^26 - 4", fn);
   AQ_PTR(dout, 16, "dout");
   AQ_PTR(dweights, 4, "dweights");
   if (fault_injected()) return fail(AQ_ERUNTIME, "%s: injected launch failure", fn);

@@ -410,8 +410,8 @@ aq_status aq_mxfp4_grouped_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scal
  * of 16 bytes); codes [E, N, K]; scales [E, N, kb] (block_rows 1) or [E, nb, kb] (block_rows 128).
  * aq_fp8_dequantize: Y [E, N, K] = fl32(c S), in bf16 rounded once more to nearest even.
  * Errors: EINVAL for a bad dtype, block_rows other than 1 and 128, E <= 0, N < 0, E * N >= 2^30, K <= 0 or K % 16,
- *         E * N * K >= 2^36, ldx < K or rows that are not 16 bytes aligned, NULL / misaligned pointers (X, Y, codes
- *         16 bytes, scales 4).
+ *         E * N * K >= 2^36, more blocks than a launch takes (2^30 - 64 of 128, and to quantise 2^24 - 1 of 128 x 128),
+ *         ldx < K or rows that are not 16 bytes aligned, NULL / misaligned pointers (X, Y, codes 16 bytes, scales 4).
  */
 aq_status aq_fp8_quantize(const void* X, int32_t x_dtype, int64_t E, int64_t N, int64_t K, int64_t ldx,
                           int32_t block_rows, uint8_t* codes, float* scales, void* stream);
@@ -432,7 +432,7 @@ aq_status aq_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t E
  * the block's codes add nothing).  A call gives the same bits every time, and a row's outputs do not depend on the other rows' values.
  * codes [N, K], scales [ceil(N / 128), ceil(K / 128)].
  * Errors: EINVAL for a bad dtype, M < 0 or M >= 2^30, N < 0 or N >= 2^22, K <= 0, K >= 2^22 or K % 16, M * N >= 2^37,
- *         M * K >= 2^36, ldx as aq_fp8_quantize, a small workspace, NULL / misaligned pointers (X, codes and workspace
+ *         M * K >= 2^36, ldx and the blocks of X as aq_fp8_quantize, a small workspace, NULL / misaligned pointers (X, codes and workspace
  *         16 bytes, scales 4, Y one element).
  */
 aq_status aq_fp8_gemm(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
@@ -457,8 +457,8 @@ aq_status aq_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, int
  * The gated activation between an expert's products: h = silu(g) u of rows [g | u] (H [M, 2 I], fp32 or bf16),
  * silu(g) = g / (1 + exp(-g)) in fp32, rounded to FP8 rows as aq_fp8_quantize rounds (block_rows 1): codes [M, I],
  * scales [M, ceil(I / 128)].  end: NULL, or a device int32: rows from *end on are neither read nor written.
- * Errors: EINVAL for a bad dtype, M < 0 or M >= 2^30, I <= 0, I >= 2^22 or I % 16, M * I >= 2^36, NULL / misaligned
- *         pointers (H, codes 16 bytes; scales, end 4).
+ * Errors: EINVAL for a bad dtype, M < 0 or M >= 2^30, I <= 0, I >= 2^22 or I % 16, M * I >= 2^36, more than 2^28 - 16
+ *         blocks of 128 (a launch), NULL / misaligned pointers (H, codes 16 bytes; scales, end 4).
  */
 aq_status aq_fp8_swiglu_quantize(const void* H, int32_t h_dtype, int64_t M, int64_t I, const int32_t* end, uint8_t* codes,
                                  float* scales, void* stream);

@@ -83,3 +83,50 @@ def test_most_columns_of_combine():
     assert torch.equal(out[:, 0], y[:, 0][slots[:, 0].long()]) and torch.equal(out[:, -1], y[:, -1][slots[:, 0].long()])
     del out
     torch.cuda.empty_cache()
+
+
+def test_most_blocks_of_the_quantiser():
+    few = torch.randn(PERIOD, 1, 16, device="cuda").to(BF16)
+    step(f"quantise {BLOCKS} matrices")
+    codes, scales = B().aq_fp8_quantize(_rows(few, BLOCKS), 128)
+    ref = B().aq_fp8_quantize(few, 128)
+    assert scales.shape == (BLOCKS, 1, 1) and _repeats(codes.view(torch.uint8), ref[0].view(torch.uint8)) and _repeats(scales, ref[1])
+    with pytest.raises(ValueError, match="128 x 128"):
+        B().aq_fp8_quantize(_rows(few, BLOCKS + 1), 128)
+
+
+def test_most_blocks_of_the_gated_activation():
+    m = 16 * BLOCKS
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("not enough memory")
+    few = torch.randn(PERIOD, 32, device="cuda").to(BF16)
+    step(f"swiglu quantize {m} rows")
+    codes, scales = B().aq_fp8_swiglu_quantize(_rows(few, m))
+    ref = B().aq_fp8_swiglu_quantize(few)
+    assert codes.shape == (m, 16) and _repeats(codes.view(torch.uint8), ref[0].view(torch.uint8)) and _repeats(scales, ref[1])
+
+
+def test_most_rows_of_the_quantiser_and_back():
+    """2^30 - 64 rows of one block: 32 GiB in, 16 GiB of codes and 4 of scales, 32 GiB back."""
+    n = 64 * BLOCKS
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("not enough memory")
+    few = torch.randn(128, 16, device="cuda").to(BF16)
+    x = few.expand(n // 128, 128, 16).reshape(-1, 16)
+    x = torch.cat([x, few[:n - x.shape[0]]]) if n % 128 else x
+    ref = B().aq_fp8_quantize(few)
+    step(f"quantise {n} rows")
+    codes, scales = B().aq_fp8_quantize(x)
+    del x
+
+    def repeats(got, ref):
+        whole = got.shape[0] // 128
+        return all(bool((part == ref).all()) for part in got[:whole * 128].view(whole, 128, *ref.shape[1:]).split(1 << 18)) \
+            and torch.equal(got[whole * 128:], ref[:got.shape[0] - whole * 128])
+
+    assert repeats(scales, ref[1]) and repeats(codes.view(torch.uint8), ref[0].view(torch.uint8))
+    step(f"read {n} rows back")
+    y = B().aq_fp8_dequantize(codes, scales, out_dtype=BF16)
+    assert repeats(y, B().aq_fp8_dequantize(*ref, out_dtype=BF16))
+    del y, codes, scales
+    torch.cuda.empty_cache()

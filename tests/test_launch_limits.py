@@ -3,7 +3,8 @@
 launch, a call whose arguments are accepted ends there.)"""
 import pytest
 
-from tests.test_moe_abi import _b, _c, _cb, _r
+from tests.test_fp8_abi import _d, _l, _q
+from tests.test_moe_abi import _b, _c, _cb, _r, _s
 from weight_only_bit_group_amd import _lib
 
 BLOCKS = (1 << 24) - 1   # workgroups of 256 threads
@@ -39,3 +40,29 @@ def test_choices_of_the_weighted_sums_gradient(lib, top):
     t = 4 * BLOCKS // top
     _limit(_cb, lib, dict(T=t, top=top, K=8), dict(T=t + 1, top=top, K=8), "T * top")
     assert _c(lib, T=t + 1, top=top, K=8) == _lib.AQ_ERUNTIME
+
+
+@pytest.mark.parametrize("K", [16, 64])
+def test_rows_of_the_quantiser(lib, K):
+    """Of one block; longer rows end at 2^36 values before."""
+    n = 64 * BLOCKS
+    for call in (_q, _d):
+        _limit(call, lib, dict(N=n, K=K), dict(N=n + 1, K=K), "blocks of 128")
+        _limit(call, lib, dict(E=n // 4, N=4, K=K), dict(E=n // 4 + 1, N=4, K=K), "blocks of 128")
+        assert call(lib, N=(1 << 36) // 144, K=144) == _lib.AQ_ERUNTIME
+    _limit(_l, lib, dict(M=n, K=K), dict(M=n + 1, K=K), "blocks of 128")
+
+
+@pytest.mark.parametrize("N", [1, 60, 63])
+def test_blocks_of_the_quantiser(lib, N):
+    """Many small matrices; of matrices of 128 rows and more 2^30 rows are fewer blocks."""
+    _limit(_q, lib, dict(E=BLOCKS, N=N, K=16, br=128), dict(E=BLOCKS + 1, N=N, K=16, br=128), "128 x 128")
+    _limit(_q, lib, dict(E=BLOCKS // 3, N=1, K=272, br=128), dict(E=BLOCKS // 3 + 1, N=1, K=272, br=128), "128 x 128")
+    assert _d(lib, E=BLOCKS + 1, N=N, K=16, br=128) == _lib.AQ_ERUNTIME
+    assert _q(lib, E=(1 << 23) - 1, N=128, K=16, br=128) == _lib.AQ_ERUNTIME
+
+
+@pytest.mark.parametrize("I,blocks", [(16, 1), (128, 1), (144, 2), (208, 2)])
+def test_blocks_of_the_gated_activation(lib, I, blocks):
+    m = 16 * BLOCKS // blocks
+    _limit(_s, lib, dict(M=m, I=I), dict(M=m + 1, I=I), "blocks of 128")

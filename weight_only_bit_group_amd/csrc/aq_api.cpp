@@ -679,6 +679,9 @@ static aq_status check_fp8_matrix(const char* fn, int64_t E, int64_t N, int64_t 
   return AQ_OK;
 }
 
+// rows of K in blocks of 128, of which a workgroup of 256 threads takes 64
+static bool launch_takes_rows(int64_t rows, int64_t K) { return rows * ((K + 127) / 128) <= 64 * kLaunchBlocks; }
+
 aq_status aq_fp8_quantize(const void* X, int32_t x_dtype, int64_t E, int64_t N, int64_t K, int64_t ldx,
                           int32_t block_rows, uint8_t* codes, float* scales, void* stream) {
   const char* fn = "aq_fp8_quantize";
@@ -687,6 +690,10 @@ aq_status aq_fp8_quantize(const void* X, int32_t x_dtype, int64_t E, int64_t N, 
   if (st != AQ_OK) return st;
   AQ_REQUIRE(ldx >= K && ldx < kDimLimit * 2 && ldx % (x_dtype == AQ_BF16 ? 8 : 4) == 0,
              "%s: ldx (%lld) must be at least K and a multiple of 16 bytes", fn, (long long)ldx);
+  if (block_rows > 1)   // (a workgroup a block)
+    AQ_REQUIRE(E * ((N + 127) / 128) * ((K + 127) / 128) <= kLaunchBlocks, "%s: at most 2^24 - 1 blocks of 128 x 128", fn);
+  else
+    AQ_REQUIRE(launch_takes_rows(E * N, K), "%s: at most 2^30 - 64 blocks of 128", fn);
   AQ_PTR(X, 16, "X");
   AQ_PTR(codes, 16, "codes");
   AQ_PTR(scales, 4, "scales");
@@ -703,6 +710,7 @@ aq_status aq_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t E
   AQ_REQUIRE(y_dtype == AQ_F32 || y_dtype == AQ_BF16, "%s: y_dtype must be AQ_F32 or AQ_BF16 (got %d)", fn, y_dtype);
   const aq_status st = check_fp8_matrix(fn, E, N, K, block_rows);
   if (st != AQ_OK) return st;
+  AQ_REQUIRE(launch_takes_rows(E * N, K), "%s: at most 2^30 - 64 blocks of 128", fn);
   AQ_PTR(codes, 16, "codes");
   AQ_PTR(scales, 4, "scales");
   AQ_PTR(Y, 16, "Y");
@@ -761,6 +769,7 @@ aq_status aq_fp8_linear(const void* X, int32_t x_dtype, int64_t M, int64_t K, in
   if (st != AQ_OK) return st;
   AQ_REQUIRE(ldx >= K && ldx < kDimLimit * 2 && ldx % (x_dtype == AQ_BF16 ? 8 : 4) == 0,
              "%s: ldx (%lld) must be at least K and a multiple of 16 bytes", fn, (long long)ldx);
+  AQ_REQUIRE(launch_takes_rows(M, K), "%s: at most 2^30 - 64 blocks of 128 in X", fn);
   AQ_PTR(X, 16, "X");
   const size_t need = aq_fp8_linear_workspace(M, K);
   if (M > 0) {
@@ -803,6 +812,8 @@ aq_status aq_fp8_swiglu_quantize(const void* H, int32_t h_dtype, int64_t M, int6
   AQ_REQUIRE(I > 0 && I < kGemmDimLimit && I % 16 == 0, "%s: I must be a positive multiple of 16 below 2^22 (got %lld)",
              fn, (long long)I);
   AQ_REQUIRE(M * I < (int64_t(1) << 36), "%s: M * I must be below 2^36", fn);
+  // (16 lanes a block)
+  AQ_REQUIRE(M * ((I + 127) / 128) <= 16 * kLaunchBlocks, "%s: at most 2^28 - 16 blocks of 128", fn);
   AQ_PTR(H, 16, "H");
   AQ_PTR(codes, 16, "codes");
   AQ_PTR(scales, 4, "scales");

@@ -537,7 +537,7 @@ aq_status aq_moe_combine_backward(const void* Y, int32_t y_dtype, int64_t R, int
  * X [T, K] fp32 or bf16, rows ldx elements apart; ids [T, top] int32, weights [T, top] fp32, slots [T, top] int32, out
  * [T, K].  workspace: aq_fp8_experts_workspace(T, top, K, E, I) bytes of device memory, 16-byte aligned, used
  * only during the call (0 for sizes that the call refuses).
- * Errors: as the calls that it is made of; 2 I below 2^22; T * top below 2^30.
+ * Errors: as the calls that it is made of; EINVAL also for 2 I >= 2^22, T * top >= 2^30 or T * K > 2^35 - 2^21.
  */
 size_t aq_fp8_experts_workspace(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I);
 aq_status aq_fp8_experts(const void* X, int32_t x_dtype, int64_t T, int64_t K, int64_t ldx, const uint8_t* gate_up,

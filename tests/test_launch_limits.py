@@ -4,6 +4,7 @@ launch, a call whose arguments are accepted ends there.)"""
 import pytest
 
 from tests.test_fp8_abi import _d, _l, _q
+from tests.test_fp8_experts_abi import _x
 from tests.test_moe_abi import _b, _c, _cb, _r, _s
 from weight_only_bit_group_amd import _lib
 
@@ -66,3 +67,21 @@ def test_blocks_of_the_quantiser(lib, N):
 def test_blocks_of_the_gated_activation(lib, I, blocks):
     m = 16 * BLOCKS // blocks
     _limit(_s, lib, dict(M=m, I=I), dict(M=m + 1, I=I), "blocks of 128")
+
+
+BIG = 1 << 60   # bytes of workspace
+
+
+@pytest.mark.parametrize("inside,outside", [
+    # the weighted sum, and few rows of K in blocks of 128 (2^35 - 2^21 in all)
+    (dict(T=16383, K=(1 << 21) - 16, top=1, E=8, I=16), dict(T=16384, K=(1 << 21) - 16, top=1, E=8, I=16)),
+    (dict(T=(1 << 25) - (1 << 11), K=1 << 10, top=1, E=8, I=16), dict(T=(1 << 25) - (1 << 11) + 1, K=1 << 10, top=1, E=8, I=16)),
+    # the activation, where it is a launch of its own
+    (dict(T=16 * BLOCKS, K=16, top=1, E=1, I=16), dict(T=16 * BLOCKS + 1, K=16, top=1, E=1, I=16)),
+    (dict(T=8 * BLOCKS, K=16, top=2, E=8, I=16), dict(T=8 * BLOCKS + 1, K=16, top=2, E=8, I=16)),
+    (dict(T=2 * BLOCKS, K=16, top=4, E=8, I=208), dict(T=2 * BLOCKS + 1, K=16, top=4, E=8, I=208)),
+])
+def test_sizes_of_the_experts(lib, inside, outside):
+    size = lambda s: lib.aq_fp8_experts_workspace(s["T"], s["top"], s["K"], s["E"], s["I"])
+    assert size(inside) > 0 == size(outside)
+    _limit(_x, lib, dict(inside, wb=BIG), dict(outside, wb=BIG), "too large")

@@ -982,10 +982,14 @@ struct ExpertsParts {
 
 // the sizes' limits, in the order of their checks in aq_fp8_experts
 bool experts_sizes(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I) {
-  return T > 0 && T < kDimLimit && E > 0 && E <= 1024 && top > 0 && T * top < kDimLimit && K > 0 && K < kGemmDimLimit &&
-         K % 16 == 0 && I > 0 && 2 * I < kGemmDimLimit && I % 16 == 0 && E * K < (int64_t(1) << 27) &&
-         E * 2 * I < (int64_t(1) << 27) && T * K < (int64_t(1) << 36) && T * top * I < (int64_t(1) << 36) &&
-         T * top * K < (int64_t(1) << 37);
+  if (!(T > 0 && T < kDimLimit && E > 0 && E <= 1024 && top > 0 && T * top < kDimLimit && K > 0 && K < kGemmDimLimit &&
+        K % 16 == 0 && I > 0 && 2 * I < kGemmDimLimit && I % 16 == 0 && E * K < (int64_t(1) << 27) &&
+        E * 2 * I < (int64_t(1) << 27) && T * top * I < (int64_t(1) << 36) && T * top * K < (int64_t(1) << 37)))
+    return false;
+  // The launches' limits: the weighted sum's and, with few choices, that of the grouping beside the rounding (64 blocks
+  // of 128 for 1024 threads, 16384 rows that may end in a part-filled one); the activation's where it is a launch
+  return T * K <= (int64_t(1) << 35) - (int64_t(1) << 21) &&
+         (aq::fp8_gated_fused((int)(T * top), (int)K, (int)I, (int)E) || T * top * ((I + 127) / 128) <= 16 * kLaunchBlocks);
 }
 
 }  // namespace

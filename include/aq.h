@@ -501,7 +501,7 @@ aq_status aq_moe_route_backward(const void* logits, int32_t l_dtype, int64_t T, 
  *   slots [T top]:   the slot of each choice, -1 for one without an expert.
  * workspace: aq_moe_group_workspace(T, top, E) bytes of device memory (0 up to 16384 choices), 4-byte aligned, used
  * only during the call.
- * Errors: EINVAL for T < 0 or T >= 2^30, E <= 0 or E > 1024, top <= 0, T * top >= 2^31, a small workspace, NULL /
+ * Errors: EINVAL for T < 0 or T >= 2^30, E <= 0 or E > 1024, top <= 0, top or T * top >= 2^31, a small workspace, NULL /
  *         misaligned pointers (4 bytes).  T = 0 writes the offsets.
  */
 size_t aq_moe_group_workspace(int64_t T, int64_t top, int64_t E);
@@ -514,8 +514,8 @@ aq_status aq_moe_group(const int32_t* ids, int64_t T, int64_t top, int64_t E, in
  * Y [R, K] fp32 or bf16, slots [T, top] int32 (outside 0 .. R - 1: adds nothing, whatever its weight holds), weights
  * [T, top] fp32, out [T, K] fp32 or bf16 rounded once.
  * aq_moe_combine_backward: dweights[t, j] = sum_k dout[t, k] Y[slots[t, j], k], fp32 sums; 0 for a slot outside.
- * Errors: EINVAL for a bad dtype, T < 0 or T >= 2^30, top <= 0, T * top >= 2^31 (backward, a launch of a wave for each
- *         choice: > 2^26 - 4), R < 0, R >= 2^31 or R = 0 with T > 0, K <= 0, K >= 2^22 or K % 8, T * K > 2^35 - 2048 (a
+ * Errors: EINVAL for a bad dtype, T < 0 or T >= 2^30, top <= 0, top or T * top >= 2^31 (backward, a launch of a wave for
+ *         each choice: T * top > 2^26 - 4), R < 0, R >= 2^31 or R = 0 with T > 0, K <= 0, K >= 2^22 or K % 8, T * K > 2^35 - 2048 (a
  *         launch of a thread for eight columns; backward: >= 2^36), NULL / misaligned pointers (Y, out, dout 16 bytes,
  *         others 4).
  */

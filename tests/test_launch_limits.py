@@ -5,7 +5,7 @@ import pytest
 
 from tests.test_fp8_abi import _d, _l, _q
 from tests.test_fp8_experts_abi import _x
-from tests.test_moe_abi import _b, _c, _cb, _r, _s
+from tests.test_moe_abi import _b, _c, _cb, _g, _r, _s
 from weight_only_bit_group_amd import _lib
 
 BLOCKS = (1 << 24) - 1   # workgroups of 256 threads
@@ -85,3 +85,12 @@ def test_sizes_of_the_experts(lib, inside, outside):
     size = lambda s: lib.aq_fp8_experts_workspace(s["T"], s["top"], s["K"], s["E"], s["I"])
     assert size(inside) > 0 == size(outside)
     _limit(_x, lib, dict(inside, wb=BIG), dict(outside, wb=BIG), "too large")
+
+
+@pytest.mark.parametrize("T,top", [(4, 1 << 62), (1 << 29, 1 << 35), (1 << 20, (1 << 44) + 1), (3, (1 << 63) - 1), (2, 1 << 31)])
+def test_choices_whose_product_overflows(lib, T, top):
+    """T * top past 64 bits, some of them small again."""
+    assert _g(lib, T=T, top=top, W=1 << 16, wb=BIG) == _lib.AQ_EINVAL and "top" in _lib.last_error()
+    assert _c(lib, T=T, top=top) == _cb(lib, T=T, top=top) == _r(lib, T=T, top=top) == _b(lib, T=T, top=top) == _lib.AQ_EINVAL
+    assert _x(lib, T=T, top=top, wb=BIG) == _lib.AQ_EINVAL and "top" in _lib.last_error()
+    assert lib.aq_moe_group_workspace(T, top, 8) == lib.aq_fp8_experts_workspace(T, top, 256, 8, 128) == 0

@@ -829,8 +829,8 @@ aq_status aq_fp8_swiglu_quantize(const void* H, int32_t h_dtype, int64_t M, int6
 static aq_status check_choices(const char* fn, int64_t T, int64_t E, int64_t top) {
   AQ_REQUIRE(T >= 0 && T < kDimLimit, "%s: T out of range (%lld)", fn, (long long)T);
   AQ_REQUIRE(E > 0 && E <= 1024, "%s: E must be 1 .. 1024 (got %lld)", fn, (long long)E);
-  AQ_REQUIRE(top > 0 && T * top < (int64_t(1) << 31), "%s: top must be positive and T * top below 2^31 (T %lld, top %lld)",
-             fn, (long long)T, (long long)top);
+  AQ_REQUIRE(top > 0 && top < (int64_t(1) << 31) && T * top < (int64_t(1) << 31),
+             "%s: top must be positive and T * top below 2^31 (T %lld, top %lld)", fn, (long long)T, (long long)top);
   return AQ_OK;
 }
 
@@ -885,7 +885,8 @@ aq_status aq_moe_route_backward(const void* logits, int32_t l_dtype, int64_t T, 
 }
 
 size_t aq_moe_group_workspace(int64_t T, int64_t top, int64_t E) {
-  if (T <= 0 || T >= kDimLimit || top <= 0 || T * top >= (int64_t(1) << 31) || E <= 0 || E > 1024) return 0;
+  if (T <= 0 || T >= kDimLimit || top <= 0 || top >= (int64_t(1) << 31) || T * top >= (int64_t(1) << 31) || E <= 0 || E > 1024)
+    return 0;
   return aq::moe_group_workspace_bytes(T * top, (int)E);
 }
 
@@ -982,9 +983,9 @@ struct ExpertsParts {
 
 // the sizes' limits, in the order of their checks in aq_fp8_experts
 bool experts_sizes(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I) {
-  if (!(T > 0 && T < kDimLimit && E > 0 && E <= 1024 && top > 0 && T * top < kDimLimit && K > 0 && K < kGemmDimLimit &&
-        K % 16 == 0 && I > 0 && 2 * I < kGemmDimLimit && I % 16 == 0 && E * K < (int64_t(1) << 27) &&
-        E * 2 * I < (int64_t(1) << 27) && T * top * I < (int64_t(1) << 36) && T * top * K < (int64_t(1) << 37)))
+  if (!(T > 0 && T < kDimLimit && E > 0 && E <= 1024 && top > 0 && top < kDimLimit && T * top < kDimLimit && K > 0 &&
+        K < kGemmDimLimit && K % 16 == 0 && I > 0 && 2 * I < kGemmDimLimit && I % 16 == 0 &&
+        E * K < (int64_t(1) << 27) && E * 2 * I < (int64_t(1) << 27) && T * top * I < (int64_t(1) << 36) && T * top * K < (int64_t(1) << 37)))
     return false;
   // The launches' limits: the weighted sum's and, with few choices, that of the grouping beside the rounding (64 blocks
   // of 128 for 1024 threads, 16384 rows that may end in a part-filled one); the activation's where it is a launch

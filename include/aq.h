@@ -515,9 +515,9 @@ aq_status aq_moe_group(const int32_t* ids, int64_t T, int64_t top, int64_t E, in
  * [T, top] fp32, out [T, K] fp32 or bf16 rounded once.
  * aq_moe_combine_backward: dweights[t, j] = sum_k dout[t, k] Y[slots[t, j], k], fp32 sums; 0 for a slot outside.
  * Errors: EINVAL for a bad dtype, T < 0 or T >= 2^30, top <= 0, top or T * top >= 2^31 (backward, a launch of a wave for
- *         each choice: T * top > 2^26 - 4), R < 0, R >= 2^31 or R = 0 with T > 0, K <= 0, K >= 2^22 or K % 8, T * K > 2^35 - 2048 (a
- *         launch of a thread for eight columns; backward: >= 2^36), NULL / misaligned pointers (Y, out, dout 16 bytes,
- *         others 4).
+ *         each choice: T * top > 2^26 - 4), R < 0, R >= 2^31 or R = 0 with T > 0, K <= 0, K >= 2^22 or K % 8,
+ *         T * K > 2^35 - 2048 (a launch of a thread for eight columns; backward: >= 2^36), NULL / misaligned pointers
+ *         (Y, out, dout 16 bytes, others 4).
  */
 aq_status aq_moe_combine(const void* Y, int32_t y_dtype, int64_t R, int64_t K, const int32_t* slots, const float* weights,
                          int64_t T, int64_t top, void* out, int32_t out_dtype, void* stream);

@@ -47,8 +47,9 @@ __device__ __forceinline__ void place_64(int64_t i, int64_t end, int id, int bit
     same &= one ? m : ~m;
   }
   int slot = -1;
+  wave_order();   // (the counters that the caller, or the 64 before, wrote)
   if (id >= 0) {
-    const uint32_t at = cnt[id];
+    const uint32_t at = cnt[id];   // (one load of all lanes, ahead of the store that depends on it)
     slot = (int)(at + __popcll(same & below));
     if ((same & ~below) == ((uint64_t)1 << lane)) cnt[id] = slot + 1;   // the last of its equals
     rows[slot] = (int)((uint32_t)i / (uint32_t)top);

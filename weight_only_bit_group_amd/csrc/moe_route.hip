@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteArgs a) {
   }
 
   if (grouped) {
-    __builtin_amdgcn_wave_barrier();   // (a wave's LDS accesses run in order: what it wrote it reads)
+    wave_order();   // (lanes read keys that others wrote)
     // q lanes a group, each over every q-th of its experts; then the group's two highest by exchanges
     const int q = a.lanes, size = a.E / a.groups, g = lane / q;
     double one = -INFINITY, two = -INFINITY;

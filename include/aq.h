@@ -455,8 +455,8 @@ aq_status aq_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, int
 
 /*
  * The gated activation between an expert's products: h = silu(g) u of rows [g | u] (H [M, 2 I], fp32 or bf16),
- * silu(g) = g / (1 + exp(-g)) in fp32, rounded to FP8 rows as aq_fp8_quantize rounds (block_rows 1): codes [M, I],
- * scales [M, ceil(I / 128)].  end: NULL, or a device int32: rows from *end on are neither read nor written.
+ * silu(g) = g / (1 + exp(-g)) in fp32 (0 below g = -87.34), rounded to FP8 rows as aq_fp8_quantize rounds (block_rows 1):
+ * codes [M, I], scales [M, ceil(I / 128)].  end: NULL, or a device int32: rows from *end on are neither read nor written.
  * Errors: EINVAL for a bad dtype, M < 0 or M >= 2^30, I <= 0, I >= 2^22 or I % 16, M * I >= 2^36, more than 2^28 - 16
  *         blocks of 128 (a launch), NULL / misaligned pointers (H, codes 16 bytes; scales, end 4).
  */
@@ -470,7 +470,8 @@ aq_status aq_fp8_swiglu_quantize(const void* H, int32_t h_dtype, int64_t M, int6
  *   an expert with l = -inf or key = -inf is never chosen;
  *   groups > 1: the experts form `groups` equal runs of neighbours; a run's score is the sum of its two highest keys
  *   (s without a bias; the highest alone where only one can be chosen), and only the experts of the top_groups best
- *   runs (ties: the lower one) can be chosen;
+ *   runs (ties: the lower one) can be chosen.  That is the rule with and without a bias: routers that rank the runs by
+ *   their highest score alone choose other experts;
  *   chosen: the `top` highest keys, in descending order, ties to the lowest index; when fewer than top can be
  *   chosen, the slots left over get id -1 and weight 0;
  *   weight of choice j: scale * s_j / sum_i s_i over the chosen ones (renormalize; 0 where that sum is 0), or
@@ -482,9 +483,9 @@ aq_status aq_fp8_swiglu_quantize(const void* H, int32_t h_dtype, int64_t M, int6
  * those choices (ids and weights as aq_moe_route wrote them; a bias has no gradient).  NaN weights give the chosen
  * experts NaN.
  * Errors: EINVAL for a bad dtype or score, T < 0 or T > 2^26 - 4 (a launch of a wave for each token), E <= 0 or
- *         E > 1024, top <= 0, top > E or top > 64, T * top >= 2^31, ld < E or ld >= 2^30, groups <= 0, groups > 64 or E % groups, top_groups <= 0,
- *         top_groups > groups or fewer than top experts in them, a scale that is not finite, NULL / misaligned
- *         pointers (one element).
+ *         E > 1024, top <= 0, top > E or top > 64, T * top >= 2^31, ld < E or ld >= 2^30, groups <= 0, groups > 64 or
+ *         E % groups, top_groups <= 0, top_groups > groups or fewer than top experts in them, a scale that is not
+ *         finite, NULL / misaligned pointers (one element).
  */
 aq_status aq_moe_route(const void* logits, int32_t l_dtype, int64_t T, int64_t E, int64_t ld, int64_t top, int32_t score,
                        const float* bias, int32_t groups, int32_t top_groups, int32_t renormalize, float scale,

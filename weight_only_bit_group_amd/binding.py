@@ -832,7 +832,8 @@ def aq_moe_route(logits, top: int, *, score: str = "softmax", bias=None, groups:
     """(ids [T, top] int32, weights [T, top] f32) of router logits [T, E] (f32 or bf16; rows may be strided).
 
     score: "softmax" or "sigmoid"; bias [E] f32 is added to the scores for the choice alone; groups > 1 keeps the
-    experts of the top_groups best runs of E / groups neighbours; renormalize divides a token's weights by their sum.
+    experts of the top_groups best runs of E / groups neighbours, a run's score being the sum of its two highest (scores
+    plus bias) whether or not there is a bias, never its highest alone; renormalize divides a token's weights by their sum.
     An expert whose logit is -inf is never chosen; slots left over get id -1 and weight 0.
     """
     pair = _mx.route(logits, top, score, bias, groups, top_groups, renormalize, scale)

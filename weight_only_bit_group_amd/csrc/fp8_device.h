@@ -65,8 +65,9 @@ __device__ __forceinline__ uint32_t row_umax(uint32_t v) {
   return v;
 }
 
-// silu(g) u; silu(g) is g times the reciprocal of 1 + 2^(-g log2 e), each of the two within 1 ulp: far below the
-// rounding to E4M3 that follows
+// silu(g) u; silu(g) is g times the reciprocal of 1 + 2^(-g log2 e).  The exponent's rounding moves the power by some
+// |g| 2^-23 of itself, exp2, sum and reciprocal add a few 2^-24: far below the 2^-4 of the rounding to E4M3 that
+// follows.  From g = -87.34 down the reciprocal is below 2^-126 and becomes 0.
 __device__ __forceinline__ float gated(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
 }

@@ -461,7 +461,8 @@ class FP8Linear(_FP8Module):
     """y = x W^T (+ bias) with W in FP8 (codes [N, K], scales [ceil(N / 128), ceil(K / 128)]).
 
     The input is rounded row by row to FP8 blocks of 128.  The output is out_dtype: float32 with sums in fp32
-    throughout, or bfloat16 on the FP8 matrix instructions, twice as fast for many rows.  There is no backward pass: an
+    throughout, or bfloat16 on the FP8 matrix instructions, twice as fast for many rows.  A bias is added to the output
+    (to bfloat16 outputs with a rounding of its own: the sum of a rounded product and the bias, rounded).  There is no backward pass: an
     input that requires a gradient gets its output, and an error when the gradient is asked for (an input with a forward
     derivative: at once).  Codes and scales keep their types when the module is cast.
     """
@@ -539,7 +540,8 @@ class _Route(torch.autograd.Function):
 def route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, score: str = "softmax", groups: int = 1,
           top_groups: int | None = None, renormalize: bool = True, scale: float = 1.0):
     """(ids [.., top] int32, weights [.., top] float32) of a router's logits [.., E], as FP8Experts and MXFP4Experts take
-    them; see ``binding.aq_moe_route`` for the arguments.  weights are differentiable with respect to the logits, the
+    them; see ``binding.aq_moe_route`` for the arguments (with groups, a run of experts counts by its two highest scores,
+    also without a bias).  weights are differentiable with respect to the logits, the
     choice is not, and the bias (which only balances the choice) gets no gradient.  The gradient has none of its own, and
     there is no forward derivative: an error when either is asked for.  A call and its backward pass may be captured; an
     error where a graph of an earlier call with the same leaves still lives on another stream."""

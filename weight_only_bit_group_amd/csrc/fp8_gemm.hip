@@ -127,12 +127,13 @@ __device__ __forceinline__ void store_columns(const F8Args& a, int r, int col, c
 // (16 FM) x (16 FN) tile through LDS buffers of its own, filled by its own LDS-DMA, so there is no barrier before the
 // sums are joined, in wave order: a wave only waits for its own oldest loads, with R stages in flight.  (Straight to
 // registers, in the order that the instructions take, neighbouring lanes read 16 bytes of different rows: four times
-// the requests, 23 us against 13 for 16 rows on [4096, 14336].)
+// the requests, 23 us against 16 for 16 rows on [4096, 14336].)
 //   Activation rows past the tile's are not fetched: their LDS bytes are whatever was there, in columns of the result
 // that are not stored.
 //   Up to 16 short rows are rounded by every block for itself, while its first weights are under way: one token on
-// [11008, 2048] takes 7.6 us, with a rounding kernel in front 9.4; 8 rows of 1024 on [11008, 1024] 6.4 and 7.6, on
-// [4096, 1024] 6.2 and 6.0 (graph-replayed; from the host a launch less).
+// [11008, 2048] takes 5.7 us, with a rounding kernel in front 7.2; 8 rows of 1024 on [4096, 1024] 5.0 and 5.8, on
+// [11008, 1024] 5.7 and 6.7 (bf16 out: equal); 16 rows of 512 on [4096, 512] 5.3 and 5.2, the worst of the rule's sizes
+// tried (graph-replayed, weights in the cache; called from the host 4.3 to 5.4 and 7.1 to 7.4, a launch less).
 constexpr int kRounded = 8192;   // their values at most (32 KiB of fp32 a block)
 template <int FM_, int FN_, int NW_, int R_>
 struct F8Split {
@@ -361,11 +362,12 @@ __global__ __launch_bounds__(C::NT) void fp8_split_kernel(F8Args a) {
 // ---- tiles ----------------------------------------------------------------------------------
 // WM x WN waves, each (16 FM) activation rows x (16 FN) weight rows.  K advances in stages of one block, 128 bytes of
 // a row, through two LDS buffers filled by LDS-DMA.
-//   M = 4096 on [11008, 2048], bf16 out: 103 to 115 us, 1.6 to 1.8 PFLOP/s (a library product of FP8 with one scale a
-// tensor 101); K = 14336 on 4096 columns 230 us, 2.1.  There the matrix cores work 48% of the loop's cycles: a stage of a
-// 256 x 256 tile has 2048 cycles of matrix instructions on a SIMD and takes 4290, a third of them waiting for the
-// hand-over; four fused multiply-adds follow every instruction, and 64 KB of a stage come from the L2 and LDS alike.
-// fp32 out: 0.9 PFLOP/s, the codes' conversion (16 instructions an operand) beside four matrix instructions a product.
+//   M = 4096 on [11008, 2048], bf16 out: 94 to 102 us, 1.8 to 2.0 PFLOP/s (a library product of FP8 with one scale a
+// tensor 101); K = 14336 on 4096 columns 196 to 205 us, 2.4 (171).  The matrix cores work 48% of the loop's cycles: a
+// stage of a 256 x 256 tile has 2048 cycles of matrix instructions on a SIMD and takes 4290, a third of them waiting for
+// the hand-over; four fused multiply-adds follow every instruction, and 64 KB of a stage come from the L2 and LDS alike.
+// fp32 out: 196 us (0.94 PFLOP/s) and 421, the codes' conversion (16 instructions an operand) beside four matrix
+// instructions a product.
 template <int WM_, int WN_, int FM_, int FN_>
 struct F8Cfg {
   static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_;
@@ -382,7 +384,9 @@ struct F8Cfg {
   // blocks that a compute unit holds; their registers leave room for 8 waves, or 12
   static constexpr int per_cu(bool gated) { return std::max(1, std::min(160 * 1024 / (lds(gated) + 1024), (FM * FN >= 16 ? 8 : 12) / NW)); }
   // Whether a block takes one tile after the other: where a compute unit holds one block, whose first loads and last
-  // stores nothing would cover.  (4096 rows on [11008, 2048] by 256 x 256: 141 us with a block a tile, 119 chained.)
+  // stores nothing would cover.  It gains little: calls of linear_prefill's sizes (4096 rows on [11008, 2048]) take 112 us
+  // alone and 115 one behind the other, with a block a tile 115 and 113; 32768 rows over 64 experts of [2048, 2048] 224
+  // and 226; and the experts' layer of 2048 tokens loses by it, 435 and 418 (three sets of inputs, both in turn).
   static constexpr bool chain(bool gated) { return per_cu(gated) == 1; }
   static int describe(char* to, size_t n) { return snprintf(to, n, "tile %d x %d of %d x %d", WM, WN, FM, FN); }
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && 128 % (16 * FN) == 0, "whole loads per wave");
@@ -738,14 +742,19 @@ hipError_t launch(const F8Args& a, hipStream_t stream) {
 // times of 469 products (1 to 16384 rows on weights of 512 to 14336 rows and columns, drawn ones of 64 to 14336, up to
 // 128 experts with 1 to 32768 rows): least squares of the relative error, then the choice's loss against the best form
 // in the geometric mean, which is 1.1% (bf16 out) and 1.3% (fp32 out) and at worst 1.27 times.  Forms without which that
-// mean would be 0.6% higher at most were left out.  Both sides, us:
-//   M = 1 on [11008, 2048], fp32 out: 16 x 64 over 8 waves 7.3, 16 x 16 over 4 waves 8.6, tiles of 32 x 128 17.8
-//   M = 16 on [4096, 14336], fp32 out: 16 x 16 over 16 waves 16.5, 16 x 32 over 8 waves 20.8, 16 x 64 over 8 waves 28.7
-//   M = 32 there, bf16 out: 16 x 32 over 8 waves 20.0, 16 x 16 over 16 waves 25.2, 16 x 64 over 8 waves 26.9
-//   M = 333 on [1003, 2064], fp32 out: 32 x 32 over 8 waves 8.1, 32 x 64 over 4 waves 9.2, 16 x 64 over 8 waves 10.4
-//   M = 128 on [11008, 2048], bf16 out: 32 x 64 over 4 waves 14.5, tiles of 32 x 128 19.2, of 128 x 128 22.1
-//   M = 4096 there: tiles of 256 x 256 114.8, of 128 x 128 142.7, of 32 x 128 232.1; fp32 out 265.7, 215.4, 296.9
-//   64 x 8 rows of 128 experts [2048, 1024]: tiles of 32 x 128 52.6, 32 x 64 over 4 waves 54.9, tiles of 128 x 128 63.2
+// mean would be 0.6% higher at most were left out.  Both sides, us of the product alone, graph-replayed on the same
+// operands (what the 256 MB cache holds comes from there):
+//   M = 1 on [11008, 2048], fp32 out: 16 x 64 over 8 waves 5.0, 16 x 16 over 4 waves 6.6, tiles of 32 x 128 12.2
+//   M = 16 on [4096, 14336], fp32 out: 16 x 16 over 16 waves 11.9, 16 x 32 over 8 waves 13.8, 16 x 64 over 8 waves 18.1
+//   M = 32 there, bf16 out: 16 x 32 over 8 waves 13.4, 32 x 32 over 8 waves 16.3, 16 x 16 over 16 waves 18.0
+//   M = 333 on [1003, 2064], fp32 out: 32 x 32 over 8 waves 7.0, 32 x 64 over 4 waves 7.7, 16 x 64 over 8 waves 9.3
+//   M = 128 on [11008, 2048], bf16 out: 32 x 64 over 4 waves 10.1, tiles of 32 x 128 11.5, of 128 x 128 14.5
+//   M = 4096 there: tiles of 256 x 256 94, of 128 x 128 114, of 32 x 128 210; fp32 out: 128 x 128 196, 32 x 128 266
+//   (256 x 256, not compiled for them, was slower than 128 x 128)
+//   64 x 8 rows of 128 experts [2048, 1024], bf16 out: tiles of 32 x 128 43.3, 32 x 64 over 4 waves 48.4, tiles of 128 x
+//   128 49.6
+//   4096 x 8 rows of 64 experts [2048, 2048]: tiles of 256 x 256 211, of 128 x 128 238; fp32 out: 128 x 128 352, 32 x
+//   128 482
 struct F8Cost {
   float fixed, round, stage, mb;
 };
@@ -844,8 +853,10 @@ int fp8_form(bool y_bf16, bool grouped, int M, int K, int N, int E, int cus) {
 
 // Whether h = silu(g) u is rounded to FP8 by the product that makes g and u (whole blocks of h, an expert's weights within
 // 32 bits of offset), or written in fp32 and rounded by a kernel of its own: the least estimated time, with figures fitted
-// like the products' to 58 sizes.  By sizes alone, so that a workspace can be told from them.  Both sides, us, on 64
-// experts of [2 x 1408, 2048]: 16 tokens of 8 choices 69 fused, 62 apart; 2048 tokens 262 and 302.
+// like the products' to 58 sizes.  By sizes alone, so that a workspace can be told from them.  Both sides, us of the whole
+// layer with bf16 outputs (graph-replayed) on 64 experts of [2 x 1408, 2048]: 16 tokens of 8 choices 124 fused, 113 apart;
+// 64 tokens 136 and 122; 256 tokens 142 and 155; 2048 tokens 417 and 445 (fp32 outputs 128 and 114, 137 and 123, 156 and
+// 157, 441 and 477).
 //   g and u are summed by the bf16 instructions whatever the output: the FP8 ones' cut moves a value of h in a few
 // thousand to its neighbouring code, which is half as much again as the rounding of a bf16 output, for 199 us.
 bool fp8_gated_fused(int M, int K, int I, int E) { return fp8_gated_form(M, K, I, E, 256) >= 0; }

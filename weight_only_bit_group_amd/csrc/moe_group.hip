@@ -16,7 +16,9 @@ namespace {
 // expert find one another by a ballot for each bit of the index, so the order needs no atomics.  (The counting uses
 // LDS atomics; sums of integers do not depend on their order.)
 //   Up to kSingle choices take one workgroup and launch; more take three launches: counts of every kChunk choices,
-// their prefix sums, the placing.
+// their prefix sums, the placing.  The choices of 16 tokens, 8 each, take 4.1 us, of 512 7.0, of 2048 15.7 (64 experts)
+// in one launch; of 2049 tokens 12.6, of 4096 12.4, of 16384 (128 experts) 15, of 65536 (256) 26, of 2^20 256 in three
+// (graph-replayed; the host has two launches more).
 constexpr int kChunk = 4096;
 constexpr int64_t kSingle = 16384;
 
@@ -286,7 +288,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_quantize_kernel(const void* _
 
 // ---- the sum over a token's choices ---------------------------------------------------------
 // out[t] = sum_j weights[t, j] Y[slots[t, j]] in the order of j, fp32; a slot outside 0 .. R - 1 adds nothing (its
-// weight and row are not looked at).  Eight columns a thread; moves bytes.
+// weight and row are not looked at).  Eight columns a thread; moves bytes: 8 choices of 2048 tokens, 2048 columns of fp32
+// to bf16, 143 MB, 22 us; 4096 tokens of 4096 columns, 570 MB, 110.
 template <bool Y16, bool O16>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const void* __restrict__ Y, int64_t R, int K8,
                                                            const int32_t* __restrict__ slots, const float* __restrict__ weights,
@@ -323,7 +326,8 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const void* __restric
   }
 }
 
-// dweights[t, j] = sum_k dout[t, k] Y[slots[t, j], k] (0 for a slot outside); one wave a choice, fp32
+// dweights[t, j] = sum_k dout[t, k] Y[slots[t, j], k] (0 for a slot outside); one wave a choice, fp32.  Moves bytes: 23.5
+// and 101 us at the sizes above.
 template <bool Y16, bool O16>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(const void* __restrict__ Y, int64_t R, int K8,
                                                                     const int32_t* __restrict__ slots, int64_t C, int top,

@@ -131,3 +131,20 @@ def test_one_token_of_any_layout(route):
         want, = torch.autograd.grad(route(leaf, top)[1], leaf, d)
         got, = torch.autograd.grad(route(view, top)[1], base, d)
         assert torch.equal(got[got != 0].sort()[0], want.reshape(-1)[want.reshape(-1) != 0].sort()[0])
+
+
+def test_numbers_that_32_bits_do_not_hold(route):
+    """Groups past 2^32 are refused, not taken for what is left of them; any true value renormalises."""
+    from weight_only_bit_group_amd import binding as B
+    l = _logits()
+    step("route with numbers past 32 bits")
+    for bad in (dict(groups=2 ** 32 + 1), dict(groups=2 ** 32 + 4, top_groups=2), dict(groups=4, top_groups=2 ** 32 + 2), dict(groups=-2 ** 32 + 1),
+                dict(groups=0), dict(groups=65), dict(groups=4, top_groups=0), dict(groups=4, top_groups=5), dict(groups=4, top_groups=-2 ** 32 + 2)):
+        for call in (lambda: route(l, 3, **bad), lambda: route(l.clone().requires_grad_(), 3, **bad), lambda: B.aq_moe_route(l, 3, **bad)):
+            with pytest.raises(ValueError, match="groups"):
+                call()
+    ref = route(l, 3)
+    for yes in (1, 2 ** 32, "yes"):
+        assert torch.equal(route(l, 3, renormalize=yes)[1], ref[1])
+    d = torch.randn(9, 3, device="cuda")
+    assert torch.equal(B.aq_moe_route_backward(l, *ref, d, renormalize=2 ** 32), B.aq_moe_route_backward(l, *ref, d))

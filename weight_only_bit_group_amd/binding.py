@@ -844,10 +844,13 @@ def aq_moe_route(logits, top: int, *, score: str = "softmax", bias=None, groups:
         _mx_need(bias, "bias", torch.float32, (e,), dev)
     if not 0 < top <= min(e, 64):
         raise ValueError(f"top must be 1 .. 64 and at most E (got {top} of {e})")
+    top_groups = groups if top_groups is None else top_groups
+    if not 0 < top_groups <= groups <= 64:   # (ctypes would cut them down to 32 bits)
+        raise ValueError(f"groups must be 1 .. 64 and top_groups 1 .. groups (got {groups} and {top_groups})")
     ids = logits.new_empty((t, top), dtype=torch.int32)
     weights = logits.new_empty((t, top), dtype=torch.float32)
     _mx_call("aq_moe_route", dev, logits.data_ptr() or 16, _MX_OUT[logits.dtype], t, e, ld, top, _score(score), _ptr(bias),
-             groups, groups if top_groups is None else top_groups, int(renormalize), float(scale), ids.data_ptr() or 16,
+             groups, top_groups, int(bool(renormalize)), float(scale), ids.data_ptr() or 16,
              weights.data_ptr() or 16)
     return ids, weights
 
@@ -880,7 +883,7 @@ def aq_moe_route_backward(logits, ids, weights, dweights, *, score: str = "softm
     dlogits = torch.empty((t, e), dtype=logits.dtype, device=logits.device)
     if t:
         _mx_call("aq_moe_route_backward", dev, logits.data_ptr(), _MX_OUT[logits.dtype], t, e, ld, shape[1], _score(score),
-                 int(renormalize), float(scale), ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr())
+                 int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr())
     return dlogits
 
 

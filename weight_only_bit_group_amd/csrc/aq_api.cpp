@@ -990,7 +990,7 @@ bool experts_sizes(int64_t T, int64_t top, int64_t K, int64_t E, int64_t I) {
   // The launches' limits: the weighted sum's and, with few choices, that of the grouping beside the rounding (64 blocks
   // of 128 for 1024 threads, 16384 rows that may end in a part-filled one); the activation's where it is a launch
   return T * K <= (int64_t(1) << 35) - (int64_t(1) << 21) &&
-         (aq::fp8_gated_fused((int)(T * top), (int)K, (int)I, (int)E) || T * top * ((I + 127) / 128) <= 16 * kLaunchBlocks);
+         (T * top * ((I + 127) / 128) <= 16 * kLaunchBlocks || aq::fp8_gated_fused((int)(T * top), (int)K, (int)I, (int)E));
 }
 
 }  // namespace

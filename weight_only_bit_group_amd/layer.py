@@ -258,6 +258,8 @@ class _NoBackward(torch.autograd.Function):
 
 def _no_tangent(name: str, *tensors) -> None:
     """Raises where one of the tensors carries a forward derivative: the kernels would lose it in silence."""
+    if getattr(forward_ad, "_current_level", 0) < 0:   # (outside of forward mode: a microsecond a tensor saved)
+        return
     for t in tensors:
         if forward_ad.unpack_dual(t).tangent is not None:
             raise RuntimeError(f"{name} has no forward derivative: the tangent of its input would be lost")
@@ -430,7 +432,7 @@ class _FP8Module(torch.nn.Module):
     _held: tuple = ()   # names of the buffers
 
     def _apply(self, fn, recurse=True):
-        held = [self._buffers[name] for name in self._held]
+        held = [self._buffers.get(name) for name in self._held]
 
         def kept(t):
             if not any(t is b for b in held):
@@ -443,8 +445,8 @@ class _FP8Module(torch.nn.Module):
     def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs):
         # (copying bytes into float8 or float8 into bytes would convert the numbers that they stand for)
         for name in self._held:
-            given, have = state_dict.get(prefix + name), self._buffers[name]
-            if given is None or given.dtype == have.dtype:
+            given, have = state_dict.get(prefix + name), self._buffers.get(name)
+            if given is None or have is None or given.dtype == have.dtype:
                 continue
             if have.dtype == torch.float32:
                 given = given.float()
